@@ -230,6 +230,114 @@ rq_status rq_check_rotq_linear_args(const void *X, int32_t x_dtype, int64_t M, i
                                     const float *bias, const rq_qconfig *cfg, const void *Y,
                                     const void *workspace, size_t ws_bytes);
 
+/* ---- Keys and values in a quantized, paged cache, and attention over it -------------------
+ *
+ * The rows of attention's keys and values take the same rotation and quantizer as the linears'
+ * activations (at head_dim 128 a row's codes and scale are those of rq_rotate_quantize): blocks of
+ * B = min(128, head_dim) along the head go through the transform above (stages h = 1, 2, 4, ...,
+ * B/2 in fp32), one scale per (token, head) covers the whole head row:
+ *   a = max |u|, inv = fl(q_max / a), scale = fl(fl(a * fl(1/sqrt B)) / q_max),
+ *   code = round_half_even(fl(u * inv)); the zero-row rule above.
+ * A held row stands for x[d] = fl(fl(scale * fl(1/sqrt B)) * WHT(code)[d]).
+ *
+ * Cache: num_pages pages of rq_kv_page_bytes() each, contiguous. A page holds page_size tokens:
+ * for each head (kv_heads blocks one after the other), with Rb = head_dim * bits / 8,
+ *   K codes    [page_size][Rb]          a token's bytes together, elements as in the row-major
+ *                                       codes above (low nibble = even element)
+ *   V codes    [page_size / 4][Rb][4]   byte b of token t at ((t / 4) * Rb + b) * 4 + t % 4: four
+ *                                       tokens' bytes side by side, the order in which the second
+ *                                       product of attention takes them
+ *   K scales   float [page_size]
+ *   V scales   float [page_size]
+ * Pages are independent of each other and can be moved or shared whole. A token's place is its
+ * slot, page * page_size + (token within the page); nothing needs to be cleared: bytes of tokens
+ * that were never written are not used.
+ *
+ * Limits: bits 8 or 4; head_dim 64, 128 or 256; 1 <= kv_heads <= 65535; page_size a power of two
+ * in [16, 1024]; 1 <= num_pages < 2^31. Rows are [tokens, heads, head_dim] with the last
+ * axis contiguous and strides (in elements) that are multiples of 16 bytes, so keys and values may
+ * be slices of one projection's output. Everything said under "Conventions" holds here too. */
+typedef struct {
+  int32_t bits;        /* 8 or 4 */
+  int32_t head_dim;    /* 64, 128 or 256 */
+  int32_t kv_heads;
+  int32_t page_size;   /* tokens a page holds */
+} rq_kv_config;
+
+/* Bytes of one page, all heads (0 if cfg is invalid). A multiple of 128. */
+size_t rq_kv_page_bytes(const rq_kv_config *cfg);
+
+/* Rotate, quantize and write `tokens` keys and values into the cache.
+ *   K, V     [tokens, kv_heads, head_dim] device, dtype RQ_F32, RQ_F16 or RQ_BF16; strides in
+ *            elements (input strides may repeat rows: any value >= 0)
+ *   slots    [tokens] device: where each goes. A slot outside [0, num_pages * page_size) (-1, say,
+ *            for a padding token) is skipped. The others must differ from each other: a slot given
+ *            twice ends up with a mix of the rows given for it.
+ *   cache    in/out: num_pages * rq_kv_page_bytes(cfg) bytes; other tokens' bytes are kept */
+rq_status rq_kv_cache_write(const void *K, const void *V, int32_t dtype, int64_t tokens,
+                            int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                            int64_t v_head_stride, const int64_t *slots, const rq_kv_config *cfg,
+                            void *cache, int64_t num_pages, void *stream);
+
+/* Read `tokens` keys and values back, rotated back and rounded once to `dtype` (RQ_F32, RQ_F16 or
+ * RQ_BF16).
+ *   slots    [tokens] device; a slot outside the cache gives a row of zeros; slots may repeat
+ *   K, V     out: [tokens, kv_heads, head_dim], strides in elements; no two rows may overlap */
+rq_status rq_kv_cache_read(const void *cache, int64_t num_pages, const int64_t *slots,
+                           int64_t tokens, const rq_kv_config *cfg, void *K, void *V,
+                           int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,
+                           int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/* Attention of queries over the cache:
+ *   O[t, h] = sum_j softmax_j(softmax_scale * Q[t, h] . K_j) V_j
+ * over the cached tokens j of t's sequence that t attends to, K_j and V_j the rows that the cache
+ * holds for head h / (q_heads / kv_heads). Sequence b has the query rows q_start[b] ..
+ * q_start[b + 1] - 1 and kv_len[b] cached tokens, token j in page pages[b, j / page_size]. Its
+ * last query row is at position kv_len[b] - 1, the others before it.
+ *   causal    a query attends to the positions up to its own; a query before position 0 (more
+ *             query rows than cached tokens) attends to nothing
+ *   window    with causal: only to the last `window` of those (its own among them); 0: all
+ * A row that attends to nothing gets O = 0 and lse = -inf. Rows of Q before q_start[0] or from
+ * q_start[seqs] on are not read, and their O and lse are left as they were.
+ * What the device tables hold is not trusted with memory: query rows outside [0, total_q) do not
+ * exist, kv_len is cut to [0, max_pages * page_size], and the tokens of a page index outside
+ * [0, num_pages) count as not there.
+ * Arithmetic: R q rounded to fp16 (fp16 queries: to two fp16, leading and remainder) after a power
+ * of two a row, codes exact, products and sums in fp32, the weights p_j * scale_j rounded to fp16
+ * after a power of two, statistics and the sums of p_j in fp32. Results do not depend on
+ * what else is in the batch beyond the way the keys are split (max_q_len, max_kv_len, seqs);
+ * calls with equal arguments give equal bits. */
+typedef struct {
+  const void *Q;             /* [total_q, q_heads, head_dim] device */
+  void *O;                   /* out: the same shape and dtype; must not overlap an input */
+  float *lse;                /* out: [total_q, q_heads], natural logarithm of each row's sum of
+                                exponentials; NULL: not written */
+  const int32_t *q_start;    /* [seqs + 1] device, not decreasing; NULL: every sequence has
+                                total_q / seqs rows (total_q must be a multiple of seqs) */
+  const int32_t *kv_len;     /* [seqs] device */
+  const int32_t *pages;      /* [seqs, max_pages] device */
+  int64_t total_q;
+  int64_t q_token_stride, q_head_stride, o_token_stride, o_head_stride;   /* elements */
+  int64_t max_q_len;         /* the most query rows of a sequence, the most cached tokens of one: */
+  int64_t max_kv_len;        /*   they choose how the work is split; results hold for other lengths
+                                too. 0 or less: total_q, max_pages * page_size. */
+  int32_t dtype;             /* RQ_F16 or RQ_BF16: of Q and O */
+  int32_t q_heads;           /* a multiple of kv_heads */
+  int32_t seqs, max_pages;   /* seqs <= 65535; max_pages * page_size <= 2^30 */
+  int32_t causal, window;
+  float softmax_scale;       /* finite and > 0 */
+} rq_kv_attention_params;
+
+/* Bytes of device workspace the call needs (0: none, or invalid arguments). */
+size_t rq_kv_attention_workspace_size(const rq_kv_attention_params *p, const rq_kv_config *cfg);
+
+/*   workspace  ws_bytes >= rq_kv_attention_workspace_size() bytes, or NULL if that is 0; nothing
+ *              in it needs to start at zero, nothing is kept in it between calls. Limit:
+ *              total_q * q_heads <= 2^30. */
+rq_status rq_kv_attention(const rq_kv_attention_params *p, const rq_kv_config *cfg,
+                          const void *cache, int64_t num_pages, void *workspace, size_t ws_bytes,
+                          void *stream);
+
 /* Static text for a status code. */
 const char *rq_status_string(rq_status s);
 

@@ -7,7 +7,7 @@ the library is missing or a call fails, a ConvRotError is raised.
 Two layers:
   * ``rq_*`` -- the C entry points under their own names, taking integer device pointers;
   * ``quantize_weights``, ``rotq_linear``, ``rotate_quantize``, ``gemm_dequant``,
-    ``gemm_s32`` -- tensor wrappers that allocate outputs with torch and pass the current
+    ``gemm_s32``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
     stream.
 """
 from __future__ import annotations
@@ -40,6 +40,19 @@ class rq_qconfig(ctypes.Structure):
                 ("act", ctypes.c_int32)]
 
 
+class rq_kv_config(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class rq_kv_attention_params(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("Q", "O", "lse", "q_start", "kv_len", "pages")]
+                + [(n, ctypes.c_int64) for n in ("total_q", "q_token_stride", "q_head_stride", "o_token_stride",
+                                                 "o_head_stride", "max_q_len", "max_kv_len")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "q_heads", "seqs", "max_pages", "causal", "window")]
+                + [("softmax_scale", ctypes.c_float)])
+
+
 _lib = None
 
 
@@ -59,6 +72,7 @@ def load():
     lib = ctypes.CDLL(_LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     CFG = ctypes.POINTER(rq_qconfig)
+    KV, ATT = ctypes.POINTER(rq_kv_config), ctypes.POINTER(rq_kv_attention_params)
     sig = {
         "rq_quantize_weights": [P, I32, I64, I64, CFG, P, P, P],
         "rq_rotate_quantize": [P, I32, I64, I64, CFG, P, P, P],
@@ -67,6 +81,9 @@ def load():
         "rq_gemm_dequant": [P, P, P, P, P, I64, I64, I64, CFG, P, I32, P],
         "rq_gemm_s32": [P, P, I64, I64, I64, CFG, P, P],
         "rq_check_rotq_linear_args": [P, I32, I64, I64, P, P, I64, P, CFG, P, P, SZ],
+        "rq_kv_cache_write": [P, P, I32, I64, I64, I64, I64, I64, P, KV, P, I64, P],
+        "rq_kv_cache_read": [P, I64, P, I64, KV, P, P, I32, I64, I64, I64, I64, P],
+        "rq_kv_attention": [ATT, KV, P, I64, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -78,6 +95,10 @@ def load():
     lib.rq_codes_bytes.restype = SZ
     lib.rq_weight_bytes.argtypes = [I64, I64, CFG]
     lib.rq_weight_bytes.restype = SZ
+    lib.rq_kv_page_bytes.argtypes = [KV]
+    lib.rq_kv_page_bytes.restype = SZ
+    lib.rq_kv_attention_workspace_size.argtypes = [ATT, KV]
+    lib.rq_kv_attention_workspace_size.restype = SZ
     lib.rq_status_string.argtypes = [ctypes.c_int]
     lib.rq_status_string.restype = ctypes.c_char_p
     lib.rq_last_error_detail.argtypes = []
@@ -151,6 +172,30 @@ def rq_weight_bytes(N, K, cfg) -> int:
 def rq_check_rotq_linear_args(X, x_dtype, M, K, Wq, w_scale, N, bias, cfg, Y, ws, ws_bytes) -> int:
     return load().rq_check_rotq_linear_args(X, x_dtype, M, K, Wq, w_scale, N, bias,
                                             ctypes.byref(cfg), Y, ws, ws_bytes)
+
+
+def rq_kv_page_bytes(cfg) -> int:
+    return load().rq_kv_page_bytes(ctypes.byref(cfg))
+
+
+def rq_kv_cache_write(K, V, dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, cfg,
+                      cache, num_pages, stream) -> int:
+    return load().rq_kv_cache_write(K, V, dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                                    slots, ctypes.byref(cfg), cache, num_pages, stream)
+
+
+def rq_kv_cache_read(cache, num_pages, slots, tokens, cfg, K, V, dtype, k_token_stride, k_head_stride, v_token_stride,
+                     v_head_stride, stream) -> int:
+    return load().rq_kv_cache_read(cache, num_pages, slots, tokens, ctypes.byref(cfg), K, V, dtype, k_token_stride,
+                                   k_head_stride, v_token_stride, v_head_stride, stream)
+
+
+def rq_kv_attention_workspace_size(params, cfg) -> int:
+    return load().rq_kv_attention_workspace_size(ctypes.byref(params), ctypes.byref(cfg))
+
+
+def rq_kv_attention(params, cfg, cache, num_pages, workspace, ws_bytes, stream) -> int:
+    return load().rq_kv_attention(ctypes.byref(params), ctypes.byref(cfg), cache, num_pages, workspace, ws_bytes, stream)
 
 
 def rq_status_string(s: int) -> str:
@@ -364,3 +409,184 @@ def gemm_s32(Xq, Wq, bits: int = 8, K: Optional[int] = None, stream=None,
     _check(rq_gemm_s32(_dev(Xq, "Xq"), _dev(Wq, "Wq"), M, N, K, cfg, acc.data_ptr(), _stream(stream)),
            "rq_gemm_s32")
     return acc
+
+
+# ------------------------------------------------------------------- the cache and attention over it
+def make_kv_cfg(kv_heads: int, head_dim: int, page_size: int = 64, bits: int = 4) -> rq_kv_config:
+    return rq_kv_config(bits, head_dim, kv_heads, page_size)
+
+
+class _Placed:
+    """Makes `device` current, and `stream` where one is given, for allocations and the launch;
+    `handle` is the stream's."""
+
+    def __init__(self, device, stream):
+        cuda = _torch().cuda
+        if stream is not None and stream.device != device:
+            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+        self._device = None if device.index == cuda.current_device() else cuda.device(device)
+        self._stream = None if stream is None else cuda.stream(stream)
+        self._given, self._at = stream, device
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        s = self._given if self._given is not None else _torch().cuda.current_stream(self._at)
+        self.handle = s.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def _kv_cache(cache, cfg):
+    """The number of pages of a uint8 cache [pages, rq_kv_page_bytes(cfg)]."""
+    page = rq_kv_page_bytes(cfg)
+    if page == 0:
+        raise ConvRotError(RQ_EUNSUPPORTED, "rq_kv_page_bytes", load().rq_last_error_detail().decode())
+    if cache.dtype != _torch().uint8 or cache.dim() != 2 or cache.shape[1] != page or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor [pages, %d], got %s %s"
+                         % (page, cache.dtype, tuple(cache.shape)))
+    return cache.shape[0]
+
+
+def _kv_rows(t, name, heads, dim, dtypes, tokens=None):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError("%s must be [%s, %d, %d], got %s" % (name, "tokens" if tokens is None else tokens, heads, dim,
+                                                              tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s dtype %s (expected one of %s)" % (name, t.dtype, ", ".join(map(str, dtypes))))
+    if t.stride(2) != 1:
+        raise ValueError("%s must be contiguous along its last axis" % name)
+    return t.stride(0), t.stride(1)
+
+
+def _kv_table(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s %s" % (name, dtype, shape, t.dtype,
+                                                                                     tuple(t.shape)))
+
+
+def _on_gpu(device):
+    if device.type != "cuda":
+        raise ValueError("tensors must be device tensors, got %s" % device)
+
+
+def kv_cache_alloc(num_pages: int, cfg: rq_kv_config, device="cuda"):
+    """A cache of num_pages pages: uint8 [num_pages, rq_kv_page_bytes(cfg)], uninitialised (no byte
+    is used before it is written)."""
+    page = rq_kv_page_bytes(cfg)
+    if page == 0:
+        raise ConvRotError(RQ_EUNSUPPORTED, "rq_kv_page_bytes", load().rq_last_error_detail().decode())
+    return _torch().empty((num_pages, page), dtype=_torch().uint8, device=device)
+
+
+def kv_cache_write(K, V, slots, cache, cfg: rq_kv_config, stream=None):
+    """Rotate, quantise and write keys and values [tokens, kv_heads, head_dim] (f32/f16/bf16, any
+    strides of 16 bytes' multiples, last axis contiguous) at slots [tokens] (int64, on the device)
+    of `cache`, in place. A slot outside the cache (-1) skips its token; the others must differ."""
+    torch = _torch()
+    pages = _kv_cache(cache, cfg)
+    types = (torch.float32, torch.float16, torch.bfloat16)
+    kt, kh = _kv_rows(K, "K", cfg.kv_heads, cfg.head_dim, types)
+    vt, vh = _kv_rows(V, "V", cfg.kv_heads, cfg.head_dim, (K.dtype,), K.shape[0])
+    _kv_table(slots, "slots", torch.int64, (K.shape[0],))
+    _same_device(K, V, slots, cache)
+    _on_gpu(cache.device)
+    with _Placed(cache.device, stream) as at:
+        _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), _dtype_code(K), K.shape[0], kt, kh, vt, vh, slots.data_ptr(),
+                                 cfg, cache.data_ptr(), pages, at.handle), "rq_kv_cache_write")
+
+
+def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, stream=None):
+    """(K, V) [tokens, kv_heads, head_dim] that `cache` holds at slots [tokens] (int64, on the
+    device), in out_dtype (default bfloat16) or into the pair `out`. A slot outside the cache gives
+    zeros."""
+    torch = _torch()
+    pages = _kv_cache(cache, cfg)
+    if slots.dim() != 1:
+        raise ValueError("slots must be a vector, got shape %s" % (tuple(slots.shape),))
+    tokens = slots.shape[0]
+    _kv_table(slots, "slots", torch.int64, (tokens,))
+    types = (torch.float32, torch.float16, torch.bfloat16)
+    if out is not None:
+        if out_dtype is not None and out[0].dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype is %s" % (out[0].dtype, out_dtype))
+        _same_device(cache, slots, *out)
+    else:
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        if out_dtype not in types:
+            raise ValueError("out_dtype must be float32, float16 or bfloat16")
+        _same_device(cache, slots)
+    _on_gpu(cache.device)
+    with _Placed(cache.device, stream) as at:
+        if out is None:
+            shape = (tokens, cfg.kv_heads, cfg.head_dim)
+            out = (torch.empty(shape, dtype=out_dtype, device=cache.device),
+                   torch.empty(shape, dtype=out_dtype, device=cache.device))
+        K, V = out
+        kt, kh = _kv_rows(K, "K", cfg.kv_heads, cfg.head_dim, types, tokens)
+        vt, vh = _kv_rows(V, "V", cfg.kv_heads, cfg.head_dim, (K.dtype,), tokens)
+        _check(rq_kv_cache_read(cache.data_ptr(), pages, slots.data_ptr(), tokens, cfg, K.data_ptr(), V.data_ptr(),
+                                _dtype_code(K), kt, kh, vt, vh, at.handle), "rq_kv_cache_read")
+    return K, V
+
+
+def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causal: bool = True, window: int = 0,
+                 softmax_scale: Optional[float] = None, max_q_len: int = 0, max_kv_len: int = 0,
+                 return_lse: bool = False, out=None, workspace=None, stream=None):
+    """Attention of Q [total_q, q_heads, head_dim] (f16/bf16) over `cache`: O in Q's shape and
+    dtype, and with return_lse also the rows' logarithms of sums [total_q, q_heads] (f32).
+
+    pages [seqs, max_pages], kv_len [seqs] and q_start [seqs + 1] are int32 device tensors; without
+    q_start every sequence has total_q / seqs query rows. softmax_scale defaults to
+    head_dim ** -0.5. max_q_len and max_kv_len (host numbers) choose how the work is split; they
+    default to what the shapes allow, and results hold for other lengths too. workspace: a uint8
+    tensor of kv_attention_workspace_size() bytes or more. See rq_kv_attention in convrot.h."""
+    torch = _torch()
+    num_pages = _kv_cache(cache, cfg)
+    if Q.dim() != 3:
+        raise ValueError("Q must be [total_q, q_heads, head_dim], got %s" % (tuple(Q.shape),))
+    total, q_heads, dim = Q.shape
+    qt, qh = _kv_rows(Q, "Q", q_heads, cfg.head_dim, (torch.float16, torch.bfloat16))
+    if pages.dim() != 2:
+        raise ValueError("pages must be [seqs, max_pages], got %s" % (tuple(pages.shape),))
+    seqs, max_pages = pages.shape
+    _kv_table(pages, "pages", torch.int32, (seqs, max_pages))
+    _kv_table(kv_len, "kv_len", torch.int32, (seqs,))
+    if q_start is not None:
+        _kv_table(q_start, "q_start", torch.int32, (seqs + 1,))
+    _same_device(Q, cache, pages, kv_len, q_start, out, workspace)
+    _on_gpu(Q.device)
+    with _Placed(Q.device, stream) as at:
+        if out is None:
+            out = torch.empty((total, q_heads, dim), dtype=Q.dtype, device=Q.device)
+        ot, oh = _kv_rows(out, "out", q_heads, dim, (Q.dtype,), total)
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=Q.device) if return_lse else None
+        p = rq_kv_attention_params(
+            Q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
+            max_q_len, max_kv_len, _dtype_code(Q), q_heads, seqs, max_pages, int(causal), window,
+            dim ** -0.5 if softmax_scale is None else softmax_scale)
+        need = rq_kv_attention_workspace_size(p, cfg)
+        if workspace is not None:
+            _check_bytes(workspace, "workspace", need, exact=False)
+        elif need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
+        _check(rq_kv_attention(p, cfg, cache.data_ptr(), num_pages, None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else _nbytes(workspace), at.handle), "rq_kv_attention")
+    return (out, lse) if return_lse else out
+
+
+def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages: int, cfg: rq_kv_config,
+                                max_q_len: int = 0, max_kv_len: int = 0, window: int = 0, ragged: bool = False) -> int:
+    """Bytes of workspace a kv_attention call of these sizes needs (0: none). ragged: the call
+    passes q_start."""
+    p = rq_kv_attention_params(None, None, None, 4 if ragged else None, None, None, total_q, 0, 0, 0, 0, max_q_len,
+                               max_kv_len, RQ_BF16, q_heads, seqs, max_pages, 1, window, 1.0)
+    return rq_kv_attention_workspace_size(p, cfg)

@@ -266,6 +266,185 @@ rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const
   return ok();
 }
 
+// ---- the cache operators
+constexpr int64_t kMaxKvTokens = int64_t(1) << 30;   // of a sequence's page table
+constexpr int64_t kMaxKvRows = int64_t(1) << 30;     // query rows times heads
+
+int log2_of(int32_t n) {
+  int l = 0;
+  while ((1 << l) < n) l++;
+  return l;
+}
+
+rq_status check_kv_cfg(const rq_kv_config* cfg) {
+  if (!cfg) return fail(RQ_EINVAL, "cfg is NULL");
+  if (cfg->bits != 8 && cfg->bits != 4) return fail(RQ_EUNSUPPORTED, "bits = %d (supported: 8, 4)", cfg->bits);
+  if (cfg->head_dim != 64 && cfg->head_dim != 128 && cfg->head_dim != 256)
+    return fail(RQ_EUNSUPPORTED, "head_dim = %d (supported: 64, 128, 256)", cfg->head_dim);
+  if (cfg->kv_heads < 1 || cfg->kv_heads > 65535)
+    return fail(RQ_EUNSUPPORTED, "kv_heads = %d (supported: 1 .. 65535)", cfg->kv_heads);
+  const int32_t ps = cfg->page_size;
+  if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0)
+    return fail(RQ_EUNSUPPORTED, "page_size = %d (supported: powers of two in 16 .. 1024)", ps);
+  return ok();
+}
+
+int64_t kv_head_bytes(const rq_kv_config* cfg) {
+  return (int64_t)cfg->page_size * (2 * (cfg->head_dim * cfg->bits / 8) + 8);
+}
+
+rq_status check_kv_cache(const void* cache, int64_t num_pages) {
+  rq_status s = check_ptr(cache, "cache");
+  if (s) return s;
+  if (num_pages < 1 || num_pages > kMaxRowsOrCols)
+    return fail(num_pages < 1 ? RQ_EINVAL : RQ_EUNSUPPORTED, "num_pages = %lld (need 1 .. 2^31 - 1)", (long long)num_pages);
+  return ok();
+}
+
+// Rows [tokens, heads, dim] at p with strides in elements of `es` bytes; returns their extent in
+// bytes. Output rows must not overlap one another.
+rq_status check_kv_rows(const void* p, const char* name, int64_t tokens, int64_t heads, int64_t dim, int64_t es,
+                        int64_t token_stride, int64_t head_stride, bool out, int64_t* bytes) {
+  rq_status s = check_ptr(p, name);
+  if (s) return s;
+  constexpr int64_t kMost = int64_t(1) << 40;
+  if (token_stride < 0 || head_stride < 0 || token_stride > kMost || head_stride > kMost)
+    return fail(RQ_EINVAL, "%s strides (%lld, %lld) out of range", name, (long long)token_stride, (long long)head_stride);
+  if (token_stride * es % 16 != 0 || head_stride * es % 16 != 0)
+    return fail(RQ_EINVAL, "%s strides (%lld, %lld) are not multiples of 16 bytes", name, (long long)token_stride,
+                (long long)head_stride);
+  if (out) {
+    // Heads within a token, or tokens within a head: one lies inside the other's stride. In
+    // 128 bits: 2^31 rows at strides up to 2^40 elements pass 64.
+    typedef __int128 wide;
+    const wide over_heads = (wide)(heads - 1) * head_stride + dim, over_tokens = (wide)(tokens - 1) * token_stride + dim;
+    const bool h_in_t = (heads == 1 || head_stride >= dim) && (tokens == 1 || token_stride >= over_heads);
+    const bool t_in_h = (tokens == 1 || token_stride >= dim) && (heads == 1 || head_stride >= over_tokens);
+    if (!h_in_t && !t_in_h)
+      return fail(RQ_EINVAL, "%s strides (%lld, %lld): rows overlap", name, (long long)token_stride, (long long)head_stride);
+  }
+  const __int128 extent = ((__int128)(tokens - 1) * token_stride + (__int128)(heads - 1) * head_stride + dim) * es;
+  if (extent > (__int128)1 << 46) return fail(RQ_EUNSUPPORTED, "%s spans over 2^46 bytes", name);
+  *bytes = (int64_t)extent;
+  return ok();
+}
+
+rq_status check_kv_rw(const void* K, const void* V, int32_t dtype, int64_t tokens, int64_t k_token, int64_t k_head,
+                      int64_t v_token, int64_t v_head, const int64_t* slots, const rq_kv_config* cfg, const void* cache,
+                      int64_t num_pages, bool out) {
+  rq_status s = check_kv_cfg(cfg);
+  if (s) return s;
+  if (dtype != RQ_F32 && dtype != RQ_F16 && dtype != RQ_BF16) return fail(RQ_EINVAL, "bad K / V dtype %d", dtype);
+  if (tokens < 0) return fail(RQ_EINVAL, "tokens = %lld < 0", (long long)tokens);
+  if (tokens > kMaxRowsOrCols) return fail(RQ_EUNSUPPORTED, "tokens = %lld >= 2^31", (long long)tokens);
+  if ((s = check_kv_cache(cache, num_pages))) return s;
+  if (tokens == 0) return ok();
+  const int64_t es = elem_size(dtype);
+  int64_t kb = 0, vb = 0;
+  if ((s = check_kv_rows(K, "K", tokens, cfg->kv_heads, cfg->head_dim, es, k_token, k_head, out, &kb))) return s;
+  if ((s = check_kv_rows(V, "V", tokens, cfg->kv_heads, cfg->head_dim, es, v_token, v_head, out, &vb))) return s;
+  if (!slots) return fail(RQ_EINVAL, "slots is NULL");
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return fail(RQ_EINVAL, "slots is not 8-byte aligned");
+  const int64_t cb = num_pages * kv_head_bytes(cfg) * cfg->kv_heads;
+  if (overlap(cache, cb, K, kb) || overlap(cache, cb, V, vb) || overlap(cache, cb, slots, tokens * 8))
+    return fail(RQ_EINVAL, "the cache overlaps K, V or slots");
+  if (out && (overlap(K, kb, slots, tokens * 8) || overlap(V, vb, slots, tokens * 8)))
+    return fail(RQ_EINVAL, "K or V overlaps slots");
+  // Interleaved K and V (slices of one buffer) share an extent: only the same start is refused.
+  if (out && K == V) return fail(RQ_EINVAL, "K and V are the same buffer");
+  return ok();
+}
+
+convrot::KvCacheArgs kv_cache_args(int32_t dtype, int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token,
+                                   int64_t v_head, const int64_t* slots, const rq_kv_config* cfg, const void* cache,
+                                   int64_t num_pages) {
+  convrot::KvCacheArgs a = {};
+  a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  a.slots = slots;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.tokens = tokens;
+  a.num_pages = num_pages;
+  a.head_bytes = kv_head_bytes(cfg);
+  a.heads = cfg->kv_heads;
+  a.lps = log2_of(cfg->page_size);
+  a.dt = dtype;
+  return a;
+}
+
+// Everything the sizes of an attention call are taken from; the lengths that choose the split.
+rq_status check_kv_shape(const rq_kv_attention_params* p, const rq_kv_config* cfg, int64_t* max_q, int64_t* max_kv) {
+  rq_status s = check_kv_cfg(cfg);
+  if (s) return s;
+  if (!p) return fail(RQ_EINVAL, "params is NULL");
+  if (p->dtype != RQ_F16 && p->dtype != RQ_BF16)
+    return fail(p->dtype == RQ_F32 ? RQ_EUNSUPPORTED : RQ_EINVAL, "Q dtype %d (supported: RQ_F16, RQ_BF16)", p->dtype);
+  if (p->seqs < 0 || p->total_q < 0 || p->max_pages < 0 || p->window < 0)
+    return fail(RQ_EINVAL, "seqs = %d, total_q = %lld, max_pages = %d, window = %d: none may be negative", p->seqs,
+                (long long)p->total_q, p->max_pages, p->window);
+  if (p->seqs > 65535) return fail(RQ_EUNSUPPORTED, "seqs = %d > 65535", p->seqs);
+  if (p->q_heads < 1 || p->q_heads % cfg->kv_heads != 0)
+    return fail(RQ_EINVAL, "q_heads = %d is not a positive multiple of kv_heads = %d", p->q_heads, cfg->kv_heads);
+  if (p->total_q > kMaxKvRows || p->total_q * p->q_heads > kMaxKvRows)
+    return fail(RQ_EUNSUPPORTED, "total_q * q_heads = %lld * %d > 2^30", (long long)p->total_q, p->q_heads);
+  if ((int64_t)p->max_pages * cfg->page_size > kMaxKvTokens)
+    return fail(RQ_EUNSUPPORTED, "max_pages * page_size = %d * %d > 2^30", p->max_pages, cfg->page_size);
+  if (p->window > 0 && !p->causal) return fail(RQ_EINVAL, "window needs causal");
+  if (!(p->softmax_scale > 0.0f) || p->softmax_scale > 3.4028234e38f)
+    return fail(RQ_EINVAL, "softmax_scale = %g (need a finite value > 0)", (double)p->softmax_scale);
+  if (p->total_q > 0 && p->seqs == 0) return fail(RQ_EINVAL, "seqs = 0 with total_q = %lld", (long long)p->total_q);
+  if (!p->q_start && p->seqs > 0 && p->total_q % p->seqs != 0)
+    return fail(RQ_EINVAL, "total_q = %lld is not a multiple of seqs = %d, and q_start is NULL", (long long)p->total_q, p->seqs);
+  const int64_t kv = (int64_t)p->max_pages * cfg->page_size;
+  *max_q = p->max_q_len < 1 || p->max_q_len > p->total_q ? p->total_q : p->max_q_len;
+  if (!p->q_start && p->seqs > 0) *max_q = p->total_q / p->seqs;
+  *max_kv = p->max_kv_len < 1 || p->max_kv_len > kv ? kv : p->max_kv_len;
+  return ok();
+}
+
+rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache,
+                             int64_t num_pages, const void* ws, size_t ws_bytes, convrot::KvAttentionPlan* plan) {
+  int64_t max_q = 0, max_kv = 0;
+  rq_status s = check_kv_shape(p, cfg, &max_q, &max_kv);
+  if (s) return s;
+  if ((s = check_kv_cache(cache, num_pages))) return s;
+  if (p->total_q == 0) return ok();
+  int64_t qb = 0, ob = 0;
+  if ((s = check_kv_rows(p->Q, "Q", p->total_q, p->q_heads, cfg->head_dim, 2, p->q_token_stride, p->q_head_stride, false, &qb)))
+    return s;
+  if ((s = check_kv_rows(p->O, "O", p->total_q, p->q_heads, cfg->head_dim, 2, p->o_token_stride, p->o_head_stride, true, &ob)))
+    return s;
+  if (!p->kv_len || (!p->pages && p->max_pages > 0)) return fail(RQ_EINVAL, "kv_len or pages is NULL");
+  const void* words[4] = {p->kv_len, p->pages, p->q_start, p->lse};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
+      return fail(RQ_EINVAL, "kv_len, pages, q_start or lse is not 4-byte aligned");
+  *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
+                                     p->window);
+  const int64_t need = (int64_t)plan->workspace_bytes;
+  if (need > 0) {
+    if (ws_bytes < plan->workspace_bytes)
+      return fail(RQ_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, plan->workspace_bytes);
+    if ((s = check_ptr(ws, "workspace"))) return s;
+  }
+  const struct { const void* at; int64_t bytes; } outs[3] = {{p->O, ob}, {p->lse, p->total_q * p->q_heads * 4}, {ws, need}},
+                                                 ins[5] = {{p->Q, qb},
+                                                           {cache, num_pages * kv_head_bytes(cfg) * cfg->kv_heads},
+                                                           {p->kv_len, (int64_t)p->seqs * 4},
+                                                           {p->q_start, (int64_t)(p->seqs + 1) * 4},
+                                                           {p->pages, (int64_t)p->seqs * p->max_pages * 4}};
+  for (int i = 0; i < 3; i++) {
+    for (const auto& in : ins)
+      if (overlap(outs[i].at, outs[i].bytes, in.at, in.bytes)) return fail(RQ_EINVAL, "O, lse or the workspace overlaps an input");
+    for (int j = 0; j < i; j++)
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes))
+        return fail(RQ_EINVAL, "O, lse and the workspace must not overlap");
+  }
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -394,6 +573,85 @@ rq_status rq_gemm_s32(const void* Xq, const void* Wq, int64_t M, int64_t N, int6
                                        cfg->x_layout == RQ_X_TILED, acc, RQ_F16, acc, RQ_ACT_NONE,
                                        static_cast<hipStream_t>(stream)),
                   "gemm launch");
+}
+
+size_t rq_kv_page_bytes(const rq_kv_config* cfg) {
+  if (check_kv_cfg(cfg) != RQ_OK) return 0;
+  return (size_t)(kv_head_bytes(cfg) * cfg->kv_heads);
+}
+
+rq_status rq_kv_cache_write(const void* K, const void* V, int32_t dtype, int64_t tokens, int64_t k_token_stride,
+                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                            const rq_kv_config* cfg, void* cache, int64_t num_pages, void* stream) {
+  rq_status s = check_kv_rw(K, V, dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, cfg,
+                            cache, num_pages, false);
+  if (s || tokens == 0) return s;
+  convrot::KvCacheArgs a = kv_cache_args(dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots,
+                                         cfg, cache, num_pages);
+  a.k = static_cast<const uint8_t*>(K);
+  a.v = static_cast<const uint8_t*>(V);
+  return from_hip(convrot::launch_kv_cache(a, cfg->head_dim, cfg->bits, true, static_cast<hipStream_t>(stream)),
+                  "kv_write launch");
+}
+
+rq_status rq_kv_cache_read(const void* cache, int64_t num_pages, const int64_t* slots, int64_t tokens,
+                           const rq_kv_config* cfg, void* K, void* V, int32_t dtype, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, void* stream) {
+  rq_status s = check_kv_rw(K, V, dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, cfg,
+                            cache, num_pages, true);
+  if (s || tokens == 0) return s;
+  convrot::KvCacheArgs a = kv_cache_args(dtype, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots,
+                                         cfg, cache, num_pages);
+  a.k_out = static_cast<uint8_t*>(K);
+  a.v_out = static_cast<uint8_t*>(V);
+  return from_hip(convrot::launch_kv_cache(a, cfg->head_dim, cfg->bits, false, static_cast<hipStream_t>(stream)),
+                  "kv_read launch");
+}
+
+size_t rq_kv_attention_workspace_size(const rq_kv_attention_params* p, const rq_kv_config* cfg) {
+  int64_t max_q = 0, max_kv = 0;
+  if (check_kv_shape(p, cfg, &max_q, &max_kv) != RQ_OK || p->total_q == 0) return 0;
+  return convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
+                                    p->window)
+      .workspace_bytes;
+}
+
+rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache, int64_t num_pages,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  convrot::KvAttentionPlan plan = {};
+  rq_status s = check_kv_attention(p, cfg, cache, num_pages, workspace, ws_bytes, &plan);
+  if (s || p->total_q == 0) return s;
+  convrot::KvAttentionArgs a = {};
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.q = static_cast<const uint8_t*>(p->Q);
+  a.out = static_cast<uint8_t*>(p->O);
+  a.lse = p->lse;
+  a.q_start = p->q_start;
+  a.kv_len = p->kv_len;
+  a.pages = p->pages;
+  a.part_out = static_cast<float*>(workspace);
+  if (plan.splits > 1) a.part_stat = a.part_out + p->total_q * p->q_heads * plan.splits * cfg->head_dim;
+  a.q_token = p->q_token_stride;
+  a.q_head = p->q_head_stride;
+  a.out_token = p->o_token_stride;
+  a.out_head = p->o_head_stride;
+  a.total_q = p->total_q;
+  a.num_pages = num_pages;
+  a.head_bytes = kv_head_bytes(cfg);
+  a.seqs = p->seqs;
+  a.q_heads = p->q_heads;
+  a.heads = cfg->kv_heads;
+  a.group = p->q_heads / cfg->kv_heads;
+  a.max_pages = p->max_pages;
+  a.lps = log2_of(cfg->page_size);
+  a.dt = p->dtype;
+  a.causal = p->causal;
+  a.window = p->window;
+  a.splits = plan.splits;
+  a.row_tiles = plan.row_tiles;
+  a.scale = p->softmax_scale;
+  return from_hip(convrot::launch_kv_attention(a, cfg->head_dim, cfg->bits, static_cast<hipStream_t>(stream)),
+                  "kv_attention launch");
 }
 
 }  // extern "C"

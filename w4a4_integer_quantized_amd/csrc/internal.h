@@ -57,4 +57,40 @@ hipError_t launch_gemm_wide(const void* Xq, const float* sx, const void* Wq, con
                             const float* bias, int64_t M, int64_t N, int64_t K, int bits,
                             void* Y, int out_dt, int32_t* acc32, hipStream_t stream);
 
+// The cache operators (layout and arithmetic in convrot.h). Strides in elements; pre-validated.
+struct KvCacheArgs {
+  uint8_t* cache;
+  const int64_t* slots;                       // [tokens]
+  const uint8_t *k, *v;                       // write: rows in
+  uint8_t *k_out, *v_out;                     // read: rows out
+  int64_t k_token, k_head, v_token, v_head;   // strides of the rows
+  int64_t tokens, num_pages, head_bytes;      // head_bytes: one head's block of a page
+  int heads, lps, dt;                         // lps: log2 of the page size; dt: the rows' type
+};
+hipError_t launch_kv_cache(const KvCacheArgs& a, int head_dim, int bits, bool write, hipStream_t stream);
+
+struct KvAttentionArgs {
+  const uint8_t* cache;
+  const uint8_t* q;
+  uint8_t* out;
+  float* lse;                 // [total_q, q_heads] or null
+  const int32_t* q_start;     // [seqs + 1], or null: every sequence has total_q / seqs rows
+  const int32_t* kv_len;      // [seqs]
+  const int32_t* pages;       // [seqs, max_pages]
+  float* part_out;            // [total_q, q_heads, splits, head_dim] when splits > 1
+  float* part_stat;           // [total_q, q_heads, splits, 2]
+  int64_t q_token, q_head, out_token, out_head;
+  int64_t total_q, num_pages, head_bytes;
+  int seqs, q_heads, heads, group, max_pages, lps, dt, causal, window, splits, row_tiles;
+  float scale;
+};
+// How a call is split: see kv_attention.hip.
+struct KvAttentionPlan {
+  int splits, row_tiles;
+  size_t workspace_bytes;
+};
+KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int bits,
+                                  int64_t max_q_len, int64_t max_kv_len, int window);
+hipError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, int bits, hipStream_t stream);
+
 }  // namespace convrot

@@ -1,0 +1,589 @@
+// kv_attention.hip -- attention over a cache of rotated 8- or 4-bit keys and values
+// (rq_kv_attention; layout and definition in convrot.h).
+//
+// Mathematics. With R the normalized block rotation, a held key is R^T (s_k c_k) for its codes
+// c_k, so q . k = s_k (R q) . c_k: the query is rotated once and the keys are used as codes. The
+// output sum_j p_j v_j = R^T (sum_j (p_j s_v,j) c_v,j) is rotated back once. Codes are integers of
+// at most 7 bits and a sign, exact in fp16, so both products run on fp16 matrix instructions with
+// fp32 sums. Two roundings remain: of R q to fp16 (scaled by a power of two a row so that its
+// largest element lies in [256, 512); for fp16 queries a second fp16 holds what the first leaves),
+// and of the weights p_j s_v,j to fp16 (scaled by a power of two that keeps them below 2^15, so
+// 28 binades below the largest stay normal). Softmax statistics are fp32, in base 2.
+#include "kv_common.h"
+
+namespace convrot {
+namespace {
+
+using namespace kv;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kTile = 64;          // keys a wave takes at a time
+constexpr int kWaves = 4;
+constexpr int kRows = 16;          // query rows of a tile: (token, head of the group) pairs
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// Maximum / sum over the four lanes that hold the same query row (lane xor 16, 32).
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+__device__ __forceinline__ uint32_t add_h2(uint32_t a, float off) {
+  const f16x2 d = {static_cast<_Float16>(off), static_cast<_Float16>(off)};
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) + d);
+}
+
+// 4-bit codes of a dword as fp16: nibbles (0, 4), (1, 5), (2, 6), (3, 7). The nibble with its
+// sign bit flipped, c + 8, goes into the mantissa of 1024 (low nibbles) or of 64 (high ones).
+__device__ __forceinline__ void nibbles_f16(uint32_t x, uint32_t (&h)[4]) {
+  h[0] = add_h2((x & 0x000F000Fu) ^ 0x64086408u, -1032.0f);
+  h[1] = add_h2((x & 0x00F000F0u) ^ 0x54805480u, -72.0f);
+  x >>= 8;
+  h[2] = add_h2((x & 0x000F000Fu) ^ 0x64086408u, -1032.0f);
+  h[3] = add_h2((x & 0x00F000F0u) ^ 0x54805480u, -72.0f);
+}
+
+// 8-bit codes of a dword as fp16: bytes (0, 2), (1, 3), as mantissas of 1024 + (c + 128).
+__device__ __forceinline__ void bytes_f16(uint32_t x, uint32_t (&h)[2]) {
+  x ^= 0x80808080u;
+  h[0] = add_h2(__builtin_amdgcn_perm(0x64646464u, x, 0x04020400u), -1152.0f);
+  h[1] = add_h2(__builtin_amdgcn_perm(0x64646464u, x, 0x04030401u), -1152.0f);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const f16x2 h = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// A sequence's rows and keys as the device sees them, whatever the tables hold: rows lie in
+// [0, total_q), keys in the sequence's page table.
+struct Seq {
+  int64_t q0;
+  int q_len, kv_len;
+};
+__device__ __forceinline__ Seq sequence(const KvAttentionArgs& a, int b) {
+  Seq s;
+  int64_t q0, q1;
+  if (a.q_start) {
+    q0 = a.q_start[b];
+    q1 = a.q_start[b + 1];
+    q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
+    q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
+  } else {
+    const int64_t n = a.total_q / a.seqs;
+    q0 = b * n;
+    q1 = q0 + n;
+  }
+  s.q0 = q0;
+  s.q_len = static_cast<int>(q1 - q0);
+  const int64_t most = (int64_t)a.max_pages << a.lps;
+  const int64_t kv = a.kv_len[b];
+  s.kv_len = static_cast<int>(kv < 0 ? 0 : kv > most ? most : kv);
+  return s;
+}
+
+// The keys [lo, hi) that row r of a sequence attends to.
+__device__ __forceinline__ void key_range(const KvAttentionArgs& a, const Seq& s, int token, int& lo, int& hi) {
+  hi = s.kv_len;
+  lo = 0;
+  if (a.causal) {
+    const int pos = s.kv_len - s.q_len + token;   // the token's own position, below 0 if it has none
+    hi = pos + 1 < 0 ? 0 : pos + 1;
+    if (a.window > 0) lo = pos + 1 - a.window < 0 ? 0 : pos + 1 - a.window;
+  }
+}
+
+// Where the codes of a tile's 16-token steps lie. A page index outside the cache masks its tokens
+// (they load from page 0).
+struct Step {
+  const uint8_t* block;   // the (page, head) block
+  int off;                // the step's first token in its page
+  bool ok;
+};
+
+template <int D, int BITS>
+struct Geometry {
+  using R = Row<D, BITS>;
+  static constexpr int kLaneBytes = R::kBytes / 4;                           // K (or V) bytes a lane loads of a 16-token step
+  static constexpr int kLoad = kLaneBytes < 16 ? kLaneBytes : 16;            // in loads of this many
+  static constexpr int kLoads = kLaneBytes / kLoad;
+  static constexpr int kWords = kLoad / 4;
+  static constexpr int kOps = D / 32;                                        // matrix steps of a q . k
+  static constexpr int kTilesD = D / 16;                                     // 16-wide tiles of the output
+};
+
+template <int D, int BITS>
+struct Tile {
+  using G = Geometry<D, BITS>;
+  uint32_t k[4][G::kLoads][G::kWords], v[4][G::kLoads][G::kWords];
+  f32x4 ks[4], vs[4];
+  uint32_t ok;   // bit j: step j's page is in the cache
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = x[i];
+  } else {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    w[0] = x[0];
+    w[1] = x[1];
+  }
+}
+
+// The codes and scales of keys [64 tile, 64 tile + 64) of sequence b. Lane (r, g) = (lane % 16,
+// lane / 16) loads, of each 16-token step, token r's K bytes (chunk g of every 4 * kLoad) and of
+// the four tokens 4g .. 4g+3 the V columns kLoad/4 * r ..: each load instruction of the wave reads
+// 64 * kLoad contiguous bytes. Steps past the last page entry re-read the table's last entry.
+template <int D, int BITS>
+__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const int32_t* table, int head, int last_page,
+                                          int tile, int r, int g, Tile<D, BITS>& t) {
+  using G = Geometry<D, BITS>;
+  using R = Row<D, BITS>;
+  const int page = 1 << a.lps;
+  t.ok = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int tok = tile * kTile + 16 * j;
+    int at = tok >> a.lps;
+    at = at > last_page ? last_page : at;
+    const int pg = __builtin_amdgcn_readfirstlane(table[at]);
+    const bool ok = pg >= 0 && pg < a.num_pages;
+    if (ok) t.ok |= 1u << j;
+    const uint8_t* block = a.cache + ((int64_t)(ok ? pg : 0) * a.heads + head) * a.head_bytes;
+    const int off = tok & (page - 1);
+    const uint8_t* kp = block + off * R::kBytes + r * R::kBytes + g * G::kLoad;
+    const uint8_t* vp = block + page * R::kBytes + off * R::kBytes + g * (4 * R::kBytes) + r * G::kLoad;
+#pragma unroll
+    for (int l = 0; l < G::kLoads; l++) {
+      load_words(kp + l * 4 * G::kLoad, t.k[j][l]);
+      load_words(vp + l * 16 * G::kLoad, t.v[j][l]);
+    }
+    const float* sp = reinterpret_cast<const float*>(block + 2 * page * R::kBytes) + off + 4 * g;
+    t.ks[j] = *reinterpret_cast<const f32x4*>(sp);
+    t.vs[j] = *reinterpret_cast<const f32x4*>(sp + page);
+  }
+}
+
+// The 8-element chunk of a row that K operand `op` of lane group g holds.
+template <int D, int BITS>
+__device__ __forceinline__ int operand_chunk(int op, int g) {
+  using G = Geometry<D, BITS>;
+  constexpr int kPer = G::kLoad / BITS;   // 8-element chunks a load brings to a lane
+  return (op / kPer) * (4 * kPer) + g * kPer + op % kPer;
+}
+
+// Column (element) of the output row that accumulator `m`, register i of lane group g holds.
+template <int D, int BITS>
+__device__ __forceinline__ int output_column(int m, int i, int g) {
+  using G = Geometry<D, BITS>;
+  const int row = 4 * g + i;
+  if constexpr (BITS == 4) {
+    const int l = m / (2 * G::kWords), x = m / 2 % G::kWords, e = m % 2;
+    return 2 * (l * 16 * G::kWords + G::kWords * row + x) + e;
+  } else {
+    return (m / G::kWords) * 16 * G::kWords + G::kWords * row + m % G::kWords;
+  }
+}
+
+// A wave's running softmax over 16 query rows; lane (r, g) holds row r.
+template <int D, int BITS>
+struct State {
+  using G = Geometry<D, BITS>;
+  f32x4 o[G::kTilesD];
+  float m;      // largest logit so far, before the row's factor c
+  float l;      // this lane's part of sum 2^(c (t - m))
+  float vref;   // the power of two that the weights are scaled by (the same in every lane)
+};
+
+constexpr float kWeightTop = 32768.0f;   // weights stay at or below 2^15
+
+template <int D, int BITS, bool SPLIT, bool FULL>
+__device__ __forceinline__ void attend_tile(const Tile<D, BITS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
+                                            float c, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
+  using G = Geometry<D, BITS>;
+  float w[4][4], vs[4][4];
+  float top = neg_inf(), vtop = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int op = 0; op < G::kOps; op++) {
+      u32x4 kop;
+      if constexpr (BITS == 4) {
+        uint32_t h[4];
+        nibbles_f16(t.k[j][op / G::kWords][op % G::kWords], h);
+        kop = u32x4{h[0], h[1], h[2], h[3]};
+      } else {
+        uint32_t h0[2], h1[2];
+        bytes_f16(t.k[j][op / 2][op % 2 * 2], h0);
+        bytes_f16(t.k[j][op / 2][op % 2 * 2 + 1], h1);
+        kop = u32x4{h0[0], h0[1], h1[0], h1[1]};
+      }
+      if constexpr (SPLIT) acc = mfma(kop, q2[op], acc);
+      acc = mfma(kop, q[op], acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      float x = acc[i] * t.ks[j][i], y = t.vs[j][i];
+      if constexpr (!FULL) {
+        const int key = first + 16 * j + i;   // `first` includes 4 g
+        const bool there = key < kv_len && (t.ok >> j & 1u);
+        if (!(there && key >= lo && key < hi)) x = neg_inf();
+        if (!there) y = 0.0f;
+      }
+      w[j][i] = x;
+      vs[j][i] = y;
+      top = fmaxf(top, x);
+      vtop = fmaxf(vtop, y);
+    }
+  }
+  top = quad_max(top);
+  vtop = quad_max(vtop);
+  const float m_new = fmaxf(s.m, top);
+  const float mc = m_new == neg_inf() ? 0.0f : m_new * c;
+  float alpha = s.m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(s.m * c - mc);
+  s.m = m_new;
+  s.l *= alpha;
+  // The weights' scale grows with the largest value scale met.
+  if (vtop >= s.vref) {
+    const float grown = __uint_as_float((__float_as_uint(vtop) & 0x7F800000u) + 0x00800000u);
+    alpha *= s.vref / grown;
+    s.vref = grown;
+  }
+  if (__any(alpha != 1.0f)) {
+#pragma unroll
+    for (int m = 0; m < G::kTilesD; m++) s.o[m] *= alpha;
+  }
+  const float up = kWeightTop / s.vref;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(w[j][i], c, -mc));
+      s.l += p;
+      w[j][i] = p * (vs[j][i] * up);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const u32x4 p = {pack_f16(w[j][0], w[j][2]), pack_f16(w[j][1], w[j][3]),
+                     pack_f16(w[j + 1][0], w[j + 1][2]), pack_f16(w[j + 1][1], w[j + 1][3])};
+#pragma unroll
+    for (int l = 0; l < G::kLoads; l++) {
+#pragma unroll
+      for (int x = 0; x < G::kWords; x++) {
+        if constexpr (BITS == 4) {
+          uint32_t h0[4], h1[4];
+          nibbles_f16(t.v[j][l][x], h0);
+          nibbles_f16(t.v[j + 1][l][x], h1);
+          const int m = (l * G::kWords + x) * 2;
+          s.o[m] = mfma(u32x4{h0[0], h0[2], h1[0], h1[2]}, p, s.o[m]);
+          s.o[m + 1] = mfma(u32x4{h0[1], h0[3], h1[1], h1[3]}, p, s.o[m + 1]);
+        } else {
+          uint32_t h0[2], h1[2];
+          bytes_f16(t.v[j][l][x], h0);
+          bytes_f16(t.v[j + 1][l][x], h1);
+          const int m = l * G::kWords + x;
+          s.o[m] = mfma(u32x4{h0[0], h0[1], h1[0], h1[1]}, p, s.o[m]);
+        }
+      }
+    }
+  }
+}
+
+// A row's output in the rotated domain, 8 elements a lane and block, rotated back and stored.
+template <int D, int BITS>
+__device__ __forceinline__ void store_row(uint8_t* p, int dt, float (&v)[Row<D, BITS>::kChunks][8], int c, bool ok) {
+  using R = Row<D, BITS>;
+#pragma unroll
+  for (int b = 0; b < R::kChunks; b++) {
+    const float f = wht_block<R::kLanes>(v[b], c) * R::kNorm;
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[b][i] *= f;
+    if (ok) store8(p + (b * 128 + c * 8) * 2, dt, v[b]);
+  }
+}
+
+// One workgroup: a tile of 16 query rows of one key head and sequence, and one split of its keys.
+// The four waves take the split's 64-key tiles in turn, each with a softmax of its own; they are
+// joined through LDS, and splits through the workspace (kv_join_kernel).
+template <int D, int BITS, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttentionArgs a) {
+  using R = Row<D, BITS>;
+  using G = Geometry<D, BITS>;
+  constexpr int kOutPad = 4;
+  __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows][D + kOutPad];
+  __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows], lds_c[kRows];
+  uint32_t* lds_q = reinterpret_cast<uint32_t*>(lds_o);   // [2][kRows][D / 2], before the first key
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.splits;
+  const int head = blockIdx.x / a.splits % a.heads;
+  const int b = blockIdx.y;
+  const Seq s = sequence(a, b);
+  const int rows = s.q_len * a.group;   // q_len < 2^31 / group is checked on the host
+  const int32_t* table = a.pages + (int64_t)b * a.max_pages;
+  const int last_page = a.max_pages - 1;
+
+  for (int tile = blockIdx.x / (a.splits * a.heads); tile * kRows < rows; tile += a.row_tiles) {
+    // Queries: rotated, scaled, to fp16, in the K operands' element order.
+    {
+      const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
+      const int at = tile * kRows + row;
+      const bool ok = row < kRows && at < rows;
+      const int token = ok ? at / a.group : 0, qh = head * a.group + (ok ? at % a.group : 0);
+      const uint8_t* x = a.q + ((s.q0 + token) * a.q_token + qh * a.q_head) * 2;
+      float v[R::kChunks][8], sign = 1.0f, top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < R::kChunks; k++) load8(x + (k * 128 + chunk * 8) * 2, a.dt, v[k]);
+#pragma unroll
+      for (int k = 0; k < R::kChunks; k++) {
+        sign = wht_block<R::kLanes>(v[k], chunk);
+#pragma unroll
+        for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[k][i]));
+      }
+      top = row_max<R::kLanes>(top);
+      // 2^(8 - exponent): the largest element comes to lie in [256, 512). Rows of zeros, and
+      // largest elements below 2^-100, are scaled by 2^108.
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      e = e < -100 ? -100 : e;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+      __syncthreads();   // the tile before has read the LDS
+      if (row < kRows) {
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) {
+          float y[8];
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            y[i] = v[k][i] * (sign * up);
+            const _Float16 h = static_cast<_Float16>(y[i]);
+            hi[i] = __builtin_bit_cast(uint16_t, h);
+            lo[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(y[i] - static_cast<float>(h)));
+          }
+          // Pairs in the order in which nibbles_f16 / bytes_f16 give the codes.
+          constexpr int kA[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5};
+          constexpr int kB = BITS == 4 ? 4 : 2;
+          uint32_t* p = lds_q + row * (D / 2) + (k * 16 + chunk) * 4;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            p[i] = hi[kA[i]] | (hi[kA[i] + kB] << 16);
+            if constexpr (SPLIT) p[kRows * (D / 2) + i] = lo[kA[i]] | (lo[kA[i] + kB] << 16);
+          }
+        }
+        // Logits in base 2 are t * c, t = sum of fp16 query times code, times the key's scale.
+        if (u == 0) lds_c[row] = a.scale * (kLog2e * R::kNorm) / up;
+      }
+      __syncthreads();
+    }
+    u32x4 q[G::kOps], q2[G::kOps];
+#pragma unroll
+    for (int op = 0; op < G::kOps; op++) {
+      const uint32_t* p = lds_q + r * (D / 2) + operand_chunk<D, BITS>(op, g) * 4;
+      q[op] = *reinterpret_cast<const u32x4*>(p);
+      q2[op] = SPLIT ? *reinterpret_cast<const u32x4*>(p + kRows * (D / 2)) : q[op];
+    }
+    const float c = fmaxf(lds_c[r], 1.1754944e-38f);   // a positive factor keeps masked logits at -inf
+    __syncthreads();   // lds_q is read: lds_o may be written
+
+    // Keys of this tile's rows, and of this lane's row.
+    const int row_first = tile * kRows, row_last = (row_first + kRows < rows ? row_first + kRows : rows) - 1;
+    int lo, hi, t_lo, t_hi, x;
+    const bool mine = row_first + r < rows;
+    key_range(a, s, (mine ? row_first + r : row_first) / a.group, lo, hi);
+    if (!mine) hi = lo = 0;
+    int full_lo, full_hi;   // every row attends to [full_lo, full_hi)
+    key_range(a, s, row_first / a.group, t_lo, full_hi);
+    key_range(a, s, row_last / a.group, full_lo, t_hi);
+    (void)x;
+    const bool whole = row_last - row_first == kRows - 1;
+    const int tiles_lo = t_lo / kTile, tiles_hi = (t_hi + kTile - 1) / kTile;
+    const int count = tiles_hi > tiles_lo ? tiles_hi - tiles_lo : 0;
+    const int begin = tiles_lo + static_cast<int>((int64_t)count * split / a.splits);
+    const int end = tiles_lo + static_cast<int>((int64_t)count * (split + 1) / a.splits);
+
+    State<D, BITS> st;
+#pragma unroll
+    for (int m = 0; m < G::kTilesD; m++) st.o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    st.m = neg_inf();
+    st.l = 0.0f;
+    st.vref = 0x1p-110f;
+    for (int i = begin + wave; i < end; i += kWaves) {
+      Tile<D, BITS> t;
+      load_tile<D, BITS>(a, table, head, last_page, i, r, g, t);
+      const int first = i * kTile;
+      const bool full = whole && t.ok == 15u && first >= full_lo && first + kTile <= full_hi;
+      if (full)
+        attend_tile<D, BITS, SPLIT, true>(t, q, q2, c, first + 4 * g, lo, hi, s.kv_len, st);
+      else
+        attend_tile<D, BITS, SPLIT, false>(t, q, q2, c, first + 4 * g, lo, hi, s.kv_len, st);
+    }
+
+    // Join the waves.
+    st.l = quad_sum(st.l);
+    if (g == 0) {
+      lds_m[wave][r] = st.m == neg_inf() ? neg_inf() : st.m * c;
+      lds_l[wave][r] = st.l;
+    }
+    __syncthreads();
+    float top = lds_m[0][r];
+#pragma unroll
+    for (int w = 1; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
+    {
+      const float m = lds_m[wave][r];
+      const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top) * (st.vref / kWeightTop);
+#pragma unroll
+      for (int m16 = 0; m16 < G::kTilesD; m16++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) lds_o[wave][r][output_column<D, BITS>(m16, i, g)] = st.o[m16][i] * f;
+      }
+    }
+    __syncthreads();
+    {
+      const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
+      const int at = tile * kRows + row, rc = row < kRows ? row : kRows - 1;
+      const bool ok = row < kRows && at < rows;
+      const int token = ok ? at / a.group : 0, qh = head * a.group + (ok ? at % a.group : 0);
+      float best = neg_inf(), sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) best = fmaxf(best, lds_m[w][rc]);
+#pragma unroll
+      for (int w = 0; w < kWaves; w++)
+        sum += lds_m[w][rc] == neg_inf() ? 0.0f : lds_l[w][rc] * __builtin_amdgcn_exp2f(lds_m[w][rc] - best);
+      float v[R::kChunks][8];
+#pragma unroll
+      for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          float y = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; w++) y += lds_o[w][rc][k * 128 + chunk * 8 + i];
+          v[k][i] = y;
+        }
+      }
+      const int64_t out_row = (s.q0 + token) * a.q_heads + qh;
+      if (a.splits > 1) {
+        if (ok) {
+          float* p = a.part_out + (out_row * a.splits + split) * D;
+#pragma unroll
+          for (int k = 0; k < R::kChunks; k++) store8(reinterpret_cast<uint8_t*>(p + k * 128 + chunk * 8), kF32, v[k]);
+          if (u == 0) {
+            a.part_stat[(out_row * a.splits + split) * 2] = best;
+            a.part_stat[(out_row * a.splits + split) * 2 + 1] = sum;
+          }
+        }
+      } else {
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[k][i] *= inv;
+        }
+        if (ok && a.lse && u == 0) a.lse[out_row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+        store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, chunk, ok);
+      }
+    }
+  }
+}
+
+// Joins the splits of a row: kLanes lanes a row.
+template <int D, int BITS>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
+  using R = Row<D, BITS>;
+  const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u);
+  const int64_t row = (int64_t)blockIdx.x * (256 / R::kLanes) + threadIdx.x / R::kLanes;
+  const int64_t all = a.total_q * a.q_heads, rc = row < all ? row : all - 1;
+  const int64_t token = rc / a.q_heads;
+  // Rows of no sequence were not computed: they are left as they were.
+  bool ok = row < all;
+  if (a.q_start) ok = ok && token >= a.q_start[0] && token < a.q_start[a.seqs];
+  const float* stat = a.part_stat + rc * a.splits * 2;
+  const float* part = a.part_out + rc * a.splits * D;
+  float best = neg_inf(), sum = 0.0f;
+  for (int i = 0; i < a.splits; i++) best = fmaxf(best, stat[2 * i]);
+  float v[R::kChunks][8];
+#pragma unroll
+  for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[k][i] = 0.0f;
+  }
+  for (int i = 0; i < a.splits; i++) {
+    const float m = stat[2 * i];
+    if (m == neg_inf()) continue;
+    const float f = __builtin_amdgcn_exp2f(m - best);
+    sum = __builtin_fmaf(stat[2 * i + 1], f, sum);
+#pragma unroll
+    for (int k = 0; k < R::kChunks; k++) {
+      float x[8];
+      load8(reinterpret_cast<const uint8_t*>(part + (int64_t)i * D + k * 128 + chunk * 8), kF32, x);
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[k][e] = __builtin_fmaf(x[e], f, v[k][e]);
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[k][i] *= inv;
+  }
+  if (ok && a.lse && u == 0) a.lse[rc] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+  store_row<D, BITS>(a.out + (token * a.out_token + rc % a.q_heads * a.out_head) * 2, a.dt, v, chunk, ok);
+}
+
+template <int D, int BITS>
+hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.splits * a.heads * a.row_tiles), static_cast<unsigned>(a.seqs));
+  if (a.dt == kF16)
+    kv_attend_kernel<D, BITS, true><<<grid, kWaves * 64, 0, stream>>>(a);
+  else
+    kv_attend_kernel<D, BITS, false><<<grid, kWaves * 64, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  constexpr int kPer = 256 / Row<D, BITS>::kLanes;
+  kv_join_kernel<D, BITS><<<dim3(static_cast<unsigned>((a.total_q * a.q_heads + kPer - 1) / kPer)), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int bits,
+                                  int64_t max_q_len, int64_t max_kv_len, int window) {
+  const int64_t group = q_heads / heads;
+  KvAttentionPlan p;
+  const int64_t tiles = (max_q_len * group + kRows - 1) / kRows;
+  p.row_tiles = static_cast<int>(tiles < 1 ? 1 : tiles);
+  // Enough workgroups for 256 compute units several times over, as long as each wave of a split
+  // has two tiles of keys or more.
+  int64_t span = max_kv_len;
+  if (window > 0 && window + max_q_len < span) span = window + max_q_len;
+  const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = (1024 + groups - 1) / groups;
+  const int64_t most = (span + kTile - 1) / kTile / (2 * kWaves);
+  int64_t splits = want < most ? want : most;
+  p.splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+  p.workspace_bytes = p.splits > 1 ? (size_t)total_q * q_heads * p.splits * (head_dim + 2) * 4 : 0;
+  return p;
+}
+
+hipError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, int bits, hipStream_t stream) {
+  if (a.total_q == 0 || a.seqs == 0) return hipSuccess;
+  switch (head_dim) {
+    case 64: return bits == 8 ? launch<64, 8>(a, stream) : launch<64, 4>(a, stream);
+    case 128: return bits == 8 ? launch<128, 8>(a, stream) : launch<128, 4>(a, stream);
+    default: return bits == 8 ? launch<256, 8>(a, stream) : launch<256, 4>(a, stream);
+  }
+}
+
+}  // namespace convrot

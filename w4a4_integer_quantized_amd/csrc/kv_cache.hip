@@ -1,0 +1,183 @@
+// kv_cache.hip -- keys and values rotated and quantized into a paged cache as they are written,
+// and read back (rq_kv_cache_write, rq_kv_cache_read; layout and arithmetic in convrot.h).
+//
+// Both are one pass over their data and bound by memory. A head row of D elements takes
+// min(D, 128) / 8 lanes, 8 consecutive elements (16 bytes of fp16 / bf16) a lane and block, so
+// that its transform is seven (six) butterfly stages of which three stay in the lane and the
+// others are DPP exchanges; a 256-element row is two blocks in the same lanes. A wave holds the
+// same head of 4 (D = 64: 8) consecutive tokens. Lanes are never masked off inside the transform:
+// rows past the end load the last row and store nothing.
+#include "kv_common.h"
+
+namespace convrot {
+namespace {
+
+using namespace kv;
+
+constexpr int kThreads = 256;
+constexpr float kRoundMagic = 12582912.0f;   // 1.5 * 2^23: its low mantissa bits hold the code
+
+// The block of (page, head) that holds `slot`, and the token's place in it. False if the slot
+// lies outside the cache.
+struct Place {
+  uint8_t* block;
+  int off;
+};
+
+template <int D, int BITS>
+__device__ __forceinline__ bool find(const KvCacheArgs& a, int64_t slot, int head, Place& p) {
+  const int64_t page = slot >> a.lps;
+  const bool in = slot >= 0 && page < a.num_pages;
+  p.block = a.cache + ((in ? page : 0) * a.heads + head) * a.head_bytes;
+  p.off = in ? static_cast<int>(slot & ((1 << a.lps) - 1)) : 0;
+  return in;
+}
+
+// The row's codes: rounded half to even by adding 1.5 * 2^23 (|u * inv| <= q_max < 2^22). `inv`
+// carries the lane's sign.
+template <int BITS>
+__device__ __forceinline__ void codes8(const float (&v)[8], float inv, uint32_t& lo, uint32_t& hi) {
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) y[i] = __float_as_uint(__fadd_rn(__fmul_rn(v[i], inv), kRoundMagic));
+  if constexpr (BITS == 8) {
+    lo = (y[0] & 0xFFu) | ((y[1] & 0xFFu) << 8) | ((y[2] & 0xFFu) << 16) | (y[3] << 24);
+    hi = (y[4] & 0xFFu) | ((y[5] & 0xFFu) << 8) | ((y[6] & 0xFFu) << 16) | (y[7] << 24);
+  } else {
+    lo = hi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) lo |= (y[i] & 0xFu) << (4 * i);
+  }
+}
+
+// One workgroup: kThreads / kLanes rows, i.e. that many consecutive tokens of one head; gridDim.y
+// is the heads. The keys' row and the values' row of a token are the same lanes' work.
+template <int D, int BITS>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a) {
+  using R = Row<D, BITS>;
+  const int u = threadIdx.x % R::kLanes, c = chunk_of_lane(u);
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / R::kLanes) + threadIdx.x / R::kLanes;
+  const int64_t tc = t < a.tokens ? t : a.tokens - 1;
+  const int head = blockIdx.y;
+  Place p;
+  const bool in = find<D, BITS>(a, a.slots[tc], head, p) && t < a.tokens;
+  const int es = elem_bytes(a.dt);
+#pragma unroll
+  for (int part = 0; part < 2; part++) {   // keys, values
+    const uint8_t* x = (part ? a.v : a.k) +
+                       (tc * (part ? a.v_token : a.k_token) + head * (part ? a.v_head : a.k_head)) * es;
+    float v[R::kChunks][8], sign = 1.0f, m = 0.0f;
+#pragma unroll
+    for (int b = 0; b < R::kChunks; b++) load8(x + (b * 128 + c * 8) * es, a.dt, v[b]);
+#pragma unroll
+    for (int b = 0; b < R::kChunks; b++) {
+      sign = wht_block<R::kLanes>(v[b], c);
+#pragma unroll
+      for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[b][i]));
+    }
+    m = row_max<R::kLanes>(m);
+    // A row whose absmax is zero, or too small for fl(q_max / a) to be finite, is a zero row.
+    float inv = m > 0.0f ? __fdiv_rn(R::kQmax, m) : 0.0f;
+    if (__builtin_isinf(inv)) inv = 0.0f;
+    const float scale = inv != 0.0f ? __fdiv_rn(__fmul_rn(m, R::kNorm), R::kQmax) : 0.0f;
+    if (!in) continue;   // no exchange follows in this part; the next one takes every lane again
+    const int page = 1 << a.lps;
+    if (u == 0)
+      reinterpret_cast<float*>(p.block + 2 * (size_t)page * R::kBytes)[part * page + p.off] = scale;
+#pragma unroll
+    for (int b = 0; b < R::kChunks; b++) {
+      uint32_t lo, hi;
+      codes8<BITS>(v[b], sign * inv, lo, hi);
+      const int at = b * (16 * BITS) + c * BITS;   // the chunk's first byte in its row
+      if (part == 0) {
+        uint8_t* q = p.block + p.off * R::kBytes + at;
+        if constexpr (BITS == 8)
+          *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
+        else
+          *reinterpret_cast<uint32_t*>(q) = lo;
+      } else {
+        uint8_t* q = p.block + (size_t)page * R::kBytes + ((p.off >> 2) * R::kBytes + at) * 4 + (p.off & 3);
+#pragma unroll
+        for (int i = 0; i < BITS; i++) q[4 * i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      }
+    }
+  }
+}
+
+// The same rows back: x = fl(fl(scale * c) * WHT(codes)), the transform of the codes exact in
+// binary32, rounded once to the output type. A slot outside the cache gives a row of zeros.
+template <int D, int BITS>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCacheArgs a) {
+  using R = Row<D, BITS>;
+  const int u = threadIdx.x % R::kLanes, c = chunk_of_lane(u);
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / R::kLanes) + threadIdx.x / R::kLanes;
+  const int64_t tc = t < a.tokens ? t : a.tokens - 1;
+  const int head = blockIdx.y;
+  Place p;
+  const bool in = find<D, BITS>(a, a.slots[tc], head, p);
+  const int es = elem_bytes(a.dt), page = 1 << a.lps;
+#pragma unroll
+  for (int part = 0; part < 2; part++) {
+    const float* scales = reinterpret_cast<const float*>(p.block + 2 * (size_t)page * R::kBytes);
+    const float s = __fmul_rn(scales[part * page + p.off], R::kNorm);
+    uint8_t* x = (part ? a.v_out : a.k_out) +
+                 (tc * (part ? a.v_token : a.k_token) + head * (part ? a.v_head : a.k_head)) * es;
+#pragma unroll
+    for (int b = 0; b < R::kChunks; b++) {
+      const int at = b * (16 * BITS) + c * BITS;
+      uint32_t w[2];
+      if (part == 0) {
+        const uint8_t* q = p.block + p.off * R::kBytes + at;
+        w[0] = *reinterpret_cast<const uint32_t*>(q);
+        if constexpr (BITS == 8) w[1] = *reinterpret_cast<const uint32_t*>(q + 4);
+      } else {
+        // Four tokens' bytes come with each 4-byte column; the neighbouring rows of the wave
+        // load the same 16 bytes, so the lines are read once.
+        const uint8_t* q = p.block + (size_t)page * R::kBytes + ((p.off >> 2) * R::kBytes + at) * 4;
+        const uint32_t shift = 8 * (p.off & 3);
+#pragma unroll
+        for (int i = 0; i < BITS / 4; i++) {
+          const u32x4 y = *reinterpret_cast<const u32x4*>(q + 16 * i);
+          w[i] = ((y[0] >> shift) & 0xFFu) | (((y[1] >> shift) & 0xFFu) << 8) |
+                 (((y[2] >> shift) & 0xFFu) << 16) | ((y[3] >> shift) << 24);
+        }
+      }
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if constexpr (BITS == 8)
+          v[i] = static_cast<float>(static_cast<int32_t>(w[i / 4] << (24 - 8 * (i & 3))) >> 24);
+        else
+          v[i] = static_cast<float>(static_cast<int32_t>(w[0] << (28 - 4 * i)) >> 28);
+      }
+      const float f = s * wht_block<R::kLanes>(v, c);
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = in ? __fmul_rn(f, v[i]) : 0.0f;
+      if (t < a.tokens) store8(x + (b * 128 + c * 8) * es, a.dt, v);
+    }
+  }
+}
+
+template <int D, int BITS>
+hipError_t launch(const KvCacheArgs& a, bool write, hipStream_t stream) {
+  constexpr int kRows = kThreads / Row<D, BITS>::kLanes;
+  const dim3 grid(static_cast<unsigned>((a.tokens + kRows - 1) / kRows), static_cast<unsigned>(a.heads));
+  if (write)
+    kv_write_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
+  else
+    kv_read_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_cache(const KvCacheArgs& a, int head_dim, int bits, bool write, hipStream_t stream) {
+  if (a.tokens == 0) return hipSuccess;
+  switch (head_dim) {
+    case 64: return bits == 8 ? launch<64, 8>(a, write, stream) : launch<64, 4>(a, write, stream);
+    case 128: return bits == 8 ? launch<128, 8>(a, write, stream) : launch<128, 4>(a, write, stream);
+    default: return bits == 8 ? launch<256, 8>(a, write, stream) : launch<256, 4>(a, write, stream);
+  }
+}
+
+}  // namespace convrot
