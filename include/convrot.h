@@ -302,9 +302,9 @@ rq_status rq_kv_cache_read(const void *cache, int64_t num_pages, const int64_t *
  * What the device tables hold is not trusted with memory: query rows outside [0, total_q) do not
  * exist, kv_len is cut to [0, max_pages * page_size], and the tokens of a page index outside
  * [0, num_pages) count as not there.
- * Arithmetic: R q rounded to fp16 (fp16 queries: to two fp16, leading and remainder) after a power
- * of two a row, codes exact, products and sums in fp32, the weights p_j * scale_j rounded to fp16
- * after a power of two, statistics and the sums of p_j in fp32. Results do not depend on
+ * Arithmetic: R q and the weights p_j * scale_j are rounded to fp16 (for RQ_F16 to two fp16, leading
+ * and remainder), scaled so that the largest of a row lies well inside fp16's range; codes are
+ * exact, products, sums and softmax statistics are fp32. Results do not depend on
  * what else is in the batch beyond the way the keys are split (max_q_len, max_kv_len, seqs);
  * calls with equal arguments give equal bits. */
 typedef struct {

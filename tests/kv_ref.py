@@ -114,8 +114,9 @@ def attention(Q, cache, pages, kv_len, q_start, dtype, causal=True, window=0, sc
     fp16: 2^-11 an element (2^-22 in two parts), and 2^-25 / 2^8 of the row's largest below fp16's normal range. Logits in base
     2: the scale, 1 / sqrt B, log2 e: 6 u of |logit|, and of the row's largest, whose multiple is taken off. An error
     d of the logits changes a normalised weight by expm1(2 d) at most. exp2: 4 u and each rescaling of a
-    partial sum 4 u (64 of them at most here). The weight's fp16: 2^-11, and 2^-25 against 2^14 of the
-    largest weight's scale where it is below fp16's range (fewer than 2^12 keys). Sums over T keys: T u. These stand
+    partial sum 4 u (64 of them at most here). The weight's fp16: 2^-11 (2^-22 in two parts), and below fp16's
+    normal range half of its smallest step, 2^-25, where the row's largest weight p s_v is at least 2^6: 2^-31 of
+    that, a key, times a code. Sums over T keys: T u. These stand
     in the rotated domain; going back spreads a row's error over the block: sum / sqrt B. Then the output's half step."""
     total, q_heads, dim = Q.shape
     group = q_heads // cache.heads
@@ -161,9 +162,9 @@ def attention(Q, cache, pages, kv_len, q_start, dtype, causal=True, window=0, sc
                 P = P / l
                 O[i, h] = R @ (P @ V)
                 lse[i, h] = m + np.log(l)
-                each = np.expm1(2 * d.max()) + 2.0 ** -11 + (len(L) + 4 + 64 * 4) * U32
-                vs = cache.scale[1][slots, h // group][ok].astype(np.float64).max() if len(L) else 0.0
-                rot = P @ np.abs(V) * each + len(L) * 2.0 ** -39 * vs * (127 if cache.bits == 8 else 7) / l
+                each = np.expm1(2 * d.max()) + uq + (len(L) + 4 + 64 * 4) * U32
+                most = (P * cache.scale[1][slots, h // group][ok].astype(np.float64)).max()
+                rot = P @ np.abs(V) * each + len(L) * 2.0 ** -31 * most * (127 if cache.bits == 8 else 7)
                 blocks = rot.reshape(-1, B).sum(1) / np.sqrt(B)
                 e = np.repeat(blocks, B) * (1 + 16 * U32)
                 tol[i, h] = e + EPS[dtype] * (np.abs(O[i, h]) + e) + (2.0 ** -25 if dtype == "f16" else 0.0)

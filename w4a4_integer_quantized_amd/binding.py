@@ -412,69 +412,64 @@ def gemm_s32(Xq, Wq, bits: int = 8, K: Optional[int] = None, stream=None,
 
 
 # ------------------------------------------------------------------- the cache and attention over it
+# These calls sit in a decode loop, where the host's time counts: the checks are a few comparisons
+# each, and the stream's handle is fetched without building a Stream object.
 def make_kv_cfg(kv_heads: int, head_dim: int, page_size: int = 64, bits: int = 4) -> rq_kv_config:
     return rq_kv_config(bits, head_dim, kv_heads, page_size)
 
 
-class _Placed:
-    """Makes `device` current, and `stream` where one is given, for allocations and the launch;
-    `handle` is the stream's."""
-
-    def __init__(self, device, stream):
-        cuda = _torch().cuda
-        if stream is not None and stream.device != device:
-            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
-        self._device = None if device.index == cuda.current_device() else cuda.device(device)
-        self._stream = None if stream is None else cuda.stream(stream)
-        self._given, self._at = stream, device
-
-    def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
-        s = self._given if self._given is not None else _torch().cuda.current_stream(self._at)
-        self.handle = s.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+def _launch_on(device, stream, call):
+    """call(handle of the stream) with `device` current, and `stream`, where one is given, too: what
+    is allocated meanwhile belongs to it."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("tensors must be device tensors, got %s" % device)
+    index = device.index
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _kv_cache(cache, cfg):
     """The number of pages of a uint8 cache [pages, rq_kv_page_bytes(cfg)]."""
-    page = rq_kv_page_bytes(cfg)
-    if page == 0:
-        raise ConvRotError(RQ_EUNSUPPORTED, "rq_kv_page_bytes", load().rq_last_error_detail().decode())
-    if cache.dtype != _torch().uint8 or cache.dim() != 2 or cache.shape[1] != page or not cache.is_contiguous():
+    shape = cache.shape
+    if (len(shape) != 2 or shape[1] != cfg.kv_heads * cfg.page_size * (cfg.head_dim * cfg.bits // 8 * 2 + 8)
+            or cache.dtype != _torch().uint8 or not cache.is_contiguous()):
+        if rq_kv_page_bytes(cfg) == 0:
+            raise ConvRotError(RQ_EUNSUPPORTED, "rq_kv_page_bytes", load().rq_last_error_detail().decode())
         raise ValueError("cache must be a contiguous uint8 tensor [pages, %d], got %s %s"
-                         % (page, cache.dtype, tuple(cache.shape)))
-    return cache.shape[0]
+                         % (rq_kv_page_bytes(cfg), cache.dtype, tuple(shape)))
+    return shape[0]
 
 
-def _kv_rows(t, name, heads, dim, dtypes, tokens=None):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError("%s must be [%s, %d, %d], got %s" % (name, "tokens" if tokens is None else tokens, heads, dim,
-                                                              tuple(t.shape)))
+def _kv_rows(t, name, shape, dtypes):
+    """The token and head strides of rows [tokens, heads, dim]."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s dtype %s (expected one of %s)" % (name, t.dtype, ", ".join(map(str, dtypes))))
-    if t.stride(2) != 1:
+    stride = t.stride()
+    if stride[2] != 1:
         raise ValueError("%s must be contiguous along its last axis" % name)
-    return t.stride(0), t.stride(1)
+    return stride[0], stride[1]
 
 
 def _kv_table(t, name, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s %s" % (name, dtype, shape, t.dtype,
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s %s" % (name, dtype, tuple(shape), t.dtype,
                                                                                      tuple(t.shape)))
 
 
-def _on_gpu(device):
-    if device.type != "cuda":
-        raise ValueError("tensors must be device tensors, got %s" % device)
+def _kv_same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("tensors are on different devices: %s, %s" % (device, t.device))
 
 
 def kv_cache_alloc(num_pages: int, cfg: rq_kv_config, device="cuda"):
@@ -492,15 +487,19 @@ def kv_cache_write(K, V, slots, cache, cfg: rq_kv_config, stream=None):
     of `cache`, in place. A slot outside the cache (-1) skips its token; the others must differ."""
     torch = _torch()
     pages = _kv_cache(cache, cfg)
-    types = (torch.float32, torch.float16, torch.bfloat16)
-    kt, kh = _kv_rows(K, "K", cfg.kv_heads, cfg.head_dim, types)
-    vt, vh = _kv_rows(V, "V", cfg.kv_heads, cfg.head_dim, (K.dtype,), K.shape[0])
-    _kv_table(slots, "slots", torch.int64, (K.shape[0],))
-    _same_device(K, V, slots, cache)
-    _on_gpu(cache.device)
-    with _Placed(cache.device, stream) as at:
-        _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), _dtype_code(K), K.shape[0], kt, kh, vt, vh, slots.data_ptr(),
-                                 cfg, cache.data_ptr(), pages, at.handle), "rq_kv_cache_write")
+    tokens = slots.shape[0] if slots.dim() == 1 else -1
+    shape = (tokens, cfg.kv_heads, cfg.head_dim)
+    kt, kh = _kv_rows(K, "K", shape, (torch.float32, torch.float16, torch.bfloat16))
+    vt, vh = _kv_rows(V, "V", shape, (K.dtype,))
+    _kv_table(slots, "slots", torch.int64, (tokens,))
+    device = cache.device
+    _kv_same_device(device, K, V, slots)
+
+    def call(handle):
+        _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kt, kh, vt, vh, slots.data_ptr(), cfg,
+                                 cache.data_ptr(), pages, handle), "rq_kv_cache_write")
+
+    _launch_on(device, stream, call)
 
 
 def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, stream=None):
@@ -509,32 +508,36 @@ def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, str
     zeros."""
     torch = _torch()
     pages = _kv_cache(cache, cfg)
-    if slots.dim() != 1:
-        raise ValueError("slots must be a vector, got shape %s" % (tuple(slots.shape),))
-    tokens = slots.shape[0]
+    tokens = slots.shape[0] if slots.dim() == 1 else -1
+    shape = (tokens, cfg.kv_heads, cfg.head_dim)
     _kv_table(slots, "slots", torch.int64, (tokens,))
     types = (torch.float32, torch.float16, torch.bfloat16)
-    if out is not None:
-        if out_dtype is not None and out[0].dtype != out_dtype:
-            raise ValueError("out is %s, out_dtype is %s" % (out[0].dtype, out_dtype))
-        _same_device(cache, slots, *out)
-    else:
-        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    device = cache.device
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
         if out_dtype not in types:
             raise ValueError("out_dtype must be float32, float16 or bfloat16")
-        _same_device(cache, slots)
-    _on_gpu(cache.device)
-    with _Placed(cache.device, stream) as at:
+        _kv_same_device(device, slots)
+    else:
+        if out_dtype is not None and out[0].dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype is %s" % (out[0].dtype, out_dtype))
+        kt, kh = _kv_rows(out[0], "K", shape, types)
+        vt, vh = _kv_rows(out[1], "V", shape, (out[0].dtype,))
+        _kv_same_device(device, slots, *out)
+
+    def call(handle):
         if out is None:
-            shape = (tokens, cfg.kv_heads, cfg.head_dim)
-            out = (torch.empty(shape, dtype=out_dtype, device=cache.device),
-                   torch.empty(shape, dtype=out_dtype, device=cache.device))
-        K, V = out
-        kt, kh = _kv_rows(K, "K", cfg.kv_heads, cfg.head_dim, types, tokens)
-        vt, vh = _kv_rows(V, "V", cfg.kv_heads, cfg.head_dim, (K.dtype,), tokens)
+            K = torch.empty(shape, dtype=out_dtype, device=device)
+            V = torch.empty(shape, dtype=out_dtype, device=device)
+            strides = (shape[1] * shape[2], shape[2]) * 2
+        else:
+            (K, V), strides = out, (kt, kh, vt, vh)
         _check(rq_kv_cache_read(cache.data_ptr(), pages, slots.data_ptr(), tokens, cfg, K.data_ptr(), V.data_ptr(),
-                                _dtype_code(K), kt, kh, vt, vh, at.handle), "rq_kv_cache_read")
-    return K, V
+                                _dtype_code(K), *strides, handle), "rq_kv_cache_read")
+        return K, V
+
+    return _launch_on(device, stream, call)
 
 
 def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causal: bool = True, window: int = 0,
@@ -550,10 +553,11 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
     tensor of kv_attention_workspace_size() bytes or more. See rq_kv_attention in convrot.h."""
     torch = _torch()
     num_pages = _kv_cache(cache, cfg)
-    if Q.dim() != 3:
-        raise ValueError("Q must be [total_q, q_heads, head_dim], got %s" % (tuple(Q.shape),))
-    total, q_heads, dim = Q.shape
-    qt, qh = _kv_rows(Q, "Q", q_heads, cfg.head_dim, (torch.float16, torch.bfloat16))
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != cfg.head_dim:
+        raise ValueError("Q must be [total_q, q_heads, %d], got %s" % (cfg.head_dim, tuple(shape)))
+    total, q_heads, dim = shape
+    qt, qh = _kv_rows(Q, "Q", shape, (torch.float16, torch.bfloat16))
     if pages.dim() != 2:
         raise ValueError("pages must be [seqs, max_pages], got %s" % (tuple(pages.shape),))
     seqs, max_pages = pages.shape
@@ -561,26 +565,32 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
     _kv_table(kv_len, "kv_len", torch.int32, (seqs,))
     if q_start is not None:
         _kv_table(q_start, "q_start", torch.int32, (seqs + 1,))
-    _same_device(Q, cache, pages, kv_len, q_start, out, workspace)
-    _on_gpu(Q.device)
-    with _Placed(Q.device, stream) as at:
-        if out is None:
-            out = torch.empty((total, q_heads, dim), dtype=Q.dtype, device=Q.device)
-        ot, oh = _kv_rows(out, "out", q_heads, dim, (Q.dtype,), total)
-        lse = torch.empty((total, q_heads), dtype=torch.float32, device=Q.device) if return_lse else None
+    if out is not None:
+        ot, oh = _kv_rows(out, "out", shape, (Q.dtype,))
+    else:
+        ot, oh = q_heads * dim, dim
+    device = Q.device
+    _kv_same_device(device, cache, pages, kv_len, q_start, out, workspace)
+
+    def call(handle):
+        O = torch.empty(shape, dtype=Q.dtype, device=device) if out is None else out
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=device) if return_lse else None
         p = rq_kv_attention_params(
-            Q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            Q.data_ptr(), O.data_ptr(), None if lse is None else lse.data_ptr(),
             None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
-            max_q_len, max_kv_len, _dtype_code(Q), q_heads, seqs, max_pages, int(causal), window,
+            max_q_len, max_kv_len, _dtype_code(Q), q_heads, seqs, max_pages, bool(causal), window,
             dim ** -0.5 if softmax_scale is None else softmax_scale)
         need = rq_kv_attention_workspace_size(p, cfg)
-        if workspace is not None:
-            _check_bytes(workspace, "workspace", need, exact=False)
+        ws = workspace      # held until the launch; later uses of its memory follow on this stream
+        if ws is not None:
+            _check_bytes(ws, "workspace", need, exact=False)
         elif need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
-        _check(rq_kv_attention(p, cfg, cache.data_ptr(), num_pages, None if workspace is None else workspace.data_ptr(),
-                               0 if workspace is None else _nbytes(workspace), at.handle), "rq_kv_attention")
-    return (out, lse) if return_lse else out
+            ws = torch.empty((need,), dtype=torch.uint8, device=device)
+        _check(rq_kv_attention(p, cfg, cache.data_ptr(), num_pages, None if ws is None else ws.data_ptr(),
+                               0 if ws is None else _nbytes(ws), handle), "rq_kv_attention")
+        return (O, lse) if return_lse else O
+
+    return _launch_on(device, stream, call)
 
 
 def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages: int, cfg: rq_kv_config,

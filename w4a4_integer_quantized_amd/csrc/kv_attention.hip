@@ -6,9 +6,16 @@
 // output sum_j p_j v_j = R^T (sum_j (p_j s_v,j) c_v,j) is rotated back once. Codes are integers of
 // at most 7 bits and a sign, exact in fp16, so both products run on fp16 matrix instructions with
 // fp32 sums. Two roundings remain: of R q to fp16 (scaled by a power of two a row so that its
-// largest element lies in [256, 512); for fp16 queries a second fp16 holds what the first leaves),
-// and of the weights p_j s_v,j to fp16 (scaled by a power of two that keeps them below 2^15, so
-// 28 binades below the largest stay normal). Softmax statistics are fp32, in base 2.
+// largest element lies in [256, 512)) and of the weights p_j s_v,j to fp16. For fp16 queries and
+// outputs a second fp16 holds what the first leaves of both, and takes a second matrix
+// instruction: one rounding to 11 bits beside the output's own would be felt. bf16 has 8.
+//
+// The running softmax keeps a reference b for each row, not the maximum: a key's logit t (base 2)
+// gives p' = 2^(t - b), sums l = sum p', and the weight p' s_v. b is set so that the largest
+// weight met is 2^7, whatever share of that is the value's size (a key that takes nearly all of l
+// may have a value of next to nothing), and stays until a weight passes 2^15; then b moves and
+// what was summed is scaled. So weights down to 2^-21 of the largest are normal fp16 numbers, and
+// most tiles only compare. l may be far above 1; 2^100 bounds what one key adds.
 #include "kv_common.h"
 
 namespace convrot {
@@ -18,7 +25,10 @@ using namespace kv;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kTile = 64;          // keys a wave takes at a time
+constexpr float kTop = 7.0f;        // log2 of the largest weight when b is set
+constexpr float kMost = 32768.0f;   // weights above this move b
+constexpr float kMostExp = 100.0f;  // and so does p' above 2 to this
+constexpr float kNoRef = -3.0e38f;  // b of a row that has met no key
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // query rows of a tile: (token, head of the group) pairs
 
@@ -59,6 +69,12 @@ __device__ __forceinline__ void bytes_f16(uint32_t x, uint32_t (&h)[2]) {
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const f16x2 h = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
   return __builtin_bit_cast(uint32_t, h);
+}
+
+// What the fp16 pair `h` leaves of (a, b), as fp16.
+__device__ __forceinline__ uint32_t rest_f16(uint32_t h, float a, float b) {
+  const f16x2 f = __builtin_bit_cast(f16x2, h);
+  return pack_f16(a - static_cast<float>(f[0]), b - static_cast<float>(f[1]));
 }
 
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -103,14 +119,6 @@ __device__ __forceinline__ void key_range(const KvAttentionArgs& a, const Seq& s
   }
 }
 
-// Where the codes of a tile's 16-token steps lie. A page index outside the cache masks its tokens
-// (they load from page 0).
-struct Step {
-  const uint8_t* block;   // the (page, head) block
-  int off;                // the step's first token in its page
-  bool ok;
-};
-
 template <int D, int BITS>
 struct Geometry {
   using R = Row<D, BITS>;
@@ -122,13 +130,32 @@ struct Geometry {
   static constexpr int kTilesD = D / 16;                                     // 16-wide tiles of the output
 };
 
-template <int D, int BITS>
+// A tile of keys as a wave holds it: STEPS times 16 tokens.
+template <int D, int BITS, int STEPS>
 struct Tile {
   using G = Geometry<D, BITS>;
-  uint32_t k[4][G::kLoads][G::kWords], v[4][G::kLoads][G::kWords];
-  f32x4 ks[4], vs[4];
+  uint32_t k[STEPS][G::kLoads][G::kWords], v[STEPS][G::kLoads][G::kWords];
+  f32x4 ks[STEPS], vs[STEPS];
   uint32_t ok;   // bit j: step j's page is in the cache
 };
+
+// Page table entries of a tile's steps, read through the scalar cache. Steps past the table's end
+// take its last entry (their tokens are masked: they lie behind kv_len).
+template <int STEPS>
+struct Pages {
+  int at[STEPS];
+};
+typedef const __attribute__((address_space(4))) int32_t* ConstTable;
+template <int STEPS>
+__device__ __forceinline__ Pages<STEPS> tile_pages(const KvAttentionArgs& a, ConstTable table, int tile) {
+  Pages<STEPS> p;
+#pragma unroll
+  for (int j = 0; j < STEPS; j++) {
+    const int at = (tile * STEPS + j) * 16 >> a.lps;
+    p.at[j] = table[at < a.max_pages ? at : a.max_pages - 1];
+  }
+  return p;
+}
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -143,37 +170,36 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// The codes and scales of keys [64 tile, 64 tile + 64) of sequence b. Lane (r, g) = (lane % 16,
-// lane / 16) loads, of each 16-token step, token r's K bytes (chunk g of every 4 * kLoad) and of
-// the four tokens 4g .. 4g+3 the V columns kLoad/4 * r ..: each load instruction of the wave reads
-// 64 * kLoad contiguous bytes. Steps past the last page entry re-read the table's last entry.
-template <int D, int BITS>
-__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const int32_t* table, int head, int last_page,
-                                          int tile, int r, int g, Tile<D, BITS>& t) {
+// The codes and scales of a tile. Lane (r, g) = (lane % 16, lane / 16) loads, of each 16-token
+// step, token r's K bytes (chunk g of every 4 * kLoad) and of the four tokens 4g .. 4g+3 the V
+// columns kLoad / 4 * r ..: each load instruction of the wave reads 64 * kLoad contiguous bytes,
+// and what arrives is the matrix operand but for the conversion: no exchange between lanes. A page
+// index outside the cache loads from page 0; its tokens are masked.
+template <int D, int BITS, int STEPS>
+__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const Pages<STEPS>& pages, int head, int tile,
+                                          int r, int g, Tile<D, BITS, STEPS>& t) {
   using G = Geometry<D, BITS>;
   using R = Row<D, BITS>;
   const int page = 1 << a.lps;
+  const uint32_t k_lane = r * R::kBytes + g * G::kLoad, v_lane = g * (4 * R::kBytes) + r * G::kLoad, s_lane = g * 16;
   t.ok = 0;
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int tok = tile * kTile + 16 * j;
-    int at = tok >> a.lps;
-    at = at > last_page ? last_page : at;
-    const int pg = __builtin_amdgcn_readfirstlane(table[at]);
+  for (int j = 0; j < STEPS; j++) {
+    const int pg = pages.at[j];
     const bool ok = pg >= 0 && pg < a.num_pages;
-    if (ok) t.ok |= 1u << j;
+    t.ok |= ok ? 1u << j : 0u;
     const uint8_t* block = a.cache + ((int64_t)(ok ? pg : 0) * a.heads + head) * a.head_bytes;
-    const int off = tok & (page - 1);
-    const uint8_t* kp = block + off * R::kBytes + r * R::kBytes + g * G::kLoad;
-    const uint8_t* vp = block + page * R::kBytes + off * R::kBytes + g * (4 * R::kBytes) + r * G::kLoad;
+    const int off = (tile * STEPS + j) * 16 & (page - 1);
+    // One scalar base a step, 32-bit lane offsets.
+    const uint32_t kp = off * R::kBytes + k_lane, vp = (page + off) * R::kBytes + v_lane;
+    const uint32_t sp = 2 * page * R::kBytes + off * 4 + s_lane;
 #pragma unroll
     for (int l = 0; l < G::kLoads; l++) {
-      load_words(kp + l * 4 * G::kLoad, t.k[j][l]);
-      load_words(vp + l * 16 * G::kLoad, t.v[j][l]);
+      load_words(block + (kp + l * 4 * G::kLoad), t.k[j][l]);
+      load_words(block + (vp + l * 16 * G::kLoad), t.v[j][l]);
     }
-    const float* sp = reinterpret_cast<const float*>(block + 2 * page * R::kBytes) + off + 4 * g;
-    t.ks[j] = *reinterpret_cast<const f32x4*>(sp);
-    t.vs[j] = *reinterpret_cast<const f32x4*>(sp + page);
+    t.ks[j] = *reinterpret_cast<const f32x4*>(block + sp);
+    t.vs[j] = *reinterpret_cast<const f32x4*>(block + (sp + page * 4));
   }
 }
 
@@ -203,21 +229,25 @@ template <int D, int BITS>
 struct State {
   using G = Geometry<D, BITS>;
   f32x4 o[G::kTilesD];
-  float m;      // largest logit so far, before the row's factor c
-  float l;      // this lane's part of sum 2^(c (t - m))
-  float vref;   // the power of two that the weights are scaled by (the same in every lane)
+  float b;   // the row's reference
+  float l;   // this lane's part of the row's sum of p'
 };
 
-constexpr float kWeightTop = 32768.0f;   // weights stay at or below 2^15
-
-template <int D, int BITS, bool SPLIT, bool FULL>
-__device__ __forceinline__ void attend_tile(const Tile<D, BITS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
-                                            float c, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
-  using G = Geometry<D, BITS>;
-  float w[4][4], vs[4][4];
-  float top = neg_inf(), vtop = 0.0f;
+template <int D, int BITS>
+__device__ __forceinline__ void start(State<D, BITS>& s) {
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
+  for (int m = 0; m < D / 16; m++) s.o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  s.b = kNoRef;
+  s.l = 0.0f;
+}
+
+template <int D, int BITS, int STEPS, bool SPLIT>
+__device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
+                                            float c, bool full, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
+  using G = Geometry<D, BITS>;
+  float x[STEPS][4], p[STEPS][4], w[STEPS][4];
+#pragma unroll
+  for (int j = 0; j < STEPS; j++) {
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int op = 0; op < G::kOps; op++) {
@@ -236,68 +266,96 @@ __device__ __forceinline__ void attend_tile(const Tile<D, BITS>& t, const u32x4 
       acc = mfma(kop, q[op], acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float x = acc[i] * t.ks[j][i], y = t.vs[j][i];
-      if constexpr (!FULL) {
+    for (int i = 0; i < 4; i++) x[j][i] = acc[i] * t.ks[j][i];
+  }
+  if (!full) {   // the same in every lane
+#pragma unroll
+    for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
         const int key = first + 16 * j + i;   // `first` includes 4 g
-        const bool there = key < kv_len && (t.ok >> j & 1u);
-        if (!(there && key >= lo && key < hi)) x = neg_inf();
-        if (!there) y = 0.0f;
+        const int end = t.ok >> j & 1u ? kv_len : 0, own = hi < end ? hi : end;
+        x[j][i] = static_cast<uint32_t>(key - lo) < static_cast<uint32_t>(own > lo ? own - lo : 0) ? x[j][i] : neg_inf();
+        t.vs[j][i] = key < end ? t.vs[j][i] : 0.0f;
       }
-      w[j][i] = x;
-      vs[j][i] = y;
-      top = fmaxf(top, x);
-      vtop = fmaxf(vtop, y);
     }
   }
-  top = quad_max(top);
-  vtop = quad_max(vtop);
-  const float m_new = fmaxf(s.m, top);
-  const float mc = m_new == neg_inf() ? 0.0f : m_new * c;
-  float alpha = s.m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(s.m * c - mc);
-  s.m = m_new;
-  s.l *= alpha;
-  // The weights' scale grows with the largest value scale met.
-  if (vtop >= s.vref) {
-    const float grown = __uint_as_float((__float_as_uint(vtop) & 0x7F800000u) + 0x00800000u);
-    alpha *= s.vref / grown;
-    s.vref = grown;
+  auto weigh = [&](float& wtop) {
+    wtop = 0.0f;
+#pragma unroll
+    for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        p[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], c, -s.b));
+        w[j][i] = p[j][i] * t.vs[j][i];
+        wtop = fmaxf(wtop, w[j][i]);
+      }
+    }
+  };
+  float top = neg_inf(), wtop;
+#pragma unroll
+  for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) top = fmaxf(top, x[j][i]);
   }
-  if (__any(alpha != 1.0f)) {
+  weigh(wtop);
+  if (__any(wtop > kMost || top * c > s.b + kMostExp)) {
+    // The logarithm of the tile's largest weight, and its largest logit, over the row's four lanes.
+    float wl = neg_inf();
+#pragma unroll
+    for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        wl = fmaxf(wl, t.vs[j][i] > 0.0f ? __builtin_fmaf(x[j][i], c, __builtin_amdgcn_logf(t.vs[j][i])) : neg_inf());
+    }
+    wl = quad_max(wl);
+    top = quad_max(top) * c;
+    const bool moves = wl - s.b > 15.0f || top - s.b > kMostExp;
+    const float b = moves ? fmaxf(wl - kTop, top - kMostExp) : s.b;
+    const float alpha = __builtin_amdgcn_exp2f(s.b - b);   // 0 for a row that had no reference
+    s.b = b;
+    s.l *= alpha;
 #pragma unroll
     for (int m = 0; m < G::kTilesD; m++) s.o[m] *= alpha;
+    weigh(wtop);
   }
-  const float up = kWeightTop / s.vref;
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
+  for (int j = 0; j < STEPS; j++) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(w[j][i], c, -mc));
-      s.l += p;
-      w[j][i] = p * (vs[j][i] * up);
+    for (int i = 0; i < 4; i++) s.l += p[j][i];
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; j += 2) {
+    const u32x4 hi = {pack_f16(w[j][0], w[j][2]), pack_f16(w[j][1], w[j][3]),
+                      pack_f16(w[j + 1][0], w[j + 1][2]), pack_f16(w[j + 1][1], w[j + 1][3])};
+    u32x4 rest;
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        rest[2 * k] = rest_f16(hi[2 * k], w[j + k][0], w[j + k][2]);
+        rest[2 * k + 1] = rest_f16(hi[2 * k + 1], w[j + k][1], w[j + k][3]);
+      }
     }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    const u32x4 p = {pack_f16(w[j][0], w[j][2]), pack_f16(w[j][1], w[j][3]),
-                     pack_f16(w[j + 1][0], w[j + 1][2]), pack_f16(w[j + 1][1], w[j + 1][3])};
+    auto add = [&](int m, const u32x4& vop) {
+      if constexpr (SPLIT) s.o[m] = mfma(vop, rest, s.o[m]);
+      s.o[m] = mfma(vop, hi, s.o[m]);
+    };
 #pragma unroll
     for (int l = 0; l < G::kLoads; l++) {
 #pragma unroll
-      for (int x = 0; x < G::kWords; x++) {
+      for (int y = 0; y < G::kWords; y++) {
         if constexpr (BITS == 4) {
           uint32_t h0[4], h1[4];
-          nibbles_f16(t.v[j][l][x], h0);
-          nibbles_f16(t.v[j + 1][l][x], h1);
-          const int m = (l * G::kWords + x) * 2;
-          s.o[m] = mfma(u32x4{h0[0], h0[2], h1[0], h1[2]}, p, s.o[m]);
-          s.o[m + 1] = mfma(u32x4{h0[1], h0[3], h1[1], h1[3]}, p, s.o[m + 1]);
+          nibbles_f16(t.v[j][l][y], h0);
+          nibbles_f16(t.v[j + 1][l][y], h1);
+          const int m = (l * G::kWords + y) * 2;
+          add(m, u32x4{h0[0], h0[2], h1[0], h1[2]});
+          add(m + 1, u32x4{h0[1], h0[3], h1[1], h1[3]});
         } else {
           uint32_t h0[2], h1[2];
-          bytes_f16(t.v[j][l][x], h0);
-          bytes_f16(t.v[j + 1][l][x], h1);
-          const int m = l * G::kWords + x;
-          s.o[m] = mfma(u32x4{h0[0], h0[1], h1[0], h1[1]}, p, s.o[m]);
+          bytes_f16(t.v[j][l][y], h0);
+          bytes_f16(t.v[j + 1][l][y], h1);
+          add(l * G::kWords + y, u32x4{h0[0], h0[1], h1[0], h1[1]});
         }
       }
     }
@@ -318,25 +376,24 @@ __device__ __forceinline__ void store_row(uint8_t* p, int dt, float (&v)[Row<D, 
 }
 
 // One workgroup: a tile of 16 query rows of one key head and sequence, and one split of its keys.
-// The four waves take the split's 64-key tiles in turn, each with a softmax of its own; they are
+// The four waves take the split's tiles of keys in turn, each with a softmax of its own; they are
 // joined through LDS, and splits through the workspace (kv_join_kernel).
-template <int D, int BITS, bool SPLIT>
-__global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttentionArgs a) {
+template <int D, int BITS, int STEPS, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kernel(KvAttentionArgs a) {
   using R = Row<D, BITS>;
   using G = Geometry<D, BITS>;
-  constexpr int kOutPad = 4;
+  constexpr int kOutPad = 4, kTile = 16 * STEPS;
   __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows][D + kOutPad];
   __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows], lds_c[kRows];
   uint32_t* lds_q = reinterpret_cast<uint32_t*>(lds_o);   // [2][kRows][D / 2], before the first key
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.splits;
   const int head = blockIdx.x / a.splits % a.heads;
   const int b = blockIdx.y;
   const Seq s = sequence(a, b);
   const int rows = s.q_len * a.group;   // q_len < 2^31 / group is checked on the host
-  const int32_t* table = a.pages + (int64_t)b * a.max_pages;
-  const int last_page = a.max_pages - 1;
+  const ConstTable table = (ConstTable)(uintptr_t)(a.pages + (int64_t)b * a.max_pages);
 
   for (int tile = blockIdx.x / (a.splits * a.heads); tile * kRows < rows; tile += a.row_tiles) {
     // Queries: rotated, scaled, to fp16, in the K operands' element order.
@@ -401,14 +458,13 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttentionArgs 
 
     // Keys of this tile's rows, and of this lane's row.
     const int row_first = tile * kRows, row_last = (row_first + kRows < rows ? row_first + kRows : rows) - 1;
-    int lo, hi, t_lo, t_hi, x;
+    int lo, hi, t_lo, t_hi;
     const bool mine = row_first + r < rows;
     key_range(a, s, (mine ? row_first + r : row_first) / a.group, lo, hi);
     if (!mine) hi = lo = 0;
     int full_lo, full_hi;   // every row attends to [full_lo, full_hi)
     key_range(a, s, row_first / a.group, t_lo, full_hi);
     key_range(a, s, row_last / a.group, full_lo, t_hi);
-    (void)x;
     const bool whole = row_last - row_first == kRows - 1;
     const int tiles_lo = t_lo / kTile, tiles_hi = (t_hi + kTile - 1) / kTile;
     const int count = tiles_hi > tiles_lo ? tiles_hi - tiles_lo : 0;
@@ -416,26 +472,45 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttentionArgs 
     const int end = tiles_lo + static_cast<int>((int64_t)count * (split + 1) / a.splits);
 
     State<D, BITS> st;
-#pragma unroll
-    for (int m = 0; m < G::kTilesD; m++) st.o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    st.m = neg_inf();
-    st.l = 0.0f;
-    st.vref = 0x1p-110f;
-    for (int i = begin + wave; i < end; i += kWaves) {
-      Tile<D, BITS> t;
-      load_tile<D, BITS>(a, table, head, last_page, i, r, g, t);
-      const int first = i * kTile;
-      const bool full = whole && t.ok == 15u && first >= full_lo && first + kTile <= full_hi;
-      if (full)
-        attend_tile<D, BITS, SPLIT, true>(t, q, q2, c, first + 4 * g, lo, hi, s.kv_len, st);
-      else
-        attend_tile<D, BITS, SPLIT, false>(t, q, q2, c, first + 4 * g, lo, hi, s.kv_len, st);
+    start(st);
+    int i = begin + wave;
+    if (i < end) {
+      // One tile is in flight while the other is worked on, and the page entries of the one after.
+      // Past the end the last tile is loaded again: loads under a condition would have to be waited
+      // for as soon as they are issued.
+      Tile<D, BITS, STEPS> t0, t1;
+      auto next = [&](int at) { return at + kWaves < end ? at + kWaves : at; };
+      auto attend = [&](Tile<D, BITS, STEPS>& t, int at) {
+        const int first = at * kTile;
+        const bool full = whole && t.ok == (1u << STEPS) - 1 && first >= full_lo && first + kTile <= full_hi;
+        attend_tile<D, BITS, STEPS, SPLIT>(t, q, q2, c, full, first + 4 * g, lo, hi, s.kv_len, st);
+      };
+      Pages<STEPS> pages = tile_pages<STEPS>(a, table, i);
+      load_tile<D, BITS, STEPS>(a, pages, head, i, r, g, t0);
+      int n = next(i);
+      pages = tile_pages<STEPS>(a, table, n);
+      while (true) {
+        load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t1);
+        int m = next(n);
+        pages = tile_pages<STEPS>(a, table, m);
+        attend(t0, i);
+        if (n == i) break;
+        i = n;
+        n = m;
+        load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t0);
+        m = next(n);
+        pages = tile_pages<STEPS>(a, table, m);
+        attend(t1, i);
+        if (n == i) break;
+        i = n;
+        n = m;
+      }
     }
 
     // Join the waves.
     st.l = quad_sum(st.l);
     if (g == 0) {
-      lds_m[wave][r] = st.m == neg_inf() ? neg_inf() : st.m * c;
+      lds_m[wave][r] = st.l > 0.0f ? st.b : neg_inf();
       lds_l[wave][r] = st.l;
     }
     __syncthreads();
@@ -444,7 +519,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttentionArgs 
     for (int w = 1; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
     {
       const float m = lds_m[wave][r];
-      const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top) * (st.vref / kWeightTop);
+      const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
       for (int m16 = 0; m16 < G::kTilesD; m16++) {
 #pragma unroll
@@ -546,10 +621,11 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
 template <int D, int BITS>
 hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.splits * a.heads * a.row_tiles), static_cast<unsigned>(a.seqs));
+  constexpr int kSteps = D * BITS <= 256 ? 4 : 2;
   if (a.dt == kF16)
-    kv_attend_kernel<D, BITS, true><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, kSteps, true><<<grid, kWaves * 64, 0, stream>>>(a);
   else
-    kv_attend_kernel<D, BITS, false><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, kSteps, false><<<grid, kWaves * 64, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   constexpr int kPer = 256 / Row<D, BITS>::kLanes;
@@ -570,7 +646,7 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
   int64_t span = max_kv_len;
   if (window > 0 && window + max_q_len < span) span = window + max_q_len;
   const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = (1024 + groups - 1) / groups;
-  const int64_t most = (span + kTile - 1) / kTile / (2 * kWaves);
+  const int64_t most = (span + 63) / 64 / (2 * kWaves);
   int64_t splits = want < most ? want : most;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
   p.workspace_bytes = p.splits > 1 ? (size_t)total_q * q_heads * p.splits * (head_dim + 2) * 4 : 0;
