@@ -318,9 +318,11 @@ typedef struct {
   const int32_t *pages;      /* [seqs, max_pages] device */
   int64_t total_q;
   int64_t q_token_stride, q_head_stride, o_token_stride, o_head_stride;   /* elements */
-  int64_t max_q_len;         /* the most query rows of a sequence, the most cached tokens of one: */
-  int64_t max_kv_len;        /*   they choose how the work is split; results hold for other lengths
-                                too. 0 or less: total_q, max_pages * page_size. */
+  int64_t max_q_len;         /* the most query rows of a sequence; 0 or less: total_q. A longer
+                                sequence's rows beyond it are left as they were. Without q_start
+                                it is not looked at */
+  int64_t max_kv_len;        /* the most cached tokens of a sequence, to split the work by; results
+                                hold for any length. 0 or less: max_pages * page_size */
   int32_t dtype;             /* RQ_F16 or RQ_BF16: of Q and O */
   int32_t q_heads;           /* a multiple of kv_heads */
   int32_t seqs, max_pages;   /* seqs <= 65535; max_pages * page_size <= 2^30 */

@@ -187,8 +187,26 @@ def test_ragged_chunks(page, group, causal, window):
     rng, c, cfg = make(128, 4, page, heads=2, pages=1536 // page)
     pages = fill(rng, c, kv_len)
     Q = rng.normal(size=(sum(q_len) + 5, 2 * group, 128))
-    for kw in ({}, dict(max_q_len=max(q_len), max_kv_len=max(kv_len)), dict(max_q_len=1, max_kv_len=1)):
+    for kw in ({}, dict(max_q_len=max(q_len), max_kv_len=max(kv_len)), dict(max_kv_len=1)):
         check(c, cfg, Q, pages, kv_len, q_len, "bf16", causal, window, before=2, after=3, **kw)
+
+
+@pytest.mark.parametrize("kv", [100, 5000])
+def test_rows_beyond_max_q_len_are_left(kv):
+    rng, c, cfg = make(64, 4, 16, heads=1, pages=700)
+    q_len, kv_len = [9, 2, 70], [kv, 60, kv]
+    pages = torch.from_numpy(fill(rng, c, kv_len)).cuda()
+    n, starts = torch.tensor(kv_len, dtype=torch.int32).cuda(), torch.tensor([0, 9, 11, 81], dtype=torch.int32).cuda()
+    Q = torch.randn(81, 3, 64, device="cuda").half()
+    dev = c.flat().cuda()
+    for most in (1, 5, 9, 69):
+        out = torch.full_like(Q, 3.0)
+        rq.kv_attention(Q, dev, pages, n, cfg, q_start=starts, max_q_len=most, out=out)
+        whole = rq.kv_attention(Q, dev, pages, n, cfg, q_start=starts)
+        for a, b in ((0, 9), (9, 11), (11, 81)):
+            e = min(b, a + most)
+            assert torch.all(out[e:b] == 3.0)
+            assert torch.all((out[a:e] - whole[a:e]).abs() <= 1e-3 * whole.abs().max())     # the split may differ
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])

@@ -548,9 +548,10 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
 
     pages [seqs, max_pages], kv_len [seqs] and q_start [seqs + 1] are int32 device tensors; without
     q_start every sequence has total_q / seqs query rows. softmax_scale defaults to
-    head_dim ** -0.5. max_q_len and max_kv_len (host numbers) choose how the work is split; they
-    default to what the shapes allow, and results hold for other lengths too. workspace: a uint8
-    tensor of kv_attention_workspace_size() bytes or more. See rq_kv_attention in convrot.h."""
+    head_dim ** -0.5. max_q_len (host number): the most query rows of a sequence, rows beyond it are
+    left as they were; max_kv_len: the most cached tokens of one, to split the work by. They
+    default to what the shapes allow; a ragged batch is faster with them. workspace: a uint8 tensor
+    of kv_attention_workspace_size() bytes or more. See rq_kv_attention in convrot.h."""
     torch = _torch()
     num_pages = _kv_cache(cache, cfg)
     shape = Q.shape

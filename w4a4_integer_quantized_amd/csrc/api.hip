@@ -405,7 +405,8 @@ rq_status check_kv_shape(const rq_kv_attention_params* p, const rq_kv_config* cf
 }
 
 rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache,
-                             int64_t num_pages, const void* ws, size_t ws_bytes, convrot::KvAttentionPlan* plan) {
+                             int64_t num_pages, const void* ws, size_t ws_bytes, convrot::KvAttentionPlan* plan,
+                             int64_t* max_q_len) {
   int64_t max_q = 0, max_kv = 0;
   rq_status s = check_kv_shape(p, cfg, &max_q, &max_kv);
   if (s) return s;
@@ -421,6 +422,7 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
   for (const void* w : words)
     if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
       return fail(RQ_EINVAL, "kv_len, pages, q_start or lse is not 4-byte aligned");
+  *max_q_len = max_q;
   *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
                                      p->window);
   const int64_t need = (int64_t)plan->workspace_bytes;
@@ -619,7 +621,8 @@ size_t rq_kv_attention_workspace_size(const rq_kv_attention_params* p, const rq_
 rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache, int64_t num_pages,
                           void* workspace, size_t ws_bytes, void* stream) {
   convrot::KvAttentionPlan plan = {};
-  rq_status s = check_kv_attention(p, cfg, cache, num_pages, workspace, ws_bytes, &plan);
+  int64_t max_q = 0;
+  rq_status s = check_kv_attention(p, cfg, cache, num_pages, workspace, ws_bytes, &plan, &max_q);
   if (s || p->total_q == 0) return s;
   convrot::KvAttentionArgs a = {};
   a.cache = static_cast<const uint8_t*>(cache);
@@ -642,6 +645,9 @@ rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* c
   a.q_heads = p->q_heads;
   a.heads = cfg->kv_heads;
   a.group = p->q_heads / cfg->kv_heads;
+  a.even_q = p->q_start ? 0 : static_cast<int>(p->total_q / p->seqs);
+  a.group_shift = log2_of(a.group);
+  a.group_mul = static_cast<uint32_t>((((uint64_t)1 << 32) * (((uint64_t)1 << a.group_shift) - a.group)) / a.group + 1);
   a.max_pages = p->max_pages;
   a.lps = log2_of(cfg->page_size);
   a.dt = p->dtype;
@@ -649,6 +655,8 @@ rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* c
   a.window = p->window;
   a.splits = plan.splits;
   a.row_tiles = plan.row_tiles;
+  a.chunk = plan.chunk;
+  a.max_q = static_cast<int>(max_q);
   a.scale = p->softmax_scale;
   return from_hip(convrot::launch_kv_attention(a, cfg->head_dim, cfg->bits, static_cast<hipStream_t>(stream)),
                   "kv_attention launch");

@@ -15,7 +15,7 @@
 // weight met is 2^7, whatever share of that is the value's size (a key that takes nearly all of l
 // may have a value of next to nothing), and stays until a weight passes 2^15; then b moves and
 // what was summed is scaled. So weights down to 2^-21 of the largest are normal fp16 numbers, and
-// most tiles only compare. l may be far above 1; 2^100 bounds what one key adds.
+// most tiles only compare. l may be far above 1.
 #include "kv_common.h"
 
 namespace convrot {
@@ -27,8 +27,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTop = 7.0f;        // log2 of the largest weight when b is set
 constexpr float kMost = 32768.0f;   // weights above this move b
-constexpr float kMostExp = 100.0f;  // and so does p' above 2 to this
+constexpr float kMostExp = 90.0f;   // log2 of the p' that a moved b allows, and the sum that
+constexpr float kMostSum = 0x1p120f;   // moves it
 constexpr float kNoRef = -3.0e38f;  // b of a row that has met no key
+constexpr int kMinChunk = 1024;     // keys
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // query rows of a tile: (token, head of the group) pairs
 
@@ -81,31 +83,54 @@ __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+typedef const __attribute__((address_space(4))) int32_t* ConstTable;   // read through the scalar cache
+__device__ __forceinline__ ConstTable const_table(const int32_t* p) { return (ConstTable)(uintptr_t)p; }
+
+// Row n of a sequence's (token, head of the group) rows, n < 2^31: its token.
+__device__ __forceinline__ int token_of(const KvAttentionArgs& a, int n) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), a.group_mul) + static_cast<uint32_t>(n)) >> a.group_shift);
+}
+
 // A sequence's rows and keys as the device sees them, whatever the tables hold: rows lie in
 // [0, total_q), keys in the sequence's page table.
 struct Seq {
-  int64_t q0;
-  int q_len, kv_len;
+  int q0, q_len, kv_len;
 };
+__device__ __forceinline__ int clamp(int x, int most) { return x < 0 ? 0 : x > most ? most : x; }
 __device__ __forceinline__ Seq sequence(const KvAttentionArgs& a, int b) {
   Seq s;
-  int64_t q0, q1;
+  const int total = static_cast<int>(a.total_q);
   if (a.q_start) {
-    q0 = a.q_start[b];
-    q1 = a.q_start[b + 1];
-    q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
-    q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
+    const ConstTable t = const_table(a.q_start);
+    s.q0 = clamp(t[b], total);
+    const int q1 = clamp(t[b + 1], total);
+    s.q_len = q1 < s.q0 ? 0 : q1 - s.q0;
   } else {
-    const int64_t n = a.total_q / a.seqs;
-    q0 = b * n;
-    q1 = q0 + n;
+    s.q0 = b * a.even_q;
+    s.q_len = a.even_q;
   }
-  s.q0 = q0;
-  s.q_len = static_cast<int>(q1 - q0);
-  const int64_t most = (int64_t)a.max_pages << a.lps;
-  const int64_t kv = a.kv_len[b];
-  s.kv_len = static_cast<int>(kv < 0 ? 0 : kv > most ? most : kv);
+  s.kv_len = clamp(const_table(a.kv_len)[b], a.max_pages << a.lps);
   return s;
+}
+
+// A workgroup's work. Workgroups go to the 8 XCDs in turn; a page's heads lie side by side in
+// memory, and heads that walk the same pages at the same time on one XCD share its address
+// translations. So the (sequence, split) pairs are dealt to the XCDs and a pair's heads (and row
+// tiles) follow each other on its XCD. A short sequence's work lies in its first splits: from
+// sequence to sequence the splits are turned by one, or some XCDs would have all of it.
+struct Place {
+  int split, head, tile, seq;   // seq >= a.seqs: nothing (pairs are padded to whole turns)
+};
+constexpr uint32_t kXcds = 8;
+__device__ __forceinline__ Place place(const KvAttentionArgs& a) {
+  const uint32_t inner = (uint32_t)a.heads * a.row_tiles, turn = blockIdx.x / kXcds;
+  const uint32_t pair = turn / inner * kXcds + blockIdx.x % kXcds, in = turn % inner;
+  Place p;
+  p.tile = a.row_tiles == 1 ? 0 : in / a.heads;
+  p.head = in - p.tile * a.heads;
+  p.seq = a.splits == 1 ? pair : pair / a.splits;
+  p.split = a.splits == 1 ? 0 : (pair - p.seq * a.splits + p.seq) % a.splits;
+  return p;
 }
 
 // The keys [lo, hi) that row r of a sequence attends to.
@@ -135,9 +160,23 @@ template <int D, int BITS, int STEPS>
 struct Tile {
   using G = Geometry<D, BITS>;
   uint32_t k[STEPS][G::kLoads][G::kWords], v[STEPS][G::kLoads][G::kWords];
-  f32x4 ks[STEPS], vs[STEPS];
-  uint32_t ok;   // bit j: step j's page is in the cache
+  float ks, vs;   // scales, spread over a row of 16 lanes: of token 16 (r / 4) + 4 g + r % 4
+  uint32_t ok;    // bit j: step j's page is in the cache
 };
+
+// The value that lane N of the lane's row of 16 holds (an operand modifier, no instruction).
+template <int N>
+__device__ __forceinline__ float row_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x150 + N, 0xF, 0xF, true));
+}
+// a[j][i] = b[j][i] times the scale of step j's token 4g + i.
+template <int STEPS, int N = 0>
+__device__ __forceinline__ void times_scale(float (&a)[STEPS][4], const float (&b)[STEPS][4], float scale) {
+  if constexpr (N < 4 * STEPS) {
+    a[N / 4][N % 4] = row_lane<N>(scale) * b[N / 4][N % 4];
+    times_scale<STEPS, N + 1>(a, b, scale);
+  }
+}
 
 // Page table entries of a tile's steps, read through the scalar cache. Steps past the table's end
 // take its last entry (their tokens are masked: they lie behind kv_len).
@@ -145,7 +184,6 @@ template <int STEPS>
 struct Pages {
   int at[STEPS];
 };
-typedef const __attribute__((address_space(4))) int32_t* ConstTable;
 template <int STEPS>
 __device__ __forceinline__ Pages<STEPS> tile_pages(const KvAttentionArgs& a, ConstTable table, int tile) {
   Pages<STEPS> p;
@@ -181,7 +219,9 @@ __device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const Pages<
   using G = Geometry<D, BITS>;
   using R = Row<D, BITS>;
   const int page = 1 << a.lps;
-  const uint32_t k_lane = r * R::kBytes + g * G::kLoad, v_lane = g * (4 * R::kBytes) + r * G::kLoad, s_lane = g * 16;
+  const uint32_t k_lane = r * R::kBytes + g * G::kLoad, v_lane = g * (4 * R::kBytes) + r * G::kLoad;
+  const int s_step = r >> 2 < STEPS ? r >> 2 : 0;   // with fewer than four steps some lanes repeat
+  const uint8_t* s_at = nullptr;
   t.ok = 0;
 #pragma unroll
   for (int j = 0; j < STEPS; j++) {
@@ -192,15 +232,17 @@ __device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const Pages<
     const int off = (tile * STEPS + j) * 16 & (page - 1);
     // One scalar base a step, 32-bit lane offsets.
     const uint32_t kp = off * R::kBytes + k_lane, vp = (page + off) * R::kBytes + v_lane;
-    const uint32_t sp = 2 * page * R::kBytes + off * 4 + s_lane;
+    const uint8_t* sp = block + (2 * page * R::kBytes + off * 4);
+    s_at = j == 0 || s_step == j ? sp : s_at;
 #pragma unroll
     for (int l = 0; l < G::kLoads; l++) {
       load_words(block + (kp + l * 4 * G::kLoad), t.k[j][l]);
       load_words(block + (vp + l * 16 * G::kLoad), t.v[j][l]);
     }
-    t.ks[j] = *reinterpret_cast<const f32x4*>(block + sp);
-    t.vs[j] = *reinterpret_cast<const f32x4*>(block + (sp + page * 4));
   }
+  const uint32_t token = 4 * g + (r & 3);
+  t.ks = *reinterpret_cast<const float*>(s_at + token * 4);
+  t.vs = *reinterpret_cast<const float*>(s_at + (page + token) * 4);
 }
 
 // The 8-element chunk of a row that K operand `op` of lane group g holds.
@@ -243,7 +285,7 @@ __device__ __forceinline__ void start(State<D, BITS>& s) {
 
 template <int D, int BITS, int STEPS, bool SPLIT>
 __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
-                                            float c, bool full, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
+                                            float c, bool full, int r, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
   using G = Geometry<D, BITS>;
   float x[STEPS][4], p[STEPS][4], w[STEPS][4];
 #pragma unroll
@@ -266,47 +308,62 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
       acc = mfma(kop, q[op], acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) x[j][i] = acc[i] * t.ks[j][i];
+    for (int i = 0; i < 4; i++) x[j][i] = acc[i];
   }
+  times_scale<STEPS>(x, x, t.ks);
   if (!full) {   // the same in every lane
+    const int mine = first + 16 * (r >> 2) + (r & 3);   // `first` includes 4 g
+    const uint32_t step = r >> 2 < STEPS ? r >> 2 : 0;
+    t.vs = mine < kv_len && (t.ok >> step & 1u) ? t.vs : 0.0f;
 #pragma unroll
     for (int j = 0; j < STEPS; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const int key = first + 16 * j + i;   // `first` includes 4 g
+        const int key = first + 16 * j + i;
         const int end = t.ok >> j & 1u ? kv_len : 0, own = hi < end ? hi : end;
         x[j][i] = static_cast<uint32_t>(key - lo) < static_cast<uint32_t>(own > lo ? own - lo : 0) ? x[j][i] : neg_inf();
-        t.vs[j][i] = key < end ? t.vs[j][i] : 0.0f;
       }
     }
   }
-  auto weigh = [&](float& wtop) {
-    wtop = 0.0f;
+  // Weights for the present b; true if they fit: none above kMost, and no p' so large that l might
+  // come near its range's end (a first key's is infinite: b is kNoRef).
+  float l;
+  auto weigh = [&]() {
+    float wtop = 0.0f;
+    l = s.l;
 #pragma unroll
     for (int j = 0; j < STEPS; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         p[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], c, -s.b));
-        w[j][i] = p[j][i] * t.vs[j][i];
-        wtop = fmaxf(wtop, w[j][i]);
+        l += p[j][i];
       }
     }
-  };
-  float top = neg_inf(), wtop;
-#pragma unroll
-  for (int j = 0; j < STEPS; j++) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) top = fmaxf(top, x[j][i]);
-  }
-  weigh(wtop);
-  if (__any(wtop > kMost || top * c > s.b + kMostExp)) {
-    // The logarithm of the tile's largest weight, and its largest logit, over the row's four lanes.
-    float wl = neg_inf();
+    times_scale<STEPS>(w, p, t.vs);
 #pragma unroll
     for (int j = 0; j < STEPS; j++) {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        wl = fmaxf(wl, t.vs[j][i] > 0.0f ? __builtin_fmaf(x[j][i], c, __builtin_amdgcn_logf(t.vs[j][i])) : neg_inf());
+      for (int i = 0; i < 4; i++) wtop = fmaxf(wtop, w[j][i]);
+    }
+    return wtop <= kMost && l < kMostSum;
+  };
+  if (!__all(weigh())) {
+    // The logarithm of the tile's largest weight, and its largest logit, over the row's four lanes.
+    const float lv = t.vs > 0.0f ? __builtin_amdgcn_logf(t.vs) : neg_inf();
+    float one[STEPS][4], wl = neg_inf(), top = neg_inf();
+#pragma unroll
+    for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) one[j][i] = 1.0f;
+    }
+    times_scale<STEPS>(p, one, lv);
+#pragma unroll
+    for (int j = 0; j < STEPS; j++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        top = fmaxf(top, x[j][i]);
+        wl = fmaxf(wl, __builtin_fmaf(x[j][i], c, p[j][i]));
+      }
     }
     wl = quad_max(wl);
     top = quad_max(top) * c;
@@ -317,13 +374,9 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
     s.l *= alpha;
 #pragma unroll
     for (int m = 0; m < G::kTilesD; m++) s.o[m] *= alpha;
-    weigh(wtop);
+    weigh();
   }
-#pragma unroll
-  for (int j = 0; j < STEPS; j++) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) s.l += p[j][i];
-  }
+  s.l = l;
 #pragma unroll
   for (int j = 0; j < STEPS; j += 2) {
     const u32x4 hi = {pack_f16(w[j][0], w[j][2]), pack_f16(w[j][1], w[j][3]),
@@ -388,217 +441,234 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
   uint32_t* lds_q = reinterpret_cast<uint32_t*>(lds_o);   // [2][kRows][D / 2], before the first key
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.splits;
-  const int head = blockIdx.x / a.splits % a.heads;
-  const int b = blockIdx.y;
+  const Place at = place(a);
+  if (at.seq >= a.seqs) return;
+  const int split = at.split, head = at.head, b = at.seq;
   const Seq s = sequence(a, b);
-  const int rows = s.q_len * a.group;   // q_len < 2^31 / group is checked on the host
-  const ConstTable table = (ConstTable)(uintptr_t)(a.pages + (int64_t)b * a.max_pages);
+  const int rows = (s.q_len < a.max_q ? s.q_len : a.max_q) * a.group;   // at most 2^30: checked on the host
+  const ConstTable table = const_table(a.pages + (int64_t)b * a.max_pages);
 
-  for (int tile = blockIdx.x / (a.splits * a.heads); tile * kRows < rows; tile += a.row_tiles) {
-    // Queries: rotated, scaled, to fp16, in the K operands' element order.
-    {
-      const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
-      const int at = tile * kRows + row;
-      const bool ok = row < kRows && at < rows;
-      const int token = ok ? at / a.group : 0, qh = head * a.group + (ok ? at % a.group : 0);
-      const uint8_t* x = a.q + ((s.q0 + token) * a.q_token + qh * a.q_head) * 2;
-      float v[R::kChunks][8], sign = 1.0f, top = 0.0f;
+  const int tile = at.tile;
+  if (tile * kRows >= rows) return;
+  // Keys of this tile's rows, and of this lane's row.
+  const int row_first = tile * kRows, row_last = (row_first + kRows < rows ? row_first + kRows : rows) - 1;
+  int lo, hi, t_lo, t_hi;
+  const bool mine = row_first + r < rows;
+  key_range(a, s, token_of(a, mine ? row_first + r : row_first), lo, hi);
+  if (!mine) hi = lo = 0;
+  int full_lo, full_hi;   // every row attends to [full_lo, full_hi)
+  key_range(a, s, token_of(a, row_first), t_lo, full_hi);
+  key_range(a, s, token_of(a, row_last), full_lo, t_hi);
+  const bool whole = row_last - row_first == kRows - 1;
+  const int tiles_lo = t_lo / kTile, tiles_hi = (t_hi + kTile - 1) / kTile;
+  const int count = tiles_hi > tiles_lo ? tiles_hi - tiles_lo : 0;
+  const int share = (count + a.splits - 1) / a.splits, chunk = share > a.chunk / kTile ? share : a.chunk / kTile;
+  const int begin = tiles_lo + (split * (int64_t)chunk < count ? split * chunk : count);
+  const int end = tiles_lo + (count - (begin - tiles_lo) < chunk ? count : begin - tiles_lo + chunk);
+  if (begin >= end) {   // no keys
+    const int n = row_first + threadIdx.x / kRows, token = token_of(a, n), qh = head * a.group + n - token * a.group;
+    if (n <= row_last) {   // 16 threads a row
+      const int64_t out_row = (int64_t)(s.q0 + token) * a.q_heads + qh;
+      if (a.splits > 1) {   // all that the join needs to know
+        if (r == 0) a.part_stat[(out_row * a.splits + split) * 2] = neg_inf();
+      } else {
+        uint8_t* p = a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2;
+        for (int d = r * 8; d < D; d += 128) *reinterpret_cast<u32x4*>(p + d * 2) = u32x4{0u, 0u, 0u, 0u};
+        if (r == 0 && a.lse) a.lse[out_row] = neg_inf();
+      }
+    }
+    return;
+  }
+  // One tile is in flight while the other is worked on, and the page entries of the one after.
+  // Past the end the last tile is loaded again: loads under a condition would have to be waited
+  // for as soon as they are issued. The first tile is under way before the queries are.
+  int i = begin + wave;
+  auto next = [&](int at) { return at + kWaves < end ? at + kWaves : at; };
+  // (A wave without tiles loads the last one too, and does not use it.)
+  Tile<D, BITS, STEPS> t0, t1;
+  Pages<STEPS> pages = tile_pages<STEPS>(a, table, i < end ? i : end - 1);
+  load_tile<D, BITS, STEPS>(a, pages, head, i < end ? i : end - 1, r, g, t0);
+  int n = next(i);
+  pages = tile_pages<STEPS>(a, table, n < end ? n : end - 1);
+  // Queries: rotated, scaled, to fp16, in the K operands' element order.
+  {
+    const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
+    const int n = tile * kRows + row;
+    const bool ok = row < kRows && n < rows;
+    const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
+    const uint8_t* x = a.q + ((s.q0 + token) * a.q_token + qh * a.q_head) * 2;
+    float v[R::kChunks][8], sign = 1.0f, top = 0.0f;
 #pragma unroll
-      for (int k = 0; k < R::kChunks; k++) load8(x + (k * 128 + chunk * 8) * 2, a.dt, v[k]);
+    for (int k = 0; k < R::kChunks; k++) load8(x + (k * 128 + chunk * 8) * 2, a.dt, v[k]);
+#pragma unroll
+    for (int k = 0; k < R::kChunks; k++) {
+      sign = wht_block<R::kLanes>(v[k], chunk);
+#pragma unroll
+      for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[k][i]));
+    }
+    top = row_max<R::kLanes>(top);
+    // 2^(8 - exponent): the largest element comes to lie in [256, 512). Rows of zeros, and
+    // largest elements below 2^-100, are scaled by 2^108.
+    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    e = e < -100 ? -100 : e;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+    if (row < kRows) {
 #pragma unroll
       for (int k = 0; k < R::kChunks; k++) {
-        sign = wht_block<R::kLanes>(v[k], chunk);
-#pragma unroll
-        for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[k][i]));
-      }
-      top = row_max<R::kLanes>(top);
-      // 2^(8 - exponent): the largest element comes to lie in [256, 512). Rows of zeros, and
-      // largest elements below 2^-100, are scaled by 2^108.
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      e = e < -100 ? -100 : e;
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
-      __syncthreads();   // the tile before has read the LDS
-      if (row < kRows) {
-#pragma unroll
-        for (int k = 0; k < R::kChunks; k++) {
-          float y[8];
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            y[i] = v[k][i] * (sign * up);
-            const _Float16 h = static_cast<_Float16>(y[i]);
-            hi[i] = __builtin_bit_cast(uint16_t, h);
-            lo[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(y[i] - static_cast<float>(h)));
-          }
-          // Pairs in the order in which nibbles_f16 / bytes_f16 give the codes.
-          constexpr int kA[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5};
-          constexpr int kB = BITS == 4 ? 4 : 2;
-          uint32_t* p = lds_q + row * (D / 2) + (k * 16 + chunk) * 4;
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            p[i] = hi[kA[i]] | (hi[kA[i] + kB] << 16);
-            if constexpr (SPLIT) p[kRows * (D / 2) + i] = lo[kA[i]] | (lo[kA[i] + kB] << 16);
-          }
-        }
-        // Logits in base 2 are t * c, t = sum of fp16 query times code, times the key's scale.
-        if (u == 0) lds_c[row] = a.scale * (kLog2e * R::kNorm) / up;
-      }
-      __syncthreads();
-    }
-    u32x4 q[G::kOps], q2[G::kOps];
-#pragma unroll
-    for (int op = 0; op < G::kOps; op++) {
-      const uint32_t* p = lds_q + r * (D / 2) + operand_chunk<D, BITS>(op, g) * 4;
-      q[op] = *reinterpret_cast<const u32x4*>(p);
-      q2[op] = SPLIT ? *reinterpret_cast<const u32x4*>(p + kRows * (D / 2)) : q[op];
-    }
-    const float c = fmaxf(lds_c[r], 1.1754944e-38f);   // a positive factor keeps masked logits at -inf
-    __syncthreads();   // lds_q is read: lds_o may be written
-
-    // Keys of this tile's rows, and of this lane's row.
-    const int row_first = tile * kRows, row_last = (row_first + kRows < rows ? row_first + kRows : rows) - 1;
-    int lo, hi, t_lo, t_hi;
-    const bool mine = row_first + r < rows;
-    key_range(a, s, (mine ? row_first + r : row_first) / a.group, lo, hi);
-    if (!mine) hi = lo = 0;
-    int full_lo, full_hi;   // every row attends to [full_lo, full_hi)
-    key_range(a, s, row_first / a.group, t_lo, full_hi);
-    key_range(a, s, row_last / a.group, full_lo, t_hi);
-    const bool whole = row_last - row_first == kRows - 1;
-    const int tiles_lo = t_lo / kTile, tiles_hi = (t_hi + kTile - 1) / kTile;
-    const int count = tiles_hi > tiles_lo ? tiles_hi - tiles_lo : 0;
-    const int begin = tiles_lo + static_cast<int>((int64_t)count * split / a.splits);
-    const int end = tiles_lo + static_cast<int>((int64_t)count * (split + 1) / a.splits);
-
-    State<D, BITS> st;
-    start(st);
-    int i = begin + wave;
-    if (i < end) {
-      // One tile is in flight while the other is worked on, and the page entries of the one after.
-      // Past the end the last tile is loaded again: loads under a condition would have to be waited
-      // for as soon as they are issued.
-      Tile<D, BITS, STEPS> t0, t1;
-      auto next = [&](int at) { return at + kWaves < end ? at + kWaves : at; };
-      auto attend = [&](Tile<D, BITS, STEPS>& t, int at) {
-        const int first = at * kTile;
-        const bool full = whole && t.ok == (1u << STEPS) - 1 && first >= full_lo && first + kTile <= full_hi;
-        attend_tile<D, BITS, STEPS, SPLIT>(t, q, q2, c, full, first + 4 * g, lo, hi, s.kv_len, st);
-      };
-      Pages<STEPS> pages = tile_pages<STEPS>(a, table, i);
-      load_tile<D, BITS, STEPS>(a, pages, head, i, r, g, t0);
-      int n = next(i);
-      pages = tile_pages<STEPS>(a, table, n);
-      while (true) {
-        load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t1);
-        int m = next(n);
-        pages = tile_pages<STEPS>(a, table, m);
-        attend(t0, i);
-        if (n == i) break;
-        i = n;
-        n = m;
-        load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t0);
-        m = next(n);
-        pages = tile_pages<STEPS>(a, table, m);
-        attend(t1, i);
-        if (n == i) break;
-        i = n;
-        n = m;
-      }
-    }
-
-    // Join the waves.
-    st.l = quad_sum(st.l);
-    if (g == 0) {
-      lds_m[wave][r] = st.l > 0.0f ? st.b : neg_inf();
-      lds_l[wave][r] = st.l;
-    }
-    __syncthreads();
-    float top = lds_m[0][r];
-#pragma unroll
-    for (int w = 1; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
-    {
-      const float m = lds_m[wave][r];
-      const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-#pragma unroll
-      for (int m16 = 0; m16 < G::kTilesD; m16++) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) lds_o[wave][r][output_column<D, BITS>(m16, i, g)] = st.o[m16][i] * f;
-      }
-    }
-    __syncthreads();
-    {
-      const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
-      const int at = tile * kRows + row, rc = row < kRows ? row : kRows - 1;
-      const bool ok = row < kRows && at < rows;
-      const int token = ok ? at / a.group : 0, qh = head * a.group + (ok ? at % a.group : 0);
-      float best = neg_inf(), sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; w++) best = fmaxf(best, lds_m[w][rc]);
-#pragma unroll
-      for (int w = 0; w < kWaves; w++)
-        sum += lds_m[w][rc] == neg_inf() ? 0.0f : lds_l[w][rc] * __builtin_amdgcn_exp2f(lds_m[w][rc] - best);
-      float v[R::kChunks][8];
-#pragma unroll
-      for (int k = 0; k < R::kChunks; k++) {
+        float y[8];
+        uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          float y = 0.0f;
+          y[i] = v[k][i] * (sign * up);
+          const _Float16 h = static_cast<_Float16>(y[i]);
+          hi[i] = __builtin_bit_cast(uint16_t, h);
+          lo[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(y[i] - static_cast<float>(h)));
+        }
+        // Pairs in the order in which nibbles_f16 / bytes_f16 give the codes.
+        constexpr int kA[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5};
+        constexpr int kB = BITS == 4 ? 4 : 2;
+        uint32_t* p = lds_q + row * (D / 2) + (k * 16 + chunk) * 4;
 #pragma unroll
-          for (int w = 0; w < kWaves; w++) y += lds_o[w][rc][k * 128 + chunk * 8 + i];
-          v[k][i] = y;
+        for (int i = 0; i < 4; i++) {
+          p[i] = hi[kA[i]] | (hi[kA[i] + kB] << 16);
+          if constexpr (SPLIT) p[kRows * (D / 2) + i] = lo[kA[i]] | (lo[kA[i] + kB] << 16);
         }
       }
-      const int64_t out_row = (s.q0 + token) * a.q_heads + qh;
-      if (a.splits > 1) {
-        if (ok) {
-          float* p = a.part_out + (out_row * a.splits + split) * D;
+      // Logits in base 2 are t * c, t = sum of fp16 query times code, times the key's scale.
+      if (u == 0) lds_c[row] = a.scale * (kLog2e * R::kNorm) / up;
+    }
+    __syncthreads();
+  }
+  u32x4 q[G::kOps], q2[G::kOps];
 #pragma unroll
-          for (int k = 0; k < R::kChunks; k++) store8(reinterpret_cast<uint8_t*>(p + k * 128 + chunk * 8), kF32, v[k]);
-          if (u == 0) {
-            a.part_stat[(out_row * a.splits + split) * 2] = best;
-            a.part_stat[(out_row * a.splits + split) * 2 + 1] = sum;
-          }
-        }
-      } else {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  for (int op = 0; op < G::kOps; op++) {
+    const uint32_t* p = lds_q + r * (D / 2) + operand_chunk<D, BITS>(op, g) * 4;
+    q[op] = *reinterpret_cast<const u32x4*>(p);
+    q2[op] = SPLIT ? *reinterpret_cast<const u32x4*>(p + kRows * (D / 2)) : q[op];
+  }
+  const float c = fmaxf(lds_c[r], 1.1754944e-38f);   // a positive factor keeps masked logits at -inf
+  __syncthreads();   // lds_q is read: lds_o may be written
+
+  State<D, BITS> st;
+  start(st);
+  if (i < end) {
+    auto attend = [&](Tile<D, BITS, STEPS>& t, int at) {
+      const int first = at * kTile;
+      const bool full = whole && t.ok == (1u << STEPS) - 1 && first >= full_lo && first + kTile <= full_hi;
+      attend_tile<D, BITS, STEPS, SPLIT>(t, q, q2, c, full, r, first + 4 * g, lo, hi, s.kv_len, st);
+    };
+    while (true) {
+      load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t1);
+      int m = next(n);
+      pages = tile_pages<STEPS>(a, table, m);
+      attend(t0, i);
+      if (n == i) break;
+      i = n;
+      n = m;
+      load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t0);
+      m = next(n);
+      pages = tile_pages<STEPS>(a, table, m);
+      attend(t1, i);
+      if (n == i) break;
+      i = n;
+      n = m;
+    }
+  }
+
+  // Join the waves.
+  st.l = quad_sum(st.l);
+  if (g == 0) {
+    lds_m[wave][r] = st.l > 0.0f ? st.b : neg_inf();
+    lds_l[wave][r] = st.l;
+  }
+  __syncthreads();
+  float top = lds_m[0][r];
 #pragma unroll
-        for (int k = 0; k < R::kChunks; k++) {
+  for (int w = 1; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
+  {
+    const float m = lds_m[wave][r];
+    const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[k][i] *= inv;
-        }
-        if (ok && a.lse && u == 0) a.lse[out_row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
-        store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, chunk, ok);
+    for (int m16 = 0; m16 < G::kTilesD; m16++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) lds_o[wave][r][output_column<D, BITS>(m16, i, g)] = st.o[m16][i] * f;
+    }
+  }
+  __syncthreads();
+  {
+    const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
+    const int n = tile * kRows + row, rc = row < kRows ? row : kRows - 1;
+    const bool ok = row < kRows && n < rows;
+    const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
+    float best = neg_inf(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) best = fmaxf(best, lds_m[w][rc]);
+#pragma unroll
+    for (int w = 0; w < kWaves; w++)
+      sum += lds_m[w][rc] == neg_inf() ? 0.0f : lds_l[w][rc] * __builtin_amdgcn_exp2f(lds_m[w][rc] - best);
+    float v[R::kChunks][8];
+#pragma unroll
+    for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) y += lds_o[w][rc][k * 128 + chunk * 8 + i];
+        v[k][i] = y;
       }
+    }
+    const int64_t out_row = (int64_t)(s.q0 + token) * a.q_heads + qh;
+    if (a.splits > 1) {
+      if (ok) {
+        float* p = a.part_out + (out_row * a.splits + split) * D;
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++)
+          if (best != neg_inf()) store8(reinterpret_cast<uint8_t*>(p + k * 128 + chunk * 8), kF32, v[k]);
+        if (u == 0) {
+          a.part_stat[(out_row * a.splits + split) * 2] = best;
+          a.part_stat[(out_row * a.splits + split) * 2 + 1] = sum;
+        }
+      }
+    } else {
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[k][i] *= inv;
+      }
+      if (ok && a.lse && u == 0) a.lse[out_row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+      store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, chunk, ok);
     }
   }
 }
 
-// Joins the splits of a row: kLanes lanes a row.
+// Joins the splits of a row. A workgroup takes one row: its 256 / kLanes groups of lanes take the
+// splits in turn, each with a reference of its own, and are joined through LDS by the first.
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
   using R = Row<D, BITS>;
-  const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u);
-  const int64_t row = (int64_t)blockIdx.x * (256 / R::kLanes) + threadIdx.x / R::kLanes;
-  const int64_t all = a.total_q * a.q_heads, rc = row < all ? row : all - 1;
-  const int64_t token = rc / a.q_heads;
-  // Rows of no sequence were not computed: they are left as they were.
-  bool ok = row < all;
-  if (a.q_start) ok = ok && token >= a.q_start[0] && token < a.q_start[a.seqs];
-  const float* stat = a.part_stat + rc * a.splits * 2;
-  const float* part = a.part_out + rc * a.splits * D;
+  constexpr int kGroups = 256 / R::kLanes;
+  __shared__ __attribute__((aligned(16))) float lds_o[kGroups][D + 4];
+  __shared__ float lds_b[kGroups], lds_l[kGroups];
+  const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), group = threadIdx.x / R::kLanes;
+  const Seq s = sequence(a, blockIdx.y);
+  const int in = blockIdx.x / a.q_heads, head = blockIdx.x - in * a.q_heads;
+  if (in >= s.q_len) return;
+  const int64_t token = s.q0 + in, row = token * a.q_heads + head;
+  const float* stat = a.part_stat + row * a.splits * 2;
+  const float* part = a.part_out + row * a.splits * D;
   float best = neg_inf(), sum = 0.0f;
-  for (int i = 0; i < a.splits; i++) best = fmaxf(best, stat[2 * i]);
   float v[R::kChunks][8];
 #pragma unroll
   for (int k = 0; k < R::kChunks; k++) {
 #pragma unroll
     for (int i = 0; i < 8; i++) v[k][i] = 0.0f;
   }
-  for (int i = 0; i < a.splits; i++) {
-    const float m = stat[2 * i];
-    if (m == neg_inf()) continue;
-    const float f = __builtin_amdgcn_exp2f(m - best);
+  for (int i = group; i < a.splits; i += kGroups) best = fmaxf(best, stat[2 * i]);
+  for (int i = group; i < a.splits; i += kGroups) {
+    const float b = stat[2 * i];
+    if (b == neg_inf()) continue;   // the split had no keys: its output was not written
+    const float f = __builtin_amdgcn_exp2f(b - best);
     sum = __builtin_fmaf(stat[2 * i + 1], f, sum);
 #pragma unroll
     for (int k = 0; k < R::kChunks; k++) {
@@ -608,28 +678,55 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
       for (int e = 0; e < 8; e++) v[k][e] = __builtin_fmaf(x[e], f, v[k][e]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < R::kChunks; k++)
+    store8(reinterpret_cast<uint8_t*>(&lds_o[group][k * 128 + chunk * 8]), kF32, v[k]);
+  if (u == 0) {
+    lds_b[group] = best;
+    lds_l[group] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 64) return;   // the first wave: its first group's lanes store
+  best = neg_inf();
+  for (int i = 0; i < kGroups; i++) best = fmaxf(best, lds_b[i]);
+  sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[k][e] = 0.0f;
+  }
+  const int groups = a.splits < kGroups ? a.splits : kGroups;
+  for (int i = 0; i < groups; i++) {
+    const float f = lds_b[i] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(lds_b[i] - best);
+    sum = __builtin_fmaf(lds_l[i], f, sum);
+#pragma unroll
+    for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[k][e] = __builtin_fmaf(lds_o[i][k * 128 + chunk * 8 + e], f, v[k][e]);
+    }
+  }
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int k = 0; k < R::kChunks; k++) {
 #pragma unroll
     for (int i = 0; i < 8; i++) v[k][i] *= inv;
   }
-  if (ok && a.lse && u == 0) a.lse[rc] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
-  store_row<D, BITS>(a.out + (token * a.out_token + rc % a.q_heads * a.out_head) * 2, a.dt, v, chunk, ok);
+  const bool ok = group == 0;
+  if (ok && a.lse && u == 0) a.lse[row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+  store_row<D, BITS>(a.out + (token * a.out_token + head * a.out_head) * 2, a.dt, v, chunk, ok);
 }
 
 template <int D, int BITS>
 hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.splits * a.heads * a.row_tiles), static_cast<unsigned>(a.seqs));
-  constexpr int kSteps = D * BITS <= 256 ? 4 : 2;
+  const dim3 grid(((unsigned)a.splits * a.seqs + kXcds - 1) / kXcds * kXcds * a.row_tiles * a.heads);
+  constexpr int kSteps = 2;
   if (a.dt == kF16)
     kv_attend_kernel<D, BITS, kSteps, true><<<grid, kWaves * 64, 0, stream>>>(a);
   else
     kv_attend_kernel<D, BITS, kSteps, false><<<grid, kWaves * 64, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  constexpr int kPer = 256 / Row<D, BITS>::kLanes;
-  kv_join_kernel<D, BITS><<<dim3(static_cast<unsigned>((a.total_q * a.q_heads + kPer - 1) / kPer)), 256, 0, stream>>>(a);
+  kv_join_kernel<D, BITS><<<dim3((unsigned)a.max_q * a.q_heads, (unsigned)a.seqs), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -641,14 +738,18 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
   KvAttentionPlan p;
   const int64_t tiles = (max_q_len * group + kRows - 1) / kRows;
   p.row_tiles = static_cast<int>(tiles < 1 ? 1 : tiles);
-  // Enough workgroups for 256 compute units several times over, as long as each wave of a split
-  // has two tiles of keys or more.
+  // Enough workgroups for 256 compute units several times over, none with fewer than kMinChunk
+  // keys. A split takes the same number of keys in every sequence, and at least kMinChunk: of a
+  // long sequence beside short ones no workgroup has more than its share. Measured (64 sequences
+  // up to 8192 tokens, 8 heads / 4 up to 131072, one of them most of the work): 768 workgroups 77 /
+  // 66 us, 1024 77 / 80, 2048 76 / 59, 4096 81 / 80.
   int64_t span = max_kv_len;
   if (window > 0 && window + max_q_len < span) span = window + max_q_len;
-  const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = (1024 + groups - 1) / groups;
-  const int64_t most = (span + 63) / 64 / (2 * kWaves);
-  int64_t splits = want < most ? want : most;
+  const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = (2048 + groups - 1) / groups;
+  const int64_t most = (span + 511) / 512;
+  const int64_t splits = want < most ? want : most;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+  p.chunk = kMinChunk;
   p.workspace_bytes = p.splits > 1 ? (size_t)total_q * q_heads * p.splits * (head_dim + 2) * 4 : 0;
   return p;
 }
