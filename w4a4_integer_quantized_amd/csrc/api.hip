@@ -425,6 +425,9 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
   *max_q_len = max_q;
   *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
                                      p->window);
+  if (((int64_t)p->seqs * plan->splits + 8) * cfg->kv_heads > kMaxRowsOrCols / plan->row_tiles)
+    return fail(RQ_EUNSUPPORTED, "%d sequences of up to %lld query rows: too many workgroups (give max_q_len)", p->seqs,
+                (long long)max_q);
   const int64_t need = (int64_t)plan->workspace_bytes;
   if (need > 0) {
     if (ws_bytes < plan->workspace_bytes)
@@ -656,6 +659,7 @@ rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* c
   a.splits = plan.splits;
   a.row_tiles = plan.row_tiles;
   a.chunk = plan.chunk;
+  a.block = plan.block;
   a.max_q = static_cast<int>(max_q);
   a.scale = p->softmax_scale;
   return from_hip(convrot::launch_kv_attention(a, cfg->head_dim, cfg->bits, static_cast<hipStream_t>(stream)),

@@ -83,6 +83,7 @@ struct KvAttentionArgs {
   int64_t total_q, num_pages, head_bytes;
   int seqs, q_heads, heads, group, max_pages, lps, dt, causal, window, splits, row_tiles;
   int chunk;                  // keys of a split, unless the split count makes it more
+  int block;                  // 1: the kernel for many query rows
   int max_q;                  // rows of a sequence that are computed
   int even_q;                 // rows of every sequence where q_start is null
   uint32_t group_mul;         // n / group = (mulhi(n, group_mul) + n) >> group_shift for n < 2^31
@@ -91,7 +92,7 @@ struct KvAttentionArgs {
 };
 // How a call is split: see kv_attention.hip.
 struct KvAttentionPlan {
-  int splits, row_tiles, chunk;
+  int splits, row_tiles, chunk, block;
   size_t workspace_bytes;
 };
 KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int bits,

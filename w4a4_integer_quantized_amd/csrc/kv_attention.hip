@@ -31,6 +31,7 @@ constexpr float kMostExp = 90.0f;   // log2 of the p' that a moved b allows, and
 constexpr float kMostSum = 0x1p120f;   // moves it
 constexpr float kNoRef = -3.0e38f;  // b of a row that has met no key
 constexpr int kMinChunk = 1024;     // keys
+constexpr int kStreamRows = 32;    // more query rows of a sequence and key head than this go by blocks
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // query rows of a tile: (token, head of the group) pairs
 
@@ -81,6 +82,28 @@ __device__ __forceinline__ uint32_t rest_f16(uint32_t h, float a, float b) {
 
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// The power of two for a query row whose largest rotated element is `top`: 2^(8 - exponent), the
+// largest comes to lie in [256, 512). Rows of zeros, and largest elements below 2^-100, get 2^108.
+__device__ __forceinline__ float query_scale(float top) {
+  int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  e = e < -100 ? -100 : e;
+  return __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+}
+
+// 8 elements of a rotated query, times `up`, as fp16 pairs in the order in which nibbles_f16 /
+// bytes_f16 give the codes; `rest`: what that rounding leaves, as fp16.
+template <int BITS>
+__device__ __forceinline__ void query_words(const float (&v)[8], float up, bool rest, uint32_t (&w)[4]) {
+  constexpr int kA[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5};
+  constexpr int kB = BITS == 4 ? 4 : 2;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float a = v[kA[i]] * up, b = v[kA[i] + kB] * up;
+    w[i] = pack_f16(a, b);
+    if (rest) w[i] = rest_f16(w[i], a, b);
+  }
 }
 
 typedef const __attribute__((address_space(4))) int32_t* ConstTable;   // read through the scalar cache
@@ -312,6 +335,7 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
   }
   times_scale<STEPS>(x, x, t.ks);
   if (!full) {   // the same in every lane
+    asm volatile("");   // a branch, not selects in every tile
     const int mine = first + 16 * (r >> 2) + (r & 3);   // `first` includes 4 g
     const uint32_t step = r >> 2 < STEPS ? r >> 2 : 0;
     t.vs = mine < kv_len && (t.ok >> step & 1u) ? t.vs : 0.0f;
@@ -507,37 +531,23 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
       for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[k][i]));
     }
     top = row_max<R::kLanes>(top);
-    // 2^(8 - exponent): the largest element comes to lie in [256, 512). Rows of zeros, and
-    // largest elements below 2^-100, are scaled by 2^108.
-    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    e = e < -100 ? -100 : e;
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - e) << 23);
+    const float up = query_scale(top);
     if (row < kRows) {
 #pragma unroll
       for (int k = 0; k < R::kChunks; k++) {
-        float y[8];
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          y[i] = v[k][i] * (sign * up);
-          const _Float16 h = static_cast<_Float16>(y[i]);
-          hi[i] = __builtin_bit_cast(uint16_t, h);
-          lo[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(y[i] - static_cast<float>(h)));
-        }
-        // Pairs in the order in which nibbles_f16 / bytes_f16 give the codes.
-        constexpr int kA[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5};
-        constexpr int kB = BITS == 4 ? 4 : 2;
+        uint32_t w[4];
         uint32_t* p = lds_q + row * (D / 2) + (k * 16 + chunk) * 4;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          p[i] = hi[kA[i]] | (hi[kA[i] + kB] << 16);
-          if constexpr (SPLIT) p[kRows * (D / 2) + i] = lo[kA[i]] | (lo[kA[i] + kB] << 16);
+        query_words<BITS>(v[k], sign * up, false, w);
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+        if constexpr (SPLIT) {
+          query_words<BITS>(v[k], sign * up, true, w);
+          *reinterpret_cast<u32x4*>(p + kRows * (D / 2)) = u32x4{w[0], w[1], w[2], w[3]};
         }
       }
       // Logits in base 2 are t * c, t = sum of fp16 query times code, times the key's scale.
       if (u == 0) lds_c[row] = a.scale * (kLog2e * R::kNorm) / up;
     }
-    __syncthreads();
+  __syncthreads();
   }
   u32x4 q[G::kOps], q2[G::kOps];
 #pragma unroll
@@ -642,6 +652,437 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
   }
 }
 
+// ---- Many query rows: tiles of keys shared by a workgroup ----------------------------------
+//
+// One workgroup: 128 query rows of one key head and sequence, 32 a wave, and one split of the
+// keys. The stream kernel above converts every code in every wave, 64 codes for a wave's 16 rows;
+// here a tile of 64 keys is converted once for 128 rows and laid in LDS as fp16 operands of
+// 32x32x16 matrix instructions:
+//   K   [key][D], 16-byte chunks (8 elements) of a row exchanged by key & 7
+//   V   [d][64 keys], chunk 2 s + h of a row: the keys that lane half h holds of 16-key step s,
+//       16 s + 4 h + {0, 2, 1, 3} and 8 further (these first where d & 64); chunks exchanged by
+//       (d ^ d / 8) & 7
+// so that eight neighbouring lanes always touch eight different 16-byte bank groups. As above the
+// logits come out with a query row in each lane (two lanes a row), which is the operand of the
+// second product. The next tile's codes are loaded while one is worked on.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kBlockRows = 128, kBlockKeys = 64;
+
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Barrier for LDS: global loads under way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <int N = 0>
+__device__ __forceinline__ void times_scale16(float (&a)[16], const float (&b)[16], float scale) {
+  if constexpr (N < 16) {
+    a[N] = row_lane<N>(scale) * b[N];
+    times_scale16<N + 1>(a, b, scale);
+  }
+}
+
+template <int D, int BITS, bool SPLIT>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(KvAttentionArgs a) {
+  using R = Row<D, BITS>;
+  constexpr int kUnits = R::kBytes / 32;        // 16-byte pieces of a tile's codes a thread loads
+  constexpr int kPieces = 4 * R::kBytes;        // of K, and as many of V
+  constexpr bool kTwoSteps = R::kBytes == 32;   // a wave's pieces lie in two 16-token steps
+  constexpr int kOps = D / 16, kTilesD = D / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBlockKeys * D * 4];
+  __shared__ float lds_ks[kBlockKeys], lds_vs[kBlockKeys];
+  __shared__ uint64_t lds_ok;
+  __shared__ float lds_c[4][32];
+  // A chunk's place in its K row: what loads and stages a row has its chunks of 64 elements in
+  // different lanes, which the second term keeps apart.
+  auto k_chunk = [](int chunk, int key) {
+    return chunk ^ (key & 7) ^ (BITS == 8 ? chunk >> 3 & 1 : D == 128 ? (chunk >> 3 & 1) * 2 : chunk >> 3 & 3);
+  };
+  uint8_t* const lds_k = lds;
+  uint8_t* const lds_v = lds + kBlockKeys * D * 2;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  // Heads first, then sequences; the tiles from the last to the first (with causal the last ones
+  // have the most keys); splits last. From tile to tile the sequences are turned by one: workgroups
+  // go to the XCDs and to the shader engines of one in turn, and of a ragged batch's tiles most
+  // are the longest sequence's (chunks of 423 to 2048 rows, 8 heads: 1212 us with that sequence
+  // always in the same place, 718 us so).
+  uint32_t id = blockIdx.x;
+  const int head = id % a.heads;
+  id /= a.heads;
+  const uint32_t turn = id / a.seqs;
+  const int b = (id - turn * a.seqs + turn) % a.seqs;
+  const int split = a.splits == 1 ? 0 : turn / a.row_tiles;
+  const int tile = a.row_tiles - 1 - (turn - split * a.row_tiles);
+  const Seq s = sequence(a, b);
+  const int rows = (s.q_len < a.max_q ? s.q_len : a.max_q) * a.group;
+  const int row_first = tile * kBlockRows;
+  if (row_first >= rows) return;
+  const int row_last = (row_first + kBlockRows < rows ? row_first + kBlockRows : rows) - 1;
+  const ConstTable table = const_table(a.pages + (int64_t)b * a.max_pages);
+  const int page = 1 << a.lps;
+
+  // Keys: of the workgroup, of the wave, of the lane's row.
+  int t_lo, t_hi, lo, hi, w_lo, w_hi, full_lo, full_hi;
+  key_range(a, s, token_of(a, row_first), t_lo, hi);
+  key_range(a, s, token_of(a, row_last), lo, t_hi);
+  const int w_first = row_first + 32 * wave, w_last = w_first + 31 < rows ? w_first + 31 : rows - 1;
+  w_lo = w_hi = full_lo = full_hi = 0;
+  if (w_first < rows) {
+    key_range(a, s, token_of(a, w_first), w_lo, full_hi);
+    key_range(a, s, token_of(a, w_last), full_lo, w_hi);
+    if (w_last != w_first + 31) full_hi = 0;
+  }
+  const bool mine = w_first + r < rows;
+  key_range(a, s, token_of(a, mine ? w_first + r : row_first), lo, hi);
+  if (!mine) lo = hi = 0;
+  const int tiles_lo = t_lo / kBlockKeys, tiles_hi = (t_hi + kBlockKeys - 1) / kBlockKeys;
+  const int count = tiles_hi > tiles_lo ? tiles_hi - tiles_lo : 0;
+  const int share = (count + a.splits - 1) / a.splits, chunk = share > a.chunk / kBlockKeys ? share : a.chunk / kBlockKeys;
+  const int begin = tiles_lo + (split * (int64_t)chunk < count ? split * chunk : count);
+  const int end = tiles_lo + (count - (begin - tiles_lo) < chunk ? count : begin - tiles_lo + chunk);
+
+  // Codes of a tile: piece p of K is 16 bytes of key p / (row_bytes / 16), piece p of V the 16
+  // bytes at column 4 (p % (row_bytes / 4)) of token group p / (row_bytes / 4); consecutive lanes
+  // read consecutive bytes of a page. The table entry of a wave's 16-token step comes through the
+  // scalar cache one tile ahead; lane L of the first two waves loads key L's scale.
+  u32x4 raw[kUnits];
+  float raw_scale = 0.0f;
+  bool raw_ok = false;
+  int at_page[kUnits][kTwoSteps ? 2 : 1], scale_page = 0;
+  auto step_of = [&](int n) {   // the first 16-token step of the wave's n-th pieces
+    const int p = (n * 256 + wave * 64) % kPieces;
+    return p / R::kBytes;       // 16 tokens are row_bytes pieces
+  };
+  auto load_pages = [&](int at) {
+#pragma unroll
+    for (int n = 0; n < kUnits; n++) {
+#pragma unroll
+      for (int k = 0; k < (kTwoSteps ? 2 : 1); k++) {
+        const int e = (at * kBlockKeys + (step_of(n) + k) * 16) >> a.lps;
+        at_page[n][k] = table[e < a.max_pages ? e : a.max_pages - 1];
+      }
+    }
+    if (wave < 2) {
+      const int e = (at * kBlockKeys + lane) >> a.lps;
+      scale_page = a.pages[(int64_t)b * a.max_pages + (e < a.max_pages ? e : a.max_pages - 1)];
+    }
+  };
+  auto load_codes = [&](int at) {
+#pragma unroll
+    for (int n = 0; n < kUnits; n++) {
+      const int p0 = n * 256 + wave * 64, p = (p0 % kPieces) + lane, step = step_of(n);
+      const bool values = p0 >= kPieces;
+      const uint8_t* block[kTwoSteps ? 2 : 1];
+#pragma unroll
+      for (int k = 0; k < (kTwoSteps ? 2 : 1); k++) {
+        const int pg = at_page[n][k];
+        const bool ok = pg >= 0 && pg < a.num_pages;
+        block[k] = a.cache + ((int64_t)(ok ? pg : 0) * a.heads + head) * a.head_bytes;
+      }
+      // The piece's bytes follow its step's first: 16 tokens' K (or V) codes are 16 row_bytes.
+      const uint8_t* base = block[0];
+      int off = (at * kBlockKeys + step * 16) & (page - 1);
+      uint32_t in = (p - step * R::kBytes) * 16;
+      if constexpr (kTwoSteps) {
+        if (lane >= 32) {
+          base = block[1];
+          off = (at * kBlockKeys + (step + 1) * 16) & (page - 1);
+          in -= 16 * R::kBytes;
+        }
+      }
+      raw[n] = *reinterpret_cast<const u32x4*>(base + ((off + (values ? page : 0)) * R::kBytes + in));
+    }
+    if (wave < 2) {
+      const int key = at * kBlockKeys + lane;
+      const bool in = scale_page >= 0 && scale_page < a.num_pages;
+      raw_ok = in && key < s.kv_len;
+      const uint8_t* block = a.cache + ((int64_t)(in ? scale_page : 0) * a.heads + head) * a.head_bytes;
+      raw_scale = reinterpret_cast<const float*>(block + 2 * page * R::kBytes)[(wave ? page : 0) + (key & (page - 1))];
+    }
+  };
+  auto stage = [&]() {
+#pragma unroll
+    for (int n = 0; n < kUnits; n++) {
+      const int p0 = n * 256 + wave * 64, p = (p0 % kPieces) + lane;
+      if (p0 < kPieces) {
+        const int key = p / (R::kBytes / 16), first = p % (R::kBytes / 16) * (16 / BITS);   // the piece's first chunk
+        uint8_t* row = lds_k + key * (D * 2);
+#pragma unroll
+        for (int w = 0; w < 4; w += BITS / 4) {
+          u32x4 c;
+          if constexpr (BITS == 4) {
+            uint32_t x[4];
+            nibbles_f16(raw[n][w], x);
+            c = u32x4{x[0], x[1], x[2], x[3]};
+          } else {
+            uint32_t x[2], y[2];
+            bytes_f16(raw[n][w], x);
+            bytes_f16(raw[n][w + 1], y);
+            c = u32x4{x[0], x[1], y[0], y[1]};
+          }
+          *reinterpret_cast<u32x4*>(row + k_chunk(first + w * 4 / BITS, key) * 16) = c;
+        }
+      } else {
+        const int group = p / (R::kBytes / 4), col = p % (R::kBytes / 4) * 4;
+        const int at = (group >> 2) * 2 + (group & 1);
+        auto put = [&](int d, uint32_t x, uint32_t y) {
+          *reinterpret_cast<u32x2*>(lds_v + d * 128 + (at ^ ((d ^ (d >> 3)) & 7)) * 16 + ((group >> 1 ^ d >> 6) & 1) * 8) = u32x2{x, y};
+        };
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+          if constexpr (BITS == 4) {
+            uint32_t x[4];
+            nibbles_f16(raw[n][w], x);
+            put(2 * (col + w), x[0], x[2]);
+            put(2 * (col + w) + 1, x[1], x[3]);
+          } else {
+            uint32_t x[2];
+            bytes_f16(raw[n][w], x);
+            put(col + w, x[0], x[1]);
+          }
+        }
+      }
+    }
+    if (wave == 0) {
+      const uint64_t ok = __ballot(raw_ok);
+      if (lane == 0) lds_ok = ok;
+      lds_ks[lane] = raw_scale;
+    } else if (wave == 1) {
+      lds_vs[lane] = raw_ok ? raw_scale : 0.0f;
+    }
+  };
+  if (begin < end) {
+    load_pages(begin);
+    load_codes(begin);
+    load_pages(begin + 1 < end ? begin + 1 : begin);
+  }
+
+  // Queries, a wave its own 32 rows: rotated, scaled, to fp16, in the K operands' element order.
+  u32x4 q[kOps], q2[kOps];
+  {
+    constexpr int kAtOnce = 64 / R::kLanes;
+    uint32_t* region = reinterpret_cast<uint32_t*>(lds) + wave * (16 * D);   // 32 rows of D / 2 words
+    const int u = lane % R::kLanes, chunk = chunk_of_lane(u);
+    for (int part = 0; part < (SPLIT ? 2 : 1); part++) {
+      for (int k0 = 0; k0 < 32; k0 += kAtOnce) {
+        const int row = k0 + lane / R::kLanes, n = w_first + row;
+        const bool ok = n < rows;
+        const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
+        const uint8_t* x = a.q + ((s.q0 + token) * a.q_token + qh * a.q_head) * 2;
+        float v[R::kChunks][8], sign = 1.0f, top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) load8(x + (k * 128 + chunk * 8) * 2, a.dt, v[k]);
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) {
+          sign = wht_block<R::kLanes>(v[k], chunk);
+#pragma unroll
+          for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[k][i]));
+        }
+        const float up = query_scale(row_max<R::kLanes>(top));
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) {
+          uint32_t w[4];
+          query_words<BITS>(v[k], sign * up, part == 1, w);
+          *reinterpret_cast<u32x4*>(region + row * (D / 2) + ((k * 16 + chunk) ^ (row & 7)) * 4) = u32x4{w[0], w[1], w[2], w[3]};
+        }
+        if (u == 0) lds_c[wave][row] = a.scale * (kLog2e * R::kNorm) / up;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int m = 0; m < kOps; m++) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(region + r * (D / 2) + ((2 * m + h) ^ (r & 7)) * 4);
+        if (part == 0) q[m] = w;
+        if (SPLIT && part == 1) q2[m] = w;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  const float c = fmaxf(lds_c[wave][r], 1.1754944e-38f);
+
+  f32x16 o[kTilesD];
+#pragma unroll
+  for (int t = 0; t < kTilesD; t++) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) o[t][i] = 0.0f;
+  }
+  float ref = kNoRef, sum = 0.0f;
+
+  for (int at = begin; at < end; at++) {
+    lds_barrier();   // the tile before (and the queries' region) has been read
+    stage();
+    load_codes(at + 1 < end ? at + 1 : at);
+    load_pages(at + 2 < end ? at + 2 : end - 1);
+    lds_barrier();
+    const uint64_t there = lds_ok;
+    const int first = at * kBlockKeys;
+    if (first >= w_hi || first + kBlockKeys <= w_lo) continue;   // none of the wave's rows
+    // Both 32-key halves together: two chains of products.
+    f32x16 acc[2];
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) acc[sub][i] = 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < kOps; m++) {
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const u32x4 kop = *reinterpret_cast<const u32x4*>(lds_k + (sub * 32 + r) * (D * 2) + k_chunk(2 * m + h, r) * 16);
+        if constexpr (SPLIT) acc[sub] = mfma32(kop, q2[m], acc[sub]);
+        acc[sub] = mfma32(kop, q[m], acc[sub]);
+      }
+    }
+    // Lane n of a row of 16 holds the scales of its half's n-th key: 8 (n / 4) + 4 h + n % 4.
+    const int sk = 8 * ((lane & 15) >> 2) + 4 * h + (lane & 3);
+    float x[2][16], p[2][16], vs[2];
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++) {
+      vs[sub] = lds_vs[sub * 32 + sk];
+#pragma unroll
+      for (int i = 0; i < 16; i++) x[sub][i] = acc[sub][i];
+      times_scale16(x[sub], x[sub], lds_ks[sub * 32 + sk]);
+    }
+    if (!(there == ~0ull && first >= full_lo && first + kBlockKeys <= full_hi)) {
+      asm volatile("");   // a branch, not 32 selects in every tile
+      const uint32_t span = hi > lo ? hi - lo : 0;
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const uint32_t bits = static_cast<uint32_t>(there >> (sub * 32)) >> (4 * h);
+        const uint32_t from = first + sub * 32 + 4 * h - lo;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          const int n = 8 * (i / 4) + i % 4;
+          x[sub][i] = from + n < span && (bits >> n & 1u) ? x[sub][i] : neg_inf();
+        }
+      }
+    }
+    float l, w[2][16];
+    auto weigh = [&]() {
+      float wtop = 0.0f;
+      l = sum;
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          p[sub][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[sub][i], c, -ref));
+          l += p[sub][i];
+        }
+        times_scale16(w[sub], p[sub], vs[sub]);
+#pragma unroll
+        for (int i = 0; i < 16; i++) wtop = fmaxf(wtop, w[sub][i]);
+      }
+      return wtop <= kMost && l < kMostSum;
+    };
+    if (!__all(weigh())) {   // as in attend_tile
+      float wl = neg_inf(), top = neg_inf();
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const float lv = vs[sub] > 0.0f ? __builtin_amdgcn_logf(vs[sub]) : neg_inf();
+#pragma unroll
+        for (int i = 0; i < 16; i++) p[sub][i] = 1.0f;
+        times_scale16(p[sub], p[sub], lv);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          top = fmaxf(top, x[sub][i]);
+          wl = fmaxf(wl, __builtin_fmaf(x[sub][i], c, p[sub][i]));
+        }
+      }
+      wl = fmaxf(wl, __shfl_xor(wl, 32, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
+      const bool moves = wl - ref > 15.0f || top - ref > kMostExp;
+      const float next = moves ? fmaxf(wl - kTop, top - kMostExp) : ref;
+      const float alpha = __builtin_amdgcn_exp2f(ref - next);
+      ref = next;
+      sum *= alpha;
+#pragma unroll
+      for (int t = 0; t < kTilesD; t++) o[t] *= alpha;
+      weigh();
+    }
+    sum = l;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float* y = w[k / 2] + 8 * (k % 2);
+      const u32x4 lead = {pack_f16(y[0], y[2]), pack_f16(y[1], y[3]), pack_f16(y[4], y[6]), pack_f16(y[5], y[7])};
+      u32x4 rest;
+      if constexpr (SPLIT)
+        rest = u32x4{rest_f16(lead[0], y[0], y[2]), rest_f16(lead[1], y[1], y[3]), rest_f16(lead[2], y[4], y[6]),
+                     rest_f16(lead[3], y[5], y[7])};
+#pragma unroll
+      for (int t = 0; t < kTilesD; t++) {
+        const int d = t * 32 + r;
+        const u32x4 vop = *reinterpret_cast<const u32x4*>(lds_v + d * 128 + ((2 * k + h) ^ ((d ^ (d >> 3)) & 7)) * 16);
+        const bool turned = t >> 1 & 1;   // rows whose halves of a chunk are exchanged
+        if constexpr (SPLIT) o[t] = mfma32(vop, turned ? u32x4{rest[2], rest[3], rest[0], rest[1]} : rest, o[t]);
+        o[t] = mfma32(vop, turned ? u32x4{lead[2], lead[3], lead[0], lead[1]} : lead, o[t]);
+      }
+    }
+  }
+
+  // Outputs, a wave its own rows, 16 at a time through its quarter of the LDS.
+  sum += __shfl_xor(sum, 32, 64);
+  lds_barrier();
+  float* region = reinterpret_cast<float*>(lds) + wave * (16 * D);
+  const int u = lane % R::kLanes, cc = chunk_of_lane(u);
+  for (int part = 0; part < 2; part++) {
+    __builtin_amdgcn_wave_barrier();
+    if ((r >> 4) == part) {
+#pragma unroll
+      for (int t = 0; t < kTilesD; t++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          *reinterpret_cast<f32x4*>(region + (r & 15) * D + ((t * 8 + 2 * i + h) ^ (r & 15)) * 4) =
+              f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int k0 = 0; k0 < 16; k0 += 64 / R::kLanes) {
+      const int row = k0 + lane / R::kLanes, n = w_first + part * 16 + row;
+      const bool ok = n < rows;
+      const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
+      const float l = __shfl(sum, part * 16 + row, 64), rb = __shfl(ref, part * 16 + row, 64);
+      float v[R::kChunks][8];
+#pragma unroll
+      for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(region + row * D + ((k * 32 + cc * 2 + e) ^ row) * 4);
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[k][4 * e + i] = y[i];
+        }
+      }
+      const int64_t out_row = (int64_t)(s.q0 + token) * a.q_heads + qh;
+      if (a.splits > 1) {
+        if (!ok) continue;
+        if (l > 0.0f) {
+          float* to = a.part_out + (out_row * a.splits + split) * D;
+#pragma unroll
+          for (int k = 0; k < R::kChunks; k++) store8(reinterpret_cast<uint8_t*>(to + k * 128 + cc * 8), kF32, v[k]);
+        }
+        if (u == 0) {
+          a.part_stat[(out_row * a.splits + split) * 2] = l > 0.0f ? rb : neg_inf();
+          a.part_stat[(out_row * a.splits + split) * 2 + 1] = l;
+        }
+      } else {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int k = 0; k < R::kChunks; k++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[k][i] *= inv;
+        }
+        if (ok && a.lse && u == 0) a.lse[out_row] = l > 0.0f ? (rb + __log2f(l)) * kLn2 : neg_inf();
+        store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, cc, ok);
+      }
+    }
+  }
+}
+
 // Joins the splits of a row. A workgroup takes one row: its 256 / kLanes groups of lanes take the
 // splits in turn, each with a reference of its own, and are joined through LDS by the first.
 template <int D, int BITS>
@@ -717,13 +1158,25 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
 }
 
 template <int D, int BITS>
-hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
+void launch_stream(const KvAttentionArgs& a, hipStream_t stream) {
   const dim3 grid(((unsigned)a.splits * a.seqs + kXcds - 1) / kXcds * kXcds * a.row_tiles * a.heads);
-  constexpr int kSteps = 2;
   if (a.dt == kF16)
-    kv_attend_kernel<D, BITS, kSteps, true><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, 2, true><<<grid, kWaves * 64, 0, stream>>>(a);
   else
-    kv_attend_kernel<D, BITS, kSteps, false><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, 2, false><<<grid, kWaves * 64, 0, stream>>>(a);
+}
+
+template <int D, int BITS>
+hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
+  if (a.block) {
+    const dim3 grid((unsigned)a.splits * a.row_tiles * a.seqs * a.heads);
+    if (a.dt == kF16)
+      kv_attend_block_kernel<D, BITS, true><<<grid, 256, 0, stream>>>(a);
+    else
+      kv_attend_block_kernel<D, BITS, false><<<grid, 256, 0, stream>>>(a);
+  } else {
+    launch_stream<D, BITS>(a, stream);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   kv_join_kernel<D, BITS><<<dim3((unsigned)a.max_q * a.q_heads, (unsigned)a.seqs), 256, 0, stream>>>(a);
@@ -736,7 +1189,9 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
                                   int64_t max_q_len, int64_t max_kv_len, int window) {
   const int64_t group = q_heads / heads;
   KvAttentionPlan p;
-  const int64_t tiles = (max_q_len * group + kRows - 1) / kRows;
+  p.block = max_q_len * group > kStreamRows;
+  const int tile_rows = p.block ? kBlockRows : kRows;
+  const int64_t tiles = (max_q_len * group + tile_rows - 1) / tile_rows;
   p.row_tiles = static_cast<int>(tiles < 1 ? 1 : tiles);
   // Enough workgroups for 256 compute units several times over, none with fewer than kMinChunk
   // keys. A split takes the same number of keys in every sequence, and at least kMinChunk: of a
@@ -745,7 +1200,7 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
   // 66 us, 1024 77 / 80, 2048 76 / 59, 4096 81 / 80.
   int64_t span = max_kv_len;
   if (window > 0 && window + max_q_len < span) span = window + max_q_len;
-  const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = (2048 + groups - 1) / groups;
+  const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = p.block ? 512 / groups : (2048 + groups - 1) / groups;
   const int64_t most = (span + 511) / 512;
   const int64_t splits = want < most ? want : most;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
