@@ -660,11 +660,11 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
 // 32x32x16 matrix instructions:
 //   K   [key][D], 16-byte chunks (8 elements) of a row exchanged by key & 7
 //   V   [d][64 keys], chunk 2 s + h of a row: the keys that lane half h holds of 16-key step s,
-//       16 s + 4 h + {0, 2, 1, 3} and 8 further (these first where d & 64); chunks exchanged by
-//       (d ^ d / 8) & 7
+//       16 s + 4 h + {0, 2, 1, 3} and 8 further; chunks exchanged by (d ^ d / 8) & 7
 // so that eight neighbouring lanes always touch eight different 16-byte bank groups. As above the
 // logits come out with a query row in each lane (two lanes a row), which is the operand of the
-// second product. The next tile's codes are loaded while one is worked on.
+// second product. While one tile is worked on the next is converted into a second buffer, and the
+// codes of the one after are on their way.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kBlockRows = 128, kBlockKeys = 64;
@@ -695,17 +695,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
   constexpr int kPieces = 4 * R::kBytes;        // of K, and as many of V
   constexpr bool kTwoSteps = R::kBytes == 32;   // a wave's pieces lie in two 16-token steps
   constexpr int kOps = D / 16, kTilesD = D / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kBlockKeys * D * 4];
-  __shared__ float lds_ks[kBlockKeys], lds_vs[kBlockKeys];
-  __shared__ uint64_t lds_ok;
+  constexpr uint32_t kBuffer = kBlockKeys * D * 4;   // a tile of K and V; two of them in turn
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuffer];
+  __shared__ float lds_ks[2][kBlockKeys], lds_vs[2][kBlockKeys];
+  __shared__ uint64_t lds_ok[2];
   __shared__ float lds_c[4][32];
   // A chunk's place in its K row: what loads and stages a row has its chunks of 64 elements in
   // different lanes, which the second term keeps apart.
   auto k_chunk = [](int chunk, int key) {
     return chunk ^ (key & 7) ^ (BITS == 8 ? chunk >> 3 & 1 : D == 128 ? (chunk >> 3 & 1) * 2 : chunk >> 3 & 3);
   };
-  uint8_t* const lds_k = lds;
-  uint8_t* const lds_v = lds + kBlockKeys * D * 2;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   // Heads first, then sequences; the tiles from the last to the first (with causal the last ones
@@ -756,10 +755,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
   float raw_scale = 0.0f;
   bool raw_ok = false;
   int at_page[kUnits][kTwoSteps ? 2 : 1], scale_page = 0;
-  auto step_of = [&](int n) {   // the first 16-token step of the wave's n-th pieces
-    const int p = (n * 256 + wave * 64) % kPieces;
-    return p / R::kBytes;       // 16 tokens are row_bytes pieces
+  // The token group of V's piece p. Of 16 neighbouring lanes 8 take groups whose tokens go into the
+  // other half of a 16-byte chunk: their writes then meet in no bank.
+  auto v_group = [](int p) {
+    const int g = p / (R::kBytes / 4);
+    if constexpr (R::kBytes == 64) return g ^ (p >> 3 & 1) * 2;
+    if constexpr (R::kBytes == 32) return (g & ~3) | (g & 1) << 1 | (g >> 1 & 1);
+    return g;
   };
+  // The wave's n-th 64 pieces: V's (known when compiling where a round of the workgroup is all K's or
+  // all V's), their first, and its 16-token step: 16 tokens are row_bytes pieces.
+  auto is_v = [&](int n) { return kPieces >= 256 ? n * 256 >= kPieces : wave * 64 >= kPieces; };
+  auto piece_of = [&](int n) { return n * 256 + wave * 64 - (is_v(n) ? kPieces : 0); };
+  auto step_of = [&](int n) { return piece_of(n) / R::kBytes; };
   auto load_pages = [&](int at) {
 #pragma unroll
     for (int n = 0; n < kUnits; n++) {
@@ -777,8 +785,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
   auto load_codes = [&](int at) {
 #pragma unroll
     for (int n = 0; n < kUnits; n++) {
-      const int p0 = n * 256 + wave * 64, p = (p0 % kPieces) + lane, step = step_of(n);
-      const bool values = p0 >= kPieces;
+      const int p = piece_of(n) + lane, step = step_of(n);
+      const bool values = is_v(n);
       const uint8_t* block[kTwoSteps ? 2 : 1];
 #pragma unroll
       for (int k = 0; k < (kTwoSteps ? 2 : 1); k++) {
@@ -789,7 +797,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       // The piece's bytes follow its step's first: 16 tokens' K (or V) codes are 16 row_bytes.
       const uint8_t* base = block[0];
       int off = (at * kBlockKeys + step * 16) & (page - 1);
-      uint32_t in = (p - step * R::kBytes) * 16;
+      const int q = values ? v_group(p) * (R::kBytes / 4) + p % (R::kBytes / 4) : p;
+      uint32_t in = (q - step * R::kBytes) * 16;
       if constexpr (kTwoSteps) {
         if (lane >= 32) {
           base = block[1];
@@ -807,13 +816,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       raw_scale = reinterpret_cast<const float*>(block + 2 * page * R::kBytes)[(wave ? page : 0) + (key & (page - 1))];
     }
   };
-  auto stage = [&]() {
+  auto stage = [&](int half) {   // into buffer `half`
 #pragma unroll
     for (int n = 0; n < kUnits; n++) {
-      const int p0 = n * 256 + wave * 64, p = (p0 % kPieces) + lane;
-      if (p0 < kPieces) {
+      const int p = piece_of(n) + lane;
+      if (!is_v(n)) {
         const int key = p / (R::kBytes / 16), first = p % (R::kBytes / 16) * (16 / BITS);   // the piece's first chunk
-        uint8_t* row = lds_k + key * (D * 2);
+        uint32_t to = half * kBuffer + key * (D * 2) + k_chunk(first, key) * 16;
+        asm volatile("" : "+v"(to));
 #pragma unroll
         for (int w = 0; w < 4; w += BITS / 4) {
           u32x4 c;
@@ -827,35 +837,40 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
             bytes_f16(raw[n][w + 1], y);
             c = u32x4{x[0], x[1], y[0], y[1]};
           }
-          *reinterpret_cast<u32x4*>(row + k_chunk(first + w * 4 / BITS, key) * 16) = c;
+          *reinterpret_cast<u32x4*>(lds + (to ^ (w * 4 / BITS) * 16)) = c;
         }
       } else {
-        const int group = p / (R::kBytes / 4), col = p % (R::kBytes / 4) * 4;
+        // Rows d = kRow col + y, y < 4 kRow <= 8: the chunk of row d is that of row kRow col, exchanged by y.
+        const int group = v_group(p), col = p % (R::kBytes / 4) * 4;
         const int at = (group >> 2) * 2 + (group & 1);
-        auto put = [&](int d, uint32_t x, uint32_t y) {
-          *reinterpret_cast<u32x2*>(lds_v + d * 128 + (at ^ ((d ^ (d >> 3)) & 7)) * 16 + ((group >> 1 ^ d >> 6) & 1) * 8) = u32x2{x, y};
+        constexpr int kRow = 8 / BITS;
+        const int d0 = kRow * col;
+        uint32_t to = half * kBuffer + kBuffer / 2 + d0 * 128 + ((at ^ ((d0 ^ (d0 >> 3)) & 7)) * 16) + (group >> 1 & 1) * 8;
+        asm volatile("" : "+v"(to));
+        auto put = [&](int y, uint32_t a0, uint32_t a1) {
+          *reinterpret_cast<u32x2*>(lds + (to ^ y * 16) + y * 128) = u32x2{a0, a1};
         };
 #pragma unroll
         for (int w = 0; w < 4; w++) {
           if constexpr (BITS == 4) {
             uint32_t x[4];
             nibbles_f16(raw[n][w], x);
-            put(2 * (col + w), x[0], x[2]);
-            put(2 * (col + w) + 1, x[1], x[3]);
+            put(2 * w, x[0], x[2]);
+            put(2 * w + 1, x[1], x[3]);
           } else {
             uint32_t x[2];
             bytes_f16(raw[n][w], x);
-            put(col + w, x[0], x[1]);
+            put(w, x[0], x[1]);
           }
         }
       }
     }
     if (wave == 0) {
       const uint64_t ok = __ballot(raw_ok);
-      if (lane == 0) lds_ok = ok;
-      lds_ks[lane] = raw_scale;
+      if (lane == 0) lds_ok[half] = ok;
+      lds_ks[half][lane] = raw_scale;
     } else if (wave == 1) {
-      lds_vs[lane] = raw_ok ? raw_scale : 0.0f;
+      lds_vs[half][lane] = raw_ok ? raw_scale : 0.0f;
     }
   };
   if (begin < end) {
@@ -906,6 +921,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
   }
   const float c = fmaxf(lds_c[wave][r], 1.1754944e-38f);
 
+  // Where the lane reads its operands: chunk 2 m + h of K row r, chunk 2 k + h of V row 32 t + r. All
+  // others follow by exchanging bits of the address, which costs less than keeping them.
+  uint32_t k_at = r * (D * 2) + k_chunk(h, r) * 16, v_at = kBuffer / 2 + r * 128 + (h ^ ((r ^ (r >> 3)) & 7)) * 16;
+
   f32x16 o[kTilesD];
 #pragma unroll
   for (int t = 0; t < kTilesD; t++) {
@@ -914,15 +933,30 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
   }
   float ref = kNoRef, sum = 0.0f;
 
+  lds_barrier();   // the queries' region has been read
+  if (begin < end) {
+    stage(0);
+    load_codes(begin + 1 < end ? begin + 1 : begin);
+    load_pages(begin + 2 < end ? begin + 2 : end - 1);
+  }
+  lds_barrier();
   for (int at = begin; at < end; at++) {
-    lds_barrier();   // the tile before (and the queries' region) has been read
-    stage();
-    load_codes(at + 1 < end ? at + 1 : at);
-    load_pages(at + 2 < end ? at + 2 : end - 1);
-    lds_barrier();
-    const uint64_t there = lds_ok;
-    const int first = at * kBlockKeys;
-    if (first >= w_hi || first + kBlockKeys <= w_lo) continue;   // none of the wave's rows
+    // One buffer is read, the next tile goes into the other, the one after is on its way.
+    const int half = (at - begin) & 1, first = at * kBlockKeys;
+    auto next = [&]() {
+      stage(half ^ 1);
+      load_codes(at + 2 < end ? at + 2 : end - 1);
+      load_pages(at + 3 < end ? at + 3 : end - 1);
+    };
+    if (first >= w_hi || first + kBlockKeys <= w_lo) {   // none of the wave's rows
+      next();
+      lds_barrier();
+      k_at ^= kBuffer;
+      v_at ^= kBuffer;
+      continue;
+    }
+    const uint64_t there = lds_ok[half];
+    asm volatile("" : "+v"(k_at), "+v"(v_at));   // not kept over the loop in all their forms
     // Both 32-key halves together: two chains of products.
     f32x16 acc[2];
 #pragma unroll
@@ -934,20 +968,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
     for (int m = 0; m < kOps; m++) {
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
-        const u32x4 kop = *reinterpret_cast<const u32x4*>(lds_k + (sub * 32 + r) * (D * 2) + k_chunk(2 * m + h, r) * 16);
+        const u32x4 kop = *reinterpret_cast<const u32x4*>(lds + (k_at ^ k_chunk(2 * m, 0) * 16) + sub * 32 * (D * 2));
         if constexpr (SPLIT) acc[sub] = mfma32(kop, q2[m], acc[sub]);
         acc[sub] = mfma32(kop, q[m], acc[sub]);
       }
     }
+    next();   // beside the products
     // Lane n of a row of 16 holds the scales of its half's n-th key: 8 (n / 4) + 4 h + n % 4.
     const int sk = 8 * ((lane & 15) >> 2) + 4 * h + (lane & 3);
     float x[2][16], p[2][16], vs[2];
 #pragma unroll
     for (int sub = 0; sub < 2; sub++) {
-      vs[sub] = lds_vs[sub * 32 + sk];
+      vs[sub] = lds_vs[half][sub * 32 + sk];
 #pragma unroll
       for (int i = 0; i < 16; i++) x[sub][i] = acc[sub][i];
-      times_scale16(x[sub], x[sub], lds_ks[sub * 32 + sk]);
+      times_scale16(x[sub], x[sub], lds_ks[half][sub * 32 + sk]);
     }
     if (!(there == ~0ull && first >= full_lo && first + kBlockKeys <= full_hi)) {
       asm volatile("");   // a branch, not 32 selects in every tile
@@ -965,8 +1000,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
     }
     float l, w[2][16];
     auto weigh = [&]() {
-      float wtop = 0.0f;
       l = sum;
+      float wtop = 0.0f;
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
 #pragma unroll
@@ -1016,18 +1051,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
                      rest_f16(lead[3], y[5], y[7])};
 #pragma unroll
       for (int t = 0; t < kTilesD; t++) {
-        const int d = t * 32 + r;
-        const u32x4 vop = *reinterpret_cast<const u32x4*>(lds_v + d * 128 + ((2 * k + h) ^ ((d ^ (d >> 3)) & 7)) * 16);
-        const bool turned = t >> 1 & 1;   // rows whose halves of a chunk are exchanged
-        if constexpr (SPLIT) o[t] = mfma32(vop, turned ? u32x4{rest[2], rest[3], rest[0], rest[1]} : rest, o[t]);
-        o[t] = mfma32(vop, turned ? u32x4{lead[2], lead[3], lead[0], lead[1]} : lead, o[t]);
+        const u32x4 vop = *reinterpret_cast<const u32x4*>(lds + (v_at ^ ((2 * k) ^ (t & 1) * 4) * 16) + t * 32 * 128);
+        if constexpr (SPLIT) o[t] = mfma32(vop, rest, o[t]);
+        o[t] = mfma32(vop, lead, o[t]);
       }
     }
+    lds_barrier();
+    k_at ^= kBuffer;
+    v_at ^= kBuffer;
   }
 
   // Outputs, a wave its own rows, 16 at a time through its quarter of the LDS.
   sum += __shfl_xor(sum, 32, 64);
-  lds_barrier();
   float* region = reinterpret_cast<float*>(lds) + wave * (16 * D);
   const int u = lane % R::kLanes, cc = chunk_of_lane(u);
   for (int part = 0; part < 2; part++) {
