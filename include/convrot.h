@@ -254,9 +254,9 @@ rq_status rq_check_rotq_linear_args(const void *X, int32_t x_dtype, int64_t M, i
  * that were never written are not used.
  *
  * Limits: bits 8 or 4; head_dim 64, 128 or 256; 1 <= kv_heads <= 65535; page_size a power of two
- * in [16, 1024]; 1 <= num_pages < 2^31. Rows are [tokens, heads, head_dim] with the last
- * axis contiguous and strides (in elements) that are multiples of 16 bytes, so keys and values may
- * be slices of one projection's output. Everything said under "Conventions" holds here too. */
+ * in [16, 1024]; 1 <= num_pages < 2^31, a cache of at most 2^46 bytes. Rows are
+ * [tokens, heads, head_dim] with the last axis contiguous and strides (in elements) that are
+ * multiples of 16 bytes, so keys and values may be slices of one projection's output. Everything said under "Conventions" holds here too. */
 typedef struct {
   int32_t bits;        /* 8 or 4 */
   int32_t head_dim;    /* 64, 128 or 256 */
@@ -335,7 +335,9 @@ size_t rq_kv_attention_workspace_size(const rq_kv_attention_params *p, const rq_
 
 /*   workspace  ws_bytes >= rq_kv_attention_workspace_size() bytes, or NULL if that is 0; nothing
  *              in it needs to start at zero, nothing is kept in it between calls. Limit:
- *              total_q * q_heads <= 2^30. */
+ *              total_q * q_heads <= 2^30. A ragged batch of many sequences should give max_q_len:
+ *              without it every sequence is launched as if it had all rows, and more than 2^31
+ *              workgroups are refused (RQ_EUNSUPPORTED). */
 rq_status rq_kv_attention(const rq_kv_attention_params *p, const rq_kv_config *cfg,
                           const void *cache, int64_t num_pages, void *workspace, size_t ws_bytes,
                           void *stream);

@@ -109,6 +109,23 @@ def test_bad_rows_are_refused(call, kw, status):
     assert rq.load().rq_last_error_detail()
 
 
+def test_sizes_that_do_not_fit_64_bits():
+    big = rq.make_kv_cfg(65535, 256, 1024, 8)
+    for call in (write, read):
+        assert call(tokens=1, cfg=big, pages=(1 << 31) - 1, kt=65535 * 256, vt=65535 * 256, kh=256, vh=256) == rq.RQ_EUNSUPPORTED
+    assert attend(cfg=big, q_heads=65535, num_pages=(1 << 31) - 1)[0] == rq.RQ_EUNSUPPORTED
+    # every sequence launched as if it had all rows: more workgroups than a launch holds
+    many = dict(total_q=1 << 24, seqs=65535, q_heads=64, cfg=rq.make_kv_cfg(64, 64), qt=4096, ot=4096, qh=64, oh=64, O=A + (1 << 42),
+                lse=None, ws=None)
+    assert attend(**many)[0] == rq.RQ_EUNSUPPORTED
+
+
+def test_the_stride_of_a_single_row_is_not_looked_at():
+    one = rq.make_kv_cfg(1, 128)
+    assert read(tokens=1, kt=3, vt=0, cfg=one, kh=7, vh=1, slots=None) == rq.RQ_EINVAL
+    assert "slots" in rq.load().rq_last_error_detail().decode()      # all that is wrong with it
+
+
 @pytest.mark.parametrize("kw", [dict(kt=512), dict(kh=64), dict(kt=0), dict(vh=0), dict(kt=128, kh=128), dict(V=A)])
 def test_output_rows_may_not_overlap(kw):
     assert read(**{**dict(tokens=5), **kw}) == rq.RQ_EINVAL

@@ -418,20 +418,17 @@ def make_kv_cfg(kv_heads: int, head_dim: int, page_size: int = 64, bits: int = 4
     return rq_kv_config(bits, head_dim, kv_heads, page_size)
 
 
-def _launch_on(device, stream, call):
-    """call(handle of the stream) with `device` current, and `stream`, where one is given, too: what
-    is allocated meanwhile belongs to it."""
+def _launch_on(index, stream, call):
+    """call(handle of the stream) with device `index` current, and `stream`, where one is given, too:
+    what is allocated meanwhile belongs to it."""
     torch = _torch()
-    if device.type != "cuda":
-        raise ValueError("tensors must be device tensors, got %s" % device)
-    index = device.index
     if stream is None:
         if index == torch.cuda.current_device():
             return call(torch._C._cuda_getCurrentRawStream(index))
         with torch.cuda.device(index):
             return call(torch._C._cuda_getCurrentRawStream(index))
-    if stream.device != device:
-        raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+    if stream.device_index != index:
+        raise ValueError("stream is on device %s, the tensors are on %s" % (stream.device_index, index))
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -466,10 +463,15 @@ def _kv_table(t, name, dtype, shape):
                                                                                      tuple(t.shape)))
 
 
-def _kv_same_device(device, *ts):
+def _kv_device(*ts):
+    """The index of the one device that all tensors are on."""
+    index = ts[0].get_device()
     for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("tensors are on different devices: %s, %s" % (device, t.device))
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors are on different devices: %s, %s" % (ts[0].device, t.device))
+    if index < 0:
+        raise ValueError("tensors must be device tensors, got %s" % ts[0].device)
+    return index
 
 
 def kv_cache_alloc(num_pages: int, cfg: rq_kv_config, device="cuda"):
@@ -492,14 +494,13 @@ def kv_cache_write(K, V, slots, cache, cfg: rq_kv_config, stream=None):
     kt, kh = _kv_rows(K, "K", shape, (torch.float32, torch.float16, torch.bfloat16))
     vt, vh = _kv_rows(V, "V", shape, (K.dtype,))
     _kv_table(slots, "slots", torch.int64, (tokens,))
-    device = cache.device
-    _kv_same_device(device, K, V, slots)
+    index = _kv_device(cache, K, V, slots)
 
     def call(handle):
         _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kt, kh, vt, vh, slots.data_ptr(), cfg,
                                  cache.data_ptr(), pages, handle), "rq_kv_cache_write")
 
-    _launch_on(device, stream, call)
+    _launch_on(index, stream, call)
 
 
 def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, stream=None):
@@ -512,24 +513,23 @@ def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, str
     shape = (tokens, cfg.kv_heads, cfg.head_dim)
     _kv_table(slots, "slots", torch.int64, (tokens,))
     types = (torch.float32, torch.float16, torch.bfloat16)
-    device = cache.device
     if out is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16
         if out_dtype not in types:
             raise ValueError("out_dtype must be float32, float16 or bfloat16")
-        _kv_same_device(device, slots)
+        index = _kv_device(cache, slots)
     else:
         if out_dtype is not None and out[0].dtype != out_dtype:
             raise ValueError("out is %s, out_dtype is %s" % (out[0].dtype, out_dtype))
         kt, kh = _kv_rows(out[0], "K", shape, types)
         vt, vh = _kv_rows(out[1], "V", shape, (out[0].dtype,))
-        _kv_same_device(device, slots, *out)
+        index = _kv_device(cache, slots, *out)
 
     def call(handle):
         if out is None:
-            K = torch.empty(shape, dtype=out_dtype, device=device)
-            V = torch.empty(shape, dtype=out_dtype, device=device)
+            K = cache.new_empty(shape, dtype=out_dtype)
+            V = torch.empty_like(K)
             strides = (shape[1] * shape[2], shape[2]) * 2
         else:
             (K, V), strides = out, (kt, kh, vt, vh)
@@ -537,7 +537,7 @@ def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, str
                                 _dtype_code(K), *strides, handle), "rq_kv_cache_read")
         return K, V
 
-    return _launch_on(device, stream, call)
+    return _launch_on(index, stream, call)
 
 
 def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causal: bool = True, window: int = 0,
@@ -570,12 +570,11 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
         ot, oh = _kv_rows(out, "out", shape, (Q.dtype,))
     else:
         ot, oh = q_heads * dim, dim
-    device = Q.device
-    _kv_same_device(device, cache, pages, kv_len, q_start, out, workspace)
+    index = _kv_device(Q, cache, pages, kv_len, q_start, out, workspace)
 
     def call(handle):
-        O = torch.empty(shape, dtype=Q.dtype, device=device) if out is None else out
-        lse = torch.empty((total, q_heads), dtype=torch.float32, device=device) if return_lse else None
+        O = Q.new_empty(shape) if out is None else out
+        lse = Q.new_empty((total, q_heads), dtype=torch.float32) if return_lse else None
         p = rq_kv_attention_params(
             Q.data_ptr(), O.data_ptr(), None if lse is None else lse.data_ptr(),
             None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
@@ -586,12 +585,12 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
         if ws is not None:
             _check_bytes(ws, "workspace", need, exact=False)
         elif need:
-            ws = torch.empty((need,), dtype=torch.uint8, device=device)
+            ws = cache.new_empty((need,))
         _check(rq_kv_attention(p, cfg, cache.data_ptr(), num_pages, None if ws is None else ws.data_ptr(),
                                0 if ws is None else _nbytes(ws), handle), "rq_kv_attention")
         return (O, lse) if return_lse else O
 
-    return _launch_on(device, stream, call)
+    return _launch_on(index, stream, call)
 
 
 def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages: int, cfg: rq_kv_config,

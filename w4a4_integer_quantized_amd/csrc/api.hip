@@ -268,6 +268,7 @@ rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const
 
 // ---- the cache operators
 constexpr int64_t kMaxKvTokens = int64_t(1) << 30;   // of a sequence's page table
+constexpr int64_t kMaxKvBytes = int64_t(1) << 46;    // of a cache, and of what strided rows span
 constexpr int64_t kMaxKvRows = int64_t(1) << 30;     // query rows times heads
 
 int log2_of(int32_t n) {
@@ -293,11 +294,13 @@ int64_t kv_head_bytes(const rq_kv_config* cfg) {
   return (int64_t)cfg->page_size * (2 * (cfg->head_dim * cfg->bits / 8) + 8);
 }
 
-rq_status check_kv_cache(const void* cache, int64_t num_pages) {
+rq_status check_kv_cache(const void* cache, int64_t num_pages, const rq_kv_config* cfg) {
   rq_status s = check_ptr(cache, "cache");
   if (s) return s;
   if (num_pages < 1 || num_pages > kMaxRowsOrCols)
     return fail(num_pages < 1 ? RQ_EINVAL : RQ_EUNSUPPORTED, "num_pages = %lld (need 1 .. 2^31 - 1)", (long long)num_pages);
+  if (num_pages > kMaxKvBytes / (kv_head_bytes(cfg) * cfg->kv_heads))
+    return fail(RQ_EUNSUPPORTED, "the cache has over 2^46 bytes (%lld pages)", (long long)num_pages);
   return ok();
 }
 
@@ -308,6 +311,8 @@ rq_status check_kv_rows(const void* p, const char* name, int64_t tokens, int64_t
   rq_status s = check_ptr(p, name);
   if (s) return s;
   constexpr int64_t kMost = int64_t(1) << 40;
+  if (tokens == 1) token_stride = 0;   // a single one's stride is never taken
+  if (heads == 1) head_stride = 0;
   if (token_stride < 0 || head_stride < 0 || token_stride > kMost || head_stride > kMost)
     return fail(RQ_EINVAL, "%s strides (%lld, %lld) out of range", name, (long long)token_stride, (long long)head_stride);
   if (token_stride * es % 16 != 0 || head_stride * es % 16 != 0)
@@ -324,7 +329,7 @@ rq_status check_kv_rows(const void* p, const char* name, int64_t tokens, int64_t
       return fail(RQ_EINVAL, "%s strides (%lld, %lld): rows overlap", name, (long long)token_stride, (long long)head_stride);
   }
   const __int128 extent = ((__int128)(tokens - 1) * token_stride + (__int128)(heads - 1) * head_stride + dim) * es;
-  if (extent > (__int128)1 << 46) return fail(RQ_EUNSUPPORTED, "%s spans over 2^46 bytes", name);
+  if (extent > kMaxKvBytes) return fail(RQ_EUNSUPPORTED, "%s spans over 2^46 bytes", name);
   *bytes = (int64_t)extent;
   return ok();
 }
@@ -337,7 +342,7 @@ rq_status check_kv_rw(const void* K, const void* V, int32_t dtype, int64_t token
   if (dtype != RQ_F32 && dtype != RQ_F16 && dtype != RQ_BF16) return fail(RQ_EINVAL, "bad K / V dtype %d", dtype);
   if (tokens < 0) return fail(RQ_EINVAL, "tokens = %lld < 0", (long long)tokens);
   if (tokens > kMaxRowsOrCols) return fail(RQ_EUNSUPPORTED, "tokens = %lld >= 2^31", (long long)tokens);
-  if ((s = check_kv_cache(cache, num_pages))) return s;
+  if ((s = check_kv_cache(cache, num_pages, cfg))) return s;
   if (tokens == 0) return ok();
   const int64_t es = elem_size(dtype);
   int64_t kb = 0, vb = 0;
@@ -410,7 +415,7 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
   int64_t max_q = 0, max_kv = 0;
   rq_status s = check_kv_shape(p, cfg, &max_q, &max_kv);
   if (s) return s;
-  if ((s = check_kv_cache(cache, num_pages))) return s;
+  if ((s = check_kv_cache(cache, num_pages, cfg))) return s;
   if (p->total_q == 0) return ok();
   int64_t qb = 0, ob = 0;
   if ((s = check_kv_rows(p->Q, "Q", p->total_q, p->q_heads, cfg->head_dim, 2, p->q_token_stride, p->q_head_stride, false, &qb)))

@@ -15,6 +15,10 @@ namespace {
 using namespace kv;
 
 constexpr int kThreads = 256;
+// Rows read back beyond this are stored past the caches: they would not stay in them (the L2s hold
+// 32 MiB) until they are used. 65536 tokens, 8 heads of 128 (268 MB): 118 us through the caches,
+// 78 us past them; 5184 tokens, 16 heads of 64 (21 MB): 9.4 us either way.
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
 constexpr float kRoundMagic = 12582912.0f;   // 1.5 * 2^23: its low mantissa bits hold the code
 
 // The block of (page, head) that holds `slot`, and the token's place in it. False if the slot
@@ -51,7 +55,8 @@ __device__ __forceinline__ void codes8(const float (&v)[8], float inv, uint32_t&
 }
 
 // One workgroup: kThreads / kLanes rows, i.e. that many consecutive tokens of one head; gridDim.y
-// is the heads. The keys' row and the values' row of a token are the same lanes' work.
+// is the heads. The keys' row and the values' row of a token are the same lanes' work, both loaded
+// before either is worked on.
 template <int D, int BITS>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a) {
   using R = Row<D, BITS>;
@@ -59,21 +64,26 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (kThreads / R::kLanes) + threadIdx.x / R::kLanes;
   const int64_t tc = t < a.tokens ? t : a.tokens - 1;
   const int head = blockIdx.y;
-  Place p;
-  const bool in = find<D, BITS>(a, a.slots[tc], head, p) && t < a.tokens;
   const int es = elem_bytes(a.dt);
+  float v[2][R::kChunks][8];
 #pragma unroll
   for (int part = 0; part < 2; part++) {   // keys, values
     const uint8_t* x = (part ? a.v : a.k) +
                        (tc * (part ? a.v_token : a.k_token) + head * (part ? a.v_head : a.k_head)) * es;
-    float v[R::kChunks][8], sign = 1.0f, m = 0.0f;
 #pragma unroll
-    for (int b = 0; b < R::kChunks; b++) load8(x + (b * 128 + c * 8) * es, a.dt, v[b]);
+    for (int b = 0; b < R::kChunks; b++) load8(x + (b * 128 + c * 8) * es, a.dt, v[part][b]);
+  }
+  Place p;
+  const bool in = find<D, BITS>(a, a.slots[tc], head, p) && t < a.tokens;
+  const int page = 1 << a.lps;
+#pragma unroll
+  for (int part = 0; part < 2; part++) {
+    float sign = 1.0f, m = 0.0f;
 #pragma unroll
     for (int b = 0; b < R::kChunks; b++) {
-      sign = wht_block<R::kLanes>(v[b], c);
+      sign = wht_block<R::kLanes>(v[part][b], c);
 #pragma unroll
-      for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[b][i]));
+      for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[part][b][i]));
     }
     m = row_max<R::kLanes>(m);
     // A row whose absmax is zero, or too small for fl(q_max / a) to be finite, is a zero row.
@@ -81,13 +91,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a) {
     if (__builtin_isinf(inv)) inv = 0.0f;
     const float scale = inv != 0.0f ? __fdiv_rn(__fmul_rn(m, R::kNorm), R::kQmax) : 0.0f;
     if (!in) continue;   // no exchange follows in this part; the next one takes every lane again
-    const int page = 1 << a.lps;
     if (u == 0)
       reinterpret_cast<float*>(p.block + 2 * (size_t)page * R::kBytes)[part * page + p.off] = scale;
 #pragma unroll
     for (int b = 0; b < R::kChunks; b++) {
       uint32_t lo, hi;
-      codes8<BITS>(v[b], sign * inv, lo, hi);
+      codes8<BITS>(v[part][b], sign * inv, lo, hi);
       const int at = b * (16 * BITS) + c * BITS;   // the chunk's first byte in its row
       if (part == 0) {
         uint8_t* q = p.block + p.off * R::kBytes + at;
@@ -106,7 +115,8 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCacheArgs a) {
 
 // The same rows back: x = fl(fl(scale * c) * WHT(codes)), the transform of the codes exact in
 // binary32, rounded once to the output type. A slot outside the cache gives a row of zeros.
-template <int D, int BITS>
+// STREAM: the outputs go past the caches (kStreamBytes).
+template <int D, int BITS, bool STREAM>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCacheArgs a) {
   using R = Row<D, BITS>;
   const int u = threadIdx.x % R::kLanes, c = chunk_of_lane(u);
@@ -116,44 +126,49 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCacheArgs a) {
   Place p;
   const bool in = find<D, BITS>(a, a.slots[tc], head, p);
   const int es = elem_bytes(a.dt), page = 1 << a.lps;
+  const float* scales = reinterpret_cast<const float*>(p.block + 2 * (size_t)page * R::kBytes) + p.off;
+  const float scale[2] = {scales[0], scales[page]};
+  uint32_t w[2][R::kChunks][2];
+  u32x4 y[R::kChunks][BITS / 4];
+#pragma unroll
+  for (int b = 0; b < R::kChunks; b++) {
+    const int at = b * (16 * BITS) + c * BITS;
+    const uint8_t* q = p.block + p.off * R::kBytes + at;
+    w[0][b][0] = *reinterpret_cast<const uint32_t*>(q);
+    if constexpr (BITS == 8) w[0][b][1] = *reinterpret_cast<const uint32_t*>(q + 4);
+    // Four tokens' V bytes come with each 4-byte column; the neighbouring rows of the wave load
+    // the same 16 bytes, so the lines are read once.
+    q = p.block + (size_t)page * R::kBytes + ((p.off >> 2) * R::kBytes + at) * 4;
+#pragma unroll
+    for (int i = 0; i < BITS / 4; i++) y[b][i] = *reinterpret_cast<const u32x4*>(q + 16 * i);
+  }
+  const uint32_t shift = 8 * (p.off & 3);
+#pragma unroll
+  for (int b = 0; b < R::kChunks; b++) {
+#pragma unroll
+    for (int i = 0; i < BITS / 4; i++)
+      w[1][b][i] = ((y[b][i][0] >> shift) & 0xFFu) | (((y[b][i][1] >> shift) & 0xFFu) << 8) |
+                   (((y[b][i][2] >> shift) & 0xFFu) << 16) | ((y[b][i][3] >> shift) << 24);
+  }
 #pragma unroll
   for (int part = 0; part < 2; part++) {
-    const float* scales = reinterpret_cast<const float*>(p.block + 2 * (size_t)page * R::kBytes);
-    const float s = __fmul_rn(scales[part * page + p.off], R::kNorm);
+    const float s = __fmul_rn(scale[part], R::kNorm);
     uint8_t* x = (part ? a.v_out : a.k_out) +
                  (tc * (part ? a.v_token : a.k_token) + head * (part ? a.v_head : a.k_head)) * es;
 #pragma unroll
     for (int b = 0; b < R::kChunks; b++) {
-      const int at = b * (16 * BITS) + c * BITS;
-      uint32_t w[2];
-      if (part == 0) {
-        const uint8_t* q = p.block + p.off * R::kBytes + at;
-        w[0] = *reinterpret_cast<const uint32_t*>(q);
-        if constexpr (BITS == 8) w[1] = *reinterpret_cast<const uint32_t*>(q + 4);
-      } else {
-        // Four tokens' bytes come with each 4-byte column; the neighbouring rows of the wave
-        // load the same 16 bytes, so the lines are read once.
-        const uint8_t* q = p.block + (size_t)page * R::kBytes + ((p.off >> 2) * R::kBytes + at) * 4;
-        const uint32_t shift = 8 * (p.off & 3);
-#pragma unroll
-        for (int i = 0; i < BITS / 4; i++) {
-          const u32x4 y = *reinterpret_cast<const u32x4*>(q + 16 * i);
-          w[i] = ((y[0] >> shift) & 0xFFu) | (((y[1] >> shift) & 0xFFu) << 8) |
-                 (((y[2] >> shift) & 0xFFu) << 16) | ((y[3] >> shift) << 24);
-        }
-      }
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         if constexpr (BITS == 8)
-          v[i] = static_cast<float>(static_cast<int32_t>(w[i / 4] << (24 - 8 * (i & 3))) >> 24);
+          v[i] = static_cast<float>(static_cast<int32_t>(w[part][b][i / 4] << (24 - 8 * (i & 3))) >> 24);
         else
-          v[i] = static_cast<float>(static_cast<int32_t>(w[0] << (28 - 4 * i)) >> 28);
+          v[i] = static_cast<float>(static_cast<int32_t>(w[part][b][0] << (28 - 4 * i)) >> 28);
       }
-      const float f = s * wht_block<R::kLanes>(v, c);
+      const float sign = wht_block<R::kLanes>(v, c), f = in ? s * sign : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = in ? __fmul_rn(f, v[i]) : 0.0f;
-      if (t < a.tokens) store8(x + (b * 128 + c * 8) * es, a.dt, v);
+      for (int i = 0; i < 8; i++) v[i] = __fmul_rn(f, v[i]);
+      if (t < a.tokens) store8<STREAM>(x + (b * 128 + c * 8) * es, a.dt, v);
     }
   }
 }
@@ -164,8 +179,10 @@ hipError_t launch(const KvCacheArgs& a, bool write, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.tokens + kRows - 1) / kRows), static_cast<unsigned>(a.heads));
   if (write)
     kv_write_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
+  else if (2 * a.tokens * a.heads * D * (a.dt == kF32 ? 4 : 2) > kStreamBytes)
+    kv_read_kernel<D, BITS, true><<<grid, kThreads, 0, stream>>>(a);
   else
-    kv_read_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
+    kv_read_kernel<D, BITS, false><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

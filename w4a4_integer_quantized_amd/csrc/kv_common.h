@@ -60,16 +60,26 @@ __device__ __forceinline__ float wht_block(float (&v)[8], int c) {
   }
   const float m0 = (c & 1) ? -1.0f : 1.0f, m1 = (c & 2) ? -1.0f : 1.0f;
   const float m2 = (c & 4) ? -1.0f : 1.0f, m3 = (c & 8) ? -1.0f : 1.0f;
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(dpp_f<0xB1>(v[i]), m0, v[i]);    // quad_perm [1,0,3,2]
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(dpp_f<0x4E>(v[i]), m1, v[i]);    // quad_perm [2,3,0,1]
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(dpp_f<0x141>(v[i]), m2, v[i]);   // row_half_mirror
-  if constexpr (LANES == 16) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(dpp_f<0x128>(v[i]), m3, v[i]); // row_ror:8
-  }
+  // v = fma(partner's v, m, v), the exchange an operand modifier of the fma (the compiler moves the
+  // value first). A lane exchange must not follow the write of what it reads by less than two
+  // instructions: the nop stands for what came before, and eight values keep each other apart.
+#define KV_EXCHANGE(CTRL, M)                                                                                    \
+  asm volatile("s_nop 1\n\t"                                                                                             \
+      "v_fmac_f32_dpp %0, %0, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %1, %1, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %2, %2, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %3, %3, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %4, %4, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %5, %5, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %6, %6, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                       \
+      "v_fmac_f32_dpp %7, %7, %8 " CTRL " row_mask:0xf bank_mask:0xf"                                           \
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])            \
+      : "v"(M))
+  KV_EXCHANGE("quad_perm:[1,0,3,2]", m0);
+  KV_EXCHANGE("quad_perm:[2,3,0,1]", m1);
+  KV_EXCHANGE("row_half_mirror", m2);
+  if constexpr (LANES == 16) KV_EXCHANGE("row_ror:8", m3);
+#undef KV_EXCHANGE
   return (__builtin_popcount(c) & 1) ? -1.0f : 1.0f;
 }
 
@@ -115,7 +125,17 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
 
-// 8 consecutive values -> 8 elements of type dt at p (one rounding, to nearest even).
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint8_t* p, const u32x4& a) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(a, reinterpret_cast<u32x4*>(p));
+  else
+    *reinterpret_cast<u32x4*>(p) = a;
+}
+
+// 8 consecutive values -> 8 elements of type dt at p (one rounding, to nearest even). STREAM: past
+// the caches.
+template <bool STREAM = false>
 __device__ __forceinline__ void store8(uint8_t* p, int dt, const float (&v)[8]) {
   u32x4 a, b;
   if (dt == kF32) {
@@ -124,8 +144,8 @@ __device__ __forceinline__ void store8(uint8_t* p, int dt, const float (&v)[8]) 
       a[i] = __float_as_uint(v[i]);
       b[i] = __float_as_uint(v[4 + i]);
     }
-    *reinterpret_cast<u32x4*>(p) = a;
-    *reinterpret_cast<u32x4*>(p + 16) = b;
+    store16<STREAM>(p, a);
+    store16<STREAM>(p + 16, b);
     return;
   }
 #pragma unroll
@@ -137,7 +157,7 @@ __device__ __forceinline__ void store8(uint8_t* p, int dt, const float (&v)[8]) 
       a[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
     }
   }
-  *reinterpret_cast<u32x4*>(p) = a;
+  store16<STREAM>(p, a);
 }
 
 __device__ __forceinline__ int elem_bytes(int dt) { return dt == kF32 ? 4 : 2; }
