@@ -1231,19 +1231,23 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
   const int tile_rows = p.block ? kBlockRows : kRows;
   const int64_t tiles = (max_q_len * group + tile_rows - 1) / tile_rows;
   p.row_tiles = static_cast<int>(tiles < 1 ? 1 : tiles);
-  // Enough workgroups for 256 compute units several times over, none with fewer than kMinChunk
-  // keys. A split takes the same number of keys in every sequence, and at least kMinChunk: of a
-  // long sequence beside short ones no workgroup has more than its share. Measured (64 sequences
-  // up to 8192 tokens, 8 heads / 4 up to 131072, one of them most of the work): 768 workgroups 77 /
-  // 66 us, 1024 77 / 80, 2048 76 / 59, 4096 81 / 80.
+  // Enough workgroups for 256 compute units several times over. A split takes the same number of
+  // keys in every sequence, the longest's share and at most kMinChunk where that is less: of a long
+  // sequence beside short ones no workgroup has more than its share, and the short ones' are few.
+  // Stream kernel (64 sequences up to 8192 tokens, 8 heads / 4 up to 131072, one of them most of the
+  // work): 768 workgroups 77 / 66 us, 1024 77 / 80, 2048 76 / 59, 4096 81 / 80. Block kernel: two a
+  // compute unit. A join costs about 5 us and each row of it some more: splits have 512 keys at
+  // least; 256 with few blocks (300 rows over 1500 keys, 8 heads: 45 us with 512, 34 with 256; 512
+  // rows of 4 heads each over 512 keys, 8 key heads: 28 unsplit, 40 with 256), and 2048 with enough
+  // groups already, where a split only spares the wait for the longest.
   int64_t span = max_kv_len;
   if (window > 0 && window + max_q_len < span) span = window + max_q_len;
   const int64_t groups = (int64_t)seqs * heads * p.row_tiles, want = p.block ? 512 / groups : (2048 + groups - 1) / groups;
-  // With enough groups already, only what the longest would hold up is worth a join.
-  const int64_t most = span / (groups < 1024 ? 512 : 2048);
+  const int64_t most = span / (groups >= 1024 ? 2048 : p.block && groups < 96 ? 256 : 512);
   const int64_t splits = want < most ? want : most;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
-  p.chunk = kMinChunk;
+  const int64_t share = (span + p.splits - 1) / p.splits;
+  p.chunk = static_cast<int>(share < kMinChunk ? (share + 127) / 128 * 128 : kMinChunk);
   p.workspace_bytes = p.splits > 1 ? (size_t)total_q * q_heads * p.splits * (head_dim + 2) * 4 : 0;
   return p;
 }
