@@ -418,26 +418,43 @@ def make_kv_cfg(kv_heads: int, head_dim: int, page_size: int = 64, bits: int = 4
     return rq_kv_config(bits, head_dim, kv_heads, page_size)
 
 
-def _launch_on(index, stream, call):
-    """call(handle of the stream) with device `index` current, and `stream`, where one is given, too:
-    what is allocated meanwhile belongs to it."""
-    torch = _torch()
+class _Kv:
+    """What the wrappers take from torch, looked up once: dtype codes and accessors."""
+
+    def __init__(self):
+        torch = _torch()
+        self.rows = {torch.float32: RQ_F32, torch.float16: RQ_F16, torch.bfloat16: RQ_BF16}
+        self.halves = {torch.float16: RQ_F16, torch.bfloat16: RQ_BF16}
+        self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
+        self.empty_like, self.cuda = torch.empty_like, torch.cuda
+        self.current_device, self.raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
+_kv_torch = None
+
+
+def _kv() -> _Kv:
+    global _kv_torch
+    if _kv_torch is None:
+        _kv_torch = _Kv()
+    return _kv_torch
+
+
+def _kv_placed(kv, index, stream):
+    """Context in which `index` is the current device and `stream`, where one is given, its current
+    stream (what is allocated meanwhile belongs to it)."""
     if stream is None:
-        if index == torch.cuda.current_device():
-            return call(torch._C._cuda_getCurrentRawStream(index))
-        with torch.cuda.device(index):
-            return call(torch._C._cuda_getCurrentRawStream(index))
+        return kv.cuda.device(index)
     if stream.device_index != index:
         raise ValueError("stream is on device %s, the tensors are on %s" % (stream.device_index, index))
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+    return kv.cuda.stream(stream)
 
 
-def _kv_cache(cache, cfg):
+def _kv_cache(kv, cache, cfg):
     """The number of pages of a uint8 cache [pages, rq_kv_page_bytes(cfg)]."""
     shape = cache.shape
     if (len(shape) != 2 or shape[1] != cfg.kv_heads * cfg.page_size * (cfg.head_dim * cfg.bits // 8 * 2 + 8)
-            or cache.dtype != _torch().uint8 or not cache.is_contiguous()):
+            or cache.dtype != kv.uint8 or not cache.is_contiguous()):
         if rq_kv_page_bytes(cfg) == 0:
             raise ConvRotError(RQ_EUNSUPPORTED, "rq_kv_page_bytes", load().rq_last_error_detail().decode())
         raise ValueError("cache must be a contiguous uint8 tensor [pages, %d], got %s %s"
@@ -451,10 +468,10 @@ def _kv_rows(t, name, shape, dtypes):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s dtype %s (expected one of %s)" % (name, t.dtype, ", ".join(map(str, dtypes))))
-    stride = t.stride()
-    if stride[2] != 1:
+    token, head, last = t.stride()
+    if last != 1:
         raise ValueError("%s must be contiguous along its last axis" % name)
-    return stride[0], stride[1]
+    return token, head
 
 
 def _kv_table(t, name, dtype, shape):
@@ -487,57 +504,57 @@ def kv_cache_write(K, V, slots, cache, cfg: rq_kv_config, stream=None):
     """Rotate, quantise and write keys and values [tokens, kv_heads, head_dim] (f32/f16/bf16, any
     strides of 16 bytes' multiples, last axis contiguous) at slots [tokens] (int64, on the device)
     of `cache`, in place. A slot outside the cache (-1) skips its token; the others must differ."""
-    torch = _torch()
-    pages = _kv_cache(cache, cfg)
+    kv = _kv()
+    pages = _kv_cache(kv, cache, cfg)
     tokens = slots.shape[0] if slots.dim() == 1 else -1
     shape = (tokens, cfg.kv_heads, cfg.head_dim)
-    kt, kh = _kv_rows(K, "K", shape, (torch.float32, torch.float16, torch.bfloat16))
-    vt, vh = _kv_rows(V, "V", shape, (K.dtype,))
-    _kv_table(slots, "slots", torch.int64, (tokens,))
+    kt, kh = _kv_rows(K, "K", shape, kv.rows)
+    dtype = K.dtype
+    vt, vh = _kv_rows(V, "V", shape, (dtype,))
+    _kv_table(slots, "slots", kv.int64, (tokens,))
     index = _kv_device(cache, K, V, slots)
-
-    def call(handle):
-        _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kt, kh, vt, vh, slots.data_ptr(), cfg,
-                                 cache.data_ptr(), pages, handle), "rq_kv_cache_write")
-
-    _launch_on(index, stream, call)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return kv_cache_write(K, V, slots, cache, cfg)
+    _check(rq_kv_cache_write(K.data_ptr(), V.data_ptr(), kv.rows[dtype], tokens, kt, kh, vt, vh, slots.data_ptr(), cfg,
+                             cache.data_ptr(), pages, kv.raw_stream(index)), "rq_kv_cache_write")
 
 
 def kv_cache_read(cache, slots, cfg: rq_kv_config, out_dtype=None, out=None, stream=None):
     """(K, V) [tokens, kv_heads, head_dim] that `cache` holds at slots [tokens] (int64, on the
     device), in out_dtype (default bfloat16) or into the pair `out`. A slot outside the cache gives
     zeros."""
-    torch = _torch()
-    pages = _kv_cache(cache, cfg)
+    kv = _kv()
+    pages = _kv_cache(kv, cache, cfg)
     tokens = slots.shape[0] if slots.dim() == 1 else -1
-    shape = (tokens, cfg.kv_heads, cfg.head_dim)
-    _kv_table(slots, "slots", torch.int64, (tokens,))
-    types = (torch.float32, torch.float16, torch.bfloat16)
+    heads, dim = cfg.kv_heads, cfg.head_dim
+    shape = (tokens, heads, dim)
+    _kv_table(slots, "slots", kv.int64, (tokens,))
     if out is None:
         if out_dtype is None:
-            out_dtype = torch.bfloat16
-        if out_dtype not in types:
+            out_dtype = _torch().bfloat16
+        if out_dtype not in kv.rows:
             raise ValueError("out_dtype must be float32, float16 or bfloat16")
+        kt = vt = heads * dim
+        kh = vh = dim
         index = _kv_device(cache, slots)
     else:
-        if out_dtype is not None and out[0].dtype != out_dtype:
-            raise ValueError("out is %s, out_dtype is %s" % (out[0].dtype, out_dtype))
-        kt, kh = _kv_rows(out[0], "K", shape, types)
-        vt, vh = _kv_rows(out[1], "V", shape, (out[0].dtype,))
-        index = _kv_device(cache, slots, *out)
-
-    def call(handle):
-        if out is None:
-            K = cache.new_empty(shape, dtype=out_dtype)
-            V = torch.empty_like(K)
-            strides = (shape[1] * shape[2], shape[2]) * 2
-        else:
-            (K, V), strides = out, (kt, kh, vt, vh)
-        _check(rq_kv_cache_read(cache.data_ptr(), pages, slots.data_ptr(), tokens, cfg, K.data_ptr(), V.data_ptr(),
-                                _dtype_code(K), *strides, handle), "rq_kv_cache_read")
-        return K, V
-
-    return _launch_on(index, stream, call)
+        K, V = out
+        if out_dtype is not None and K.dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype is %s" % (K.dtype, out_dtype))
+        kt, kh = _kv_rows(K, "K", shape, kv.rows)
+        out_dtype = K.dtype
+        vt, vh = _kv_rows(V, "V", shape, (out_dtype,))
+        index = _kv_device(cache, slots, K, V)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return kv_cache_read(cache, slots, cfg, out_dtype, out)
+    if out is None:
+        K = cache.new_empty(shape, dtype=out_dtype)
+        V = kv.empty_like(K)
+    _check(rq_kv_cache_read(cache.data_ptr(), pages, slots.data_ptr(), tokens, cfg, K.data_ptr(), V.data_ptr(),
+                            kv.rows[out_dtype], kt, kh, vt, vh, kv.raw_stream(index)), "rq_kv_cache_read")
+    return K, V
 
 
 def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causal: bool = True, window: int = 0,
@@ -552,45 +569,53 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
     left as they were; max_kv_len: the most cached tokens of one, to split the work by. They
     default to what the shapes allow; a ragged batch is faster with them. workspace: a uint8 tensor
     of kv_attention_workspace_size() bytes or more. See rq_kv_attention in convrot.h."""
-    torch = _torch()
-    num_pages = _kv_cache(cache, cfg)
+    kv = _kv()
+    num_pages = _kv_cache(kv, cache, cfg)
     shape = Q.shape
     if len(shape) != 3 or shape[2] != cfg.head_dim:
         raise ValueError("Q must be [total_q, q_heads, %d], got %s" % (cfg.head_dim, tuple(shape)))
     total, q_heads, dim = shape
-    qt, qh = _kv_rows(Q, "Q", shape, (torch.float16, torch.bfloat16))
-    if pages.dim() != 2:
-        raise ValueError("pages must be [seqs, max_pages], got %s" % (tuple(pages.shape),))
-    seqs, max_pages = pages.shape
-    _kv_table(pages, "pages", torch.int32, (seqs, max_pages))
-    _kv_table(kv_len, "kv_len", torch.int32, (seqs,))
+    qt, qh = _kv_rows(Q, "Q", shape, kv.halves)
+    dtype = Q.dtype
+    tables = pages.shape
+    if len(tables) != 2:
+        raise ValueError("pages must be [seqs, max_pages], got %s" % (tuple(tables),))
+    seqs, max_pages = tables
+    _kv_table(pages, "pages", kv.int32, tables)
+    _kv_table(kv_len, "kv_len", kv.int32, (seqs,))
     if q_start is not None:
-        _kv_table(q_start, "q_start", torch.int32, (seqs + 1,))
+        _kv_table(q_start, "q_start", kv.int32, (seqs + 1,))
     if out is not None:
-        ot, oh = _kv_rows(out, "out", shape, (Q.dtype,))
+        ot, oh = _kv_rows(out, "out", shape, (dtype,))
     else:
         ot, oh = q_heads * dim, dim
     index = _kv_device(Q, cache, pages, kv_len, q_start, out, workspace)
-
-    def call(handle):
-        O = Q.new_empty(shape) if out is None else out
-        lse = Q.new_empty((total, q_heads), dtype=torch.float32) if return_lse else None
-        p = rq_kv_attention_params(
-            Q.data_ptr(), O.data_ptr(), None if lse is None else lse.data_ptr(),
-            None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
-            max_q_len, max_kv_len, _dtype_code(Q), q_heads, seqs, max_pages, bool(causal), window,
-            dim ** -0.5 if softmax_scale is None else softmax_scale)
-        need = rq_kv_attention_workspace_size(p, cfg)
-        ws = workspace      # held until the launch; later uses of its memory follow on this stream
-        if ws is not None:
-            _check_bytes(ws, "workspace", need, exact=False)
-        elif need:
-            ws = cache.new_empty((need,))
-        _check(rq_kv_attention(p, cfg, cache.data_ptr(), num_pages, None if ws is None else ws.data_ptr(),
-                               0 if ws is None else _nbytes(ws), handle), "rq_kv_attention")
-        return (O, lse) if return_lse else O
-
-    return _launch_on(index, stream, call)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return kv_attention(Q, cache, pages, kv_len, cfg, q_start, causal, window, softmax_scale, max_q_len, max_kv_len,
+                                return_lse, out, workspace)
+    if out is None:
+        out = Q.new_empty(shape)
+    lse = Q.new_empty((total, q_heads), dtype=_torch().float32) if return_lse else None
+    p = rq_kv_attention_params(
+        Q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
+        max_q_len, max_kv_len, kv.halves[dtype], q_heads, seqs, max_pages, bool(causal), window,
+        dim ** -0.5 if softmax_scale is None else softmax_scale)
+    at, handle = cache.data_ptr(), kv.raw_stream(index)
+    if workspace is None:
+        # Most short calls need none: asked for only when the call says so (nothing is launched then).
+        status = rq_kv_attention(p, cfg, at, num_pages, None, 0, handle)
+        if status == RQ_EWORKSPACE:
+            # Held until the launch; later uses of its memory follow on this stream.
+            need = rq_kv_attention_workspace_size(p, cfg)
+            workspace = cache.new_empty((need,))
+            status = rq_kv_attention(p, cfg, at, num_pages, workspace.data_ptr(), need, handle)
+    else:
+        _check_bytes(workspace, "workspace", rq_kv_attention_workspace_size(p, cfg), exact=False)
+        status = rq_kv_attention(p, cfg, at, num_pages, workspace.data_ptr(), _nbytes(workspace), handle)
+    _check(status, "rq_kv_attention")
+    return (out, lse) if return_lse else out
 
 
 def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages: int, cfg: rq_kv_config,
