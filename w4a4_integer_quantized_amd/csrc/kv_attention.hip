@@ -35,7 +35,7 @@ constexpr int kMinChunk = 1024;     // keys
 // stream / block: 16 sequences of 4096 tokens, 48 rows 54 / 71 us, 64 rows 61 / 67, 96 rows 82 / 73;
 // 2 of 16384, 64 rows 37 / 46, 96 rows 54 / 49.
 constexpr int kStreamRows = 64;
-constexpr int kWaves = 4;
+constexpr int kSteps = 2;          // 16-token steps of a stream tile
 constexpr int kRows = 16;          // query rows of a tile: (token, head of the group) pairs
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -181,11 +181,11 @@ struct Geometry {
   static constexpr int kTilesD = D / 16;                                     // 16-wide tiles of the output
 };
 
-// A tile of keys as a wave holds it: STEPS times 16 tokens.
-template <int D, int BITS, int STEPS>
+// A tile of keys as a wave holds it: kSteps times 16 tokens.
+template <int D, int BITS>
 struct Tile {
   using G = Geometry<D, BITS>;
-  uint32_t k[STEPS][G::kLoads][G::kWords], v[STEPS][G::kLoads][G::kWords];
+  uint32_t k[kSteps][G::kLoads][G::kWords], v[kSteps][G::kLoads][G::kWords];
   float ks, vs;   // scales, spread over a row of 16 lanes: of token 16 (r / 4) + 4 g + r % 4
   uint32_t ok;    // bit j: step j's page is in the cache
 };
@@ -196,26 +196,24 @@ __device__ __forceinline__ float row_lane(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x150 + N, 0xF, 0xF, true));
 }
 // a[j][i] = b[j][i] times the scale of step j's token 4g + i.
-template <int STEPS, int N = 0>
-__device__ __forceinline__ void times_scale(float (&a)[STEPS][4], const float (&b)[STEPS][4], float scale) {
-  if constexpr (N < 4 * STEPS) {
+template <int N = 0>
+__device__ __forceinline__ void times_scale(float (&a)[kSteps][4], const float (&b)[kSteps][4], float scale) {
+  if constexpr (N < 4 * kSteps) {
     a[N / 4][N % 4] = row_lane<N>(scale) * b[N / 4][N % 4];
-    times_scale<STEPS, N + 1>(a, b, scale);
+    times_scale<N + 1>(a, b, scale);
   }
 }
 
 // Page table entries of a tile's steps, read through the scalar cache. Steps past the table's end
 // take its last entry (their tokens are masked: they lie behind kv_len).
-template <int STEPS>
 struct Pages {
-  int at[STEPS];
+  int at[kSteps];
 };
-template <int STEPS>
-__device__ __forceinline__ Pages<STEPS> tile_pages(const KvAttentionArgs& a, ConstTable table, int tile) {
-  Pages<STEPS> p;
+__device__ __forceinline__ Pages tile_pages(const KvAttentionArgs& a, ConstTable table, int tile) {
+  Pages p;
 #pragma unroll
-  for (int j = 0; j < STEPS; j++) {
-    const int at = (tile * STEPS + j) * 16 >> a.lps;
+  for (int j = 0; j < kSteps; j++) {
+    const int at = (tile * kSteps + j) * 16 >> a.lps;
     p.at[j] = table[at < a.max_pages ? at : a.max_pages - 1];
   }
   return p;
@@ -239,23 +237,23 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 // columns kLoad / 4 * r ..: each load instruction of the wave reads 64 * kLoad contiguous bytes,
 // and what arrives is the matrix operand but for the conversion: no exchange between lanes. A page
 // index outside the cache loads from page 0; its tokens are masked.
-template <int D, int BITS, int STEPS>
-__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const Pages<STEPS>& pages, int head, int tile,
-                                          int r, int g, Tile<D, BITS, STEPS>& t) {
+template <int D, int BITS>
+__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, const Pages& pages, int head, int tile,
+                                          int r, int g, Tile<D, BITS>& t) {
   using G = Geometry<D, BITS>;
   using R = Row<D, BITS>;
   const int page = 1 << a.lps;
   const uint32_t k_lane = r * R::kBytes + g * G::kLoad, v_lane = g * (4 * R::kBytes) + r * G::kLoad;
-  const int s_step = r >> 2 < STEPS ? r >> 2 : 0;   // with fewer than four steps some lanes repeat
+  const int s_step = r >> 2 < kSteps ? r >> 2 : 0;   // with fewer than four steps some lanes repeat
   const uint8_t* s_at = nullptr;
   t.ok = 0;
 #pragma unroll
-  for (int j = 0; j < STEPS; j++) {
+  for (int j = 0; j < kSteps; j++) {
     const int pg = pages.at[j];
     const bool ok = pg >= 0 && pg < a.num_pages;
     t.ok |= ok ? 1u << j : 0u;
     const uint8_t* block = a.cache + ((int64_t)(ok ? pg : 0) * a.heads + head) * a.head_bytes;
-    const int off = (tile * STEPS + j) * 16 & (page - 1);
+    const int off = (tile * kSteps + j) * 16 & (page - 1);
     // One scalar base a step, 32-bit lane offsets.
     const uint32_t kp = off * R::kBytes + k_lane, vp = (page + off) * R::kBytes + v_lane;
     const uint8_t* sp = block + (2 * page * R::kBytes + off * 4);
@@ -309,13 +307,13 @@ __device__ __forceinline__ void start(State<D, BITS>& s) {
   s.l = 0.0f;
 }
 
-template <int D, int BITS, int STEPS, bool SPLIT>
-__device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
+template <int D, int BITS, bool SPLIT>
+__device__ __forceinline__ void attend_tile(Tile<D, BITS>& t, const u32x4 (&q)[D / 32], const u32x4 (&q2)[D / 32],
                                             float c, bool full, int r, int first, int lo, int hi, int kv_len, State<D, BITS>& s) {
   using G = Geometry<D, BITS>;
-  float x[STEPS][4], p[STEPS][4], w[STEPS][4];
+  float x[kSteps][4], p[kSteps][4], w[kSteps][4];
 #pragma unroll
-  for (int j = 0; j < STEPS; j++) {
+  for (int j = 0; j < kSteps; j++) {
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int op = 0; op < G::kOps; op++) {
@@ -336,14 +334,14 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
 #pragma unroll
     for (int i = 0; i < 4; i++) x[j][i] = acc[i];
   }
-  times_scale<STEPS>(x, x, t.ks);
+  times_scale(x, x, t.ks);
   if (!full) {   // the same in every lane
     asm volatile("");   // a branch, not selects in every tile
     const int mine = first + 16 * (r >> 2) + (r & 3);   // `first` includes 4 g
-    const uint32_t step = r >> 2 < STEPS ? r >> 2 : 0;
+    const uint32_t step = r >> 2 < kSteps ? r >> 2 : 0;
     t.vs = mine < kv_len && (t.ok >> step & 1u) ? t.vs : 0.0f;
 #pragma unroll
-    for (int j = 0; j < STEPS; j++) {
+    for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int key = first + 16 * j + i;
@@ -359,16 +357,16 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
     float wtop = 0.0f;
     l = s.l;
 #pragma unroll
-    for (int j = 0; j < STEPS; j++) {
+    for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         p[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], c, -s.b));
         l += p[j][i];
       }
     }
-    times_scale<STEPS>(w, p, t.vs);
+    times_scale(w, p, t.vs);
 #pragma unroll
-    for (int j = 0; j < STEPS; j++) {
+    for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) wtop = fmaxf(wtop, w[j][i]);
     }
@@ -377,15 +375,15 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
   if (!__all(weigh())) {
     // The logarithm of the tile's largest weight, and its largest logit, over the row's four lanes.
     const float lv = t.vs > 0.0f ? __builtin_amdgcn_logf(t.vs) : neg_inf();
-    float one[STEPS][4], wl = neg_inf(), top = neg_inf();
+    float one[kSteps][4], wl = neg_inf(), top = neg_inf();
 #pragma unroll
-    for (int j = 0; j < STEPS; j++) {
+    for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) one[j][i] = 1.0f;
     }
-    times_scale<STEPS>(p, one, lv);
+    times_scale(p, one, lv);
 #pragma unroll
-    for (int j = 0; j < STEPS; j++) {
+    for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         top = fmaxf(top, x[j][i]);
@@ -405,7 +403,7 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS, STEPS>& t, const u32x4
   }
   s.l = l;
 #pragma unroll
-  for (int j = 0; j < STEPS; j += 2) {
+  for (int j = 0; j < kSteps; j += 2) {
     const u32x4 hi = {pack_f16(w[j][0], w[j][2]), pack_f16(w[j][1], w[j][3]),
                       pack_f16(w[j + 1][0], w[j + 1][2]), pack_f16(w[j + 1][1], w[j + 1][3])};
     u32x4 rest;
@@ -456,15 +454,15 @@ __device__ __forceinline__ void store_row(uint8_t* p, int dt, float (&v)[Row<D, 
 }
 
 // One workgroup: a tile of 16 query rows of one key head and sequence, and one split of its keys.
-// The four waves take the split's tiles of keys in turn, each with a softmax of its own; they are
-// joined through LDS, and splits through the workspace (kv_join_kernel).
-template <int D, int BITS, int STEPS, bool SPLIT>
-__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kernel(KvAttentionArgs a) {
+// The waves take the split's tiles of keys in turn, each with a softmax of its own; they are joined
+// through LDS, and splits through the workspace (kv_join_kernel).
+template <int D, int BITS, bool SPLIT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel(KvAttentionArgs a) {
   using R = Row<D, BITS>;
   using G = Geometry<D, BITS>;
-  constexpr int kOutPad = 4, kTile = 16 * STEPS;
-  __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows][D + kOutPad];
-  __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows], lds_c[kRows];
+  constexpr int kOutPad = 4, kTile = 16 * kSteps;
+  __shared__ __attribute__((aligned(16))) float lds_o[WAVES][kRows][D + kOutPad];
+  __shared__ float lds_m[WAVES][kRows], lds_l[WAVES][kRows], lds_c[kRows];
   uint32_t* lds_q = reinterpret_cast<uint32_t*>(lds_o);   // [2][kRows][D / 2], before the first key
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -510,13 +508,13 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
   // Past the end the last tile is loaded again: loads under a condition would have to be waited
   // for as soon as they are issued. The first tile is under way before the queries are.
   int i = begin + wave;
-  auto next = [&](int at) { return at + kWaves < end ? at + kWaves : at; };
+  auto next = [&](int at) { return at + WAVES < end ? at + WAVES : at; };
   // (A wave without tiles loads the last one too, and does not use it.)
-  Tile<D, BITS, STEPS> t0, t1;
-  Pages<STEPS> pages = tile_pages<STEPS>(a, table, i < end ? i : end - 1);
-  load_tile<D, BITS, STEPS>(a, pages, head, i < end ? i : end - 1, r, g, t0);
+  Tile<D, BITS> t0, t1;
+  Pages pages = tile_pages(a, table, i < end ? i : end - 1);
+  load_tile<D, BITS>(a, pages, head, i < end ? i : end - 1, r, g, t0);
   int n = next(i);
-  pages = tile_pages<STEPS>(a, table, n < end ? n : end - 1);
+  pages = tile_pages(a, table, n < end ? n : end - 1);
   // Queries: rotated, scaled, to fp16, in the K operands' element order.
   {
     const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
@@ -565,22 +563,22 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
   State<D, BITS> st;
   start(st);
   if (i < end) {
-    auto attend = [&](Tile<D, BITS, STEPS>& t, int at) {
+    auto attend = [&](Tile<D, BITS>& t, int at) {
       const int first = at * kTile;
-      const bool full = whole && t.ok == (1u << STEPS) - 1 && first >= full_lo && first + kTile <= full_hi;
-      attend_tile<D, BITS, STEPS, SPLIT>(t, q, q2, c, full, r, first + 4 * g, lo, hi, s.kv_len, st);
+      const bool full = whole && t.ok == (1u << kSteps) - 1 && first >= full_lo && first + kTile <= full_hi;
+      attend_tile<D, BITS, SPLIT>(t, q, q2, c, full, r, first + 4 * g, lo, hi, s.kv_len, st);
     };
     while (true) {
-      load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t1);
+      load_tile<D, BITS>(a, pages, head, n, r, g, t1);
       int m = next(n);
-      pages = tile_pages<STEPS>(a, table, m);
+      pages = tile_pages(a, table, m);
       attend(t0, i);
       if (n == i) break;
       i = n;
       n = m;
-      load_tile<D, BITS, STEPS>(a, pages, head, n, r, g, t0);
+      load_tile<D, BITS>(a, pages, head, n, r, g, t0);
       m = next(n);
-      pages = tile_pages<STEPS>(a, table, m);
+      pages = tile_pages(a, table, m);
       attend(t1, i);
       if (n == i) break;
       i = n;
@@ -597,7 +595,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
   __syncthreads();
   float top = lds_m[0][r];
 #pragma unroll
-  for (int w = 1; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
+  for (int w = 1; w < WAVES; w++) top = fmaxf(top, lds_m[w][r]);
   {
     const float m = lds_m[wave][r];
     const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
@@ -615,9 +613,9 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
     const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
     float best = neg_inf(), sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) best = fmaxf(best, lds_m[w][rc]);
+    for (int w = 0; w < WAVES; w++) best = fmaxf(best, lds_m[w][rc]);
 #pragma unroll
-    for (int w = 0; w < kWaves; w++)
+    for (int w = 0; w < WAVES; w++)
       sum += lds_m[w][rc] == neg_inf() ? 0.0f : lds_l[w][rc] * __builtin_amdgcn_exp2f(lds_m[w][rc] - best);
     float v[R::kChunks][8];
 #pragma unroll
@@ -626,7 +624,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void kv_attend_kerne
       for (int i = 0; i < 8; i++) {
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; w++) y += lds_o[w][rc][k * 128 + chunk * 8 + i];
+        for (int w = 0; w < WAVES; w++) y += lds_o[w][rc][k * 128 + chunk * 8 + i];
         v[k][i] = y;
       }
     }
@@ -1198,10 +1196,23 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
 template <int D, int BITS>
 void launch_stream(const KvAttentionArgs& a, hipStream_t stream) {
   const dim3 grid(((unsigned)a.splits * a.seqs + kXcds - 1) / kXcds * kXcds * a.row_tiles * a.heads);
+  // With a workgroup for each compute unit or fewer, eight waves share a split's keys: a wave's tiles
+  // come one behind the other, each a trip to memory (one token over 2048, 2 key heads of 128, in a
+  // graph: 19.9 us with four waves, 16.3 with eight; over 128 tokens 6.5 both). With more workgroups
+  // four: the registers hold twelve waves a unit, and hold no eight of head_dim 256 at all.
+  if constexpr (D < 256) {
+    if (grid.x <= 256) {
+      if (a.dt == kF16)
+        kv_attend_kernel<D, BITS, true, 8><<<grid, 512, 0, stream>>>(a);
+      else
+        kv_attend_kernel<D, BITS, false, 8><<<grid, 512, 0, stream>>>(a);
+      return;
+    }
+  }
   if (a.dt == kF16)
-    kv_attend_kernel<D, BITS, 2, true><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, true, 4><<<grid, 256, 0, stream>>>(a);
   else
-    kv_attend_kernel<D, BITS, 2, false><<<grid, kWaves * 64, 0, stream>>>(a);
+    kv_attend_kernel<D, BITS, false, 4><<<grid, 256, 0, stream>>>(a);
 }
 
 template <int D, int BITS>
