@@ -237,6 +237,31 @@ def test_long_caches_are_split(dim, bits, dtype):
     check(c, cfg, Q, pages, kv_len, [4, 1, 4], dtype, window=900, max_q_len=4)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim,bits", [(64, 4), (128, 8), (128, 4), (256, 8)])
+def test_chunks_over_long_caches_are_split(dim, bits, dtype):
+    kv_len, q_len = [2500, 70, 1300], [25, 1, 19]
+    rng, c, cfg = make(dim, bits, 64, heads=1, pages=64)
+    pages = fill(rng, c, kv_len)
+    assert rq.kv_attention_workspace_size(45, 4, 3, pages.shape[1], cfg, ragged=True, max_q_len=25) > 0
+    Q = rng.normal(size=(sum(q_len) + 3, 4, dim))
+    check(c, cfg, Q, pages, kv_len, q_len, dtype, before=1, after=2, max_q_len=25)
+    check(c, cfg, Q, pages, kv_len, q_len, dtype, before=1, after=2, window=600)
+    check(c, cfg, Q, pages, kv_len, q_len, dtype, causal=False, before=1, after=2, max_kv_len=2500)
+
+
+@pytest.mark.parametrize("group", [33, 64, 65, 128])
+@pytest.mark.parametrize("page", [16, 1024])
+def test_many_heads_share_one(group, page):
+    rng, c, cfg = make(64, 4, page, heads=1, pages=max(4, 512 // page))
+    kv_len = [137, 1, 300]
+    pages = fill(rng, c, kv_len)
+    Q = rng.normal(size=(3, group, 64))
+    check(c, cfg, Q, pages, kv_len, [1, 1, 1], "bf16")
+    Q = rng.normal(size=(9, group, 64))
+    check(c, cfg, Q, pages, kv_len, [3, 2, 4], "f16")
+
+
 @pytest.mark.parametrize("rows_", [1, 40])
 @pytest.mark.parametrize("bits", BITS)
 def test_extremes(bits, rows_):
@@ -400,6 +425,15 @@ def test_captured_and_replayed(q):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
         assert torch.equal(cache, eager_cache)
+
+
+def test_many_sequences_without_hints():
+    """A ragged batch of single tokens whose longest the call is not told: launched as if any sequence had all rows."""
+    rng, c, cfg = make(64, 8, 16, heads=2, pages=400)
+    kv_len = [int(x) for x in rng.integers(0, 60, 90)]
+    pages = fill(rng, c, kv_len)
+    Q = rng.normal(size=(90, 4, 64))
+    check(c, cfg, Q, pages, kv_len, [1] * 90, "f16")
 
 
 def test_equal_calls_give_equal_bits():

@@ -548,7 +548,7 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel
       // Logits in base 2 are t * c, t = sum of fp16 query times code, times the key's scale.
       if (u == 0) lds_c[row] = a.scale * (kLog2e * R::kNorm) / up;
     }
-  __syncthreads();
+    __syncthreads();
   }
   u32x4 q[G::kOps], q2[G::kOps];
 #pragma unroll
