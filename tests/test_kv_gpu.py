@@ -223,6 +223,16 @@ def test_prompts(dim, bits, dtype):
     check(c, cfg, Q, pages, kv_len, q_len, dtype, False, scale=0.3)
 
 
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, 1 << 40])
+@pytest.mark.parametrize("rows", [12, 140])
+def test_windows_wider_than_any_cache(rows, window):
+    """As none at all, also where rows lie before position 0."""
+    kv_len, q_len = [5, 40], [rows, rows - 3]
+    rng, c, cfg = make(64, 4, 16, heads=2, pages=8)
+    pages = fill(rng, c, kv_len)
+    check(c, cfg, rng.normal(size=(sum(q_len), 4, 64)), pages, kv_len, q_len, "bf16", window=window)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("dim,bits", [(64, 8), (128, 4), (256, 4)])
 def test_long_caches_are_split(dim, bits, dtype):

@@ -213,3 +213,13 @@ def test_wrappers_check_their_tensors():
             rq.kv_attention(*args, cfg, **kw)
     with pytest.raises(rq.ConvRotError):
         rq.kv_cache_alloc(3, rq.make_kv_cfg(2, 96), device="cpu")
+
+
+def test_windows_of_any_width():
+    cfg = rq.make_kv_cfg(8, 128)
+    whole = rq.kv_attention_workspace_size(3, 32, 3, 2048, cfg)
+    assert whole > 0
+    for window in (1 << 30, (1 << 31) - 1, 1 << 31, (1 << 32) + 1, 1 << 40):
+        assert rq.kv_attention_workspace_size(3, 32, 3, 2048, cfg, window=window) == whole
+    for window in (-1, -(1 << 32) + 1):
+        assert rq.kv_attention_workspace_size(3, 32, 3, 2048, cfg, window=window) == 0

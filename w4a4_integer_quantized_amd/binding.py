@@ -480,6 +480,11 @@ def _kv_table(t, name, dtype, shape):
                                                                                      tuple(t.shape)))
 
 
+def _kv_window(window):
+    """A window as the int32 of the call: any beyond the longest cache is all of it."""
+    return max(-1, min(window, (1 << 31) - 1))
+
+
 def _kv_device(*ts):
     """The index of the one device that all tensors are on."""
     index = ts[0].get_device()
@@ -600,7 +605,7 @@ def kv_attention(Q, cache, pages, kv_len, cfg: rq_kv_config, q_start=None, causa
     p = rq_kv_attention_params(
         Q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), total, qt, qh, ot, oh,
-        max_q_len, max_kv_len, kv.halves[dtype], q_heads, seqs, max_pages, bool(causal), window,
+        max_q_len, max_kv_len, kv.halves[dtype], q_heads, seqs, max_pages, bool(causal), _kv_window(window),
         dim ** -0.5 if softmax_scale is None else softmax_scale)
     at, handle = cache.data_ptr(), kv.raw_stream(index)
     if workspace is None:
@@ -623,5 +628,5 @@ def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages
     """Bytes of workspace a kv_attention call of these sizes needs (0: none). ragged: the call
     passes q_start."""
     p = rq_kv_attention_params(None, None, None, 4 if ragged else None, None, None, total_q, 0, 0, 0, 0, max_q_len,
-                               max_kv_len, RQ_BF16, q_heads, seqs, max_pages, 1, window, 1.0)
+                               max_kv_len, RQ_BF16, q_heads, seqs, max_pages, 1, _kv_window(window), 1.0)
     return rq_kv_attention_workspace_size(p, cfg)

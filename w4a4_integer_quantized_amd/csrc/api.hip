@@ -660,7 +660,8 @@ rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* c
   a.lps = log2_of(cfg->page_size);
   a.dt = p->dtype;
   a.causal = p->causal;
-  a.window = p->window;
+  // Positions are below 2^30: a wider window is no other, and the kernels' differences stay in 32 bits.
+  a.window = p->window < kMaxKvTokens ? p->window : static_cast<int>(kMaxKvTokens);
   a.splits = plan.splits;
   a.row_tiles = plan.row_tiles;
   a.chunk = plan.chunk;
