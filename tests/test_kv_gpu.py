@@ -523,3 +523,23 @@ def test_a_block_with_its_cache(bits):
         assert torch.equal(dev.cpu(), c.flat())
         want, _, _, tol, _ = kv_ref.attention(Q.float().cpu().numpy(), c, pages, [done], [0, step], "bf16")
         assert np.all(np.abs(O.double().cpu().numpy() - want) <= tol)
+
+
+def test_more_tokens_than_one_launch_takes():
+    need_gpu()
+    tokens, cfg = (1 << 27) + 37, rq.make_kv_cfg(1, 64, 16, 4)
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB of device memory")
+    at = torch.tensor([0, 1, (1 << 27) - 1, 1 << 27, tokens - 1])
+    x = torch.randn(5, 1, 64).bfloat16()
+    slots = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    slots[at.cuda()] = torch.arange(5, device="cuda") * 3
+    rows_in = torch.empty((tokens, 1, 64), dtype=torch.bfloat16, device="cuda")
+    rows_in[at.cuda()] = x.cuda()
+    small, cache = (rq.kv_cache_alloc(1, cfg) for _ in range(2))
+    rq.kv_cache_write(x.cuda(), x.cuda(), torch.arange(5, device="cuda") * 3, small, cfg)
+    rq.kv_cache_write(rows_in, rows_in, slots, cache, cfg)
+    want = rq.kv_cache_read(small, torch.arange(5, device="cuda") * 3, cfg)[0]
+    K, V = rq.kv_cache_read(cache, slots, cfg, out=(rows_in, torch.empty_like(rows_in)))
+    assert torch.equal(K[at.cuda()], want) and torch.equal(V[at.cuda()], want)
+    assert not K[5:4096].any() and not K[-30:-1].any() and not V[-30:-1].any()

@@ -223,3 +223,10 @@ def test_windows_of_any_width():
         assert rq.kv_attention_workspace_size(3, 32, 3, 2048, cfg, window=window) == whole
     for window in (-1, -(1 << 32) + 1):
         assert rq.kv_attention_workspace_size(3, 32, 3, 2048, cfg, window=window) == 0
+
+
+def test_attention_grids_beyond_the_hardwares():
+    """2^32 threads: 512 sequences of as many as 2^18 rows each, 8 heads, are 2^25 workgroups."""
+    big = dict(total_q=1 << 18, seqs=512)
+    assert attend(**big)[0] == rq.RQ_EUNSUPPORTED
+    assert attend(**big, max_q=600, O=A)[0] == rq.RQ_EINVAL        # fits; refused later, for O on Q

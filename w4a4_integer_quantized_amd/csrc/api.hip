@@ -430,7 +430,8 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
   *max_q_len = max_q;
   *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
                                      p->window);
-  if (((int64_t)p->seqs * plan->splits + 8) * cfg->kv_heads > kMaxRowsOrCols / plan->row_tiles)
+  // A grid has fewer than 2^32 threads, 256 a workgroup. (Splits come with few rows: the join's fits.)
+  if (((int64_t)p->seqs * plan->splits + 8) * cfg->kv_heads >= ((int64_t)1 << 24) / plan->row_tiles)
     return fail(RQ_EUNSUPPORTED, "%d sequences of up to %lld query rows: too many workgroups (give max_q_len)", p->seqs,
                 (long long)max_q);
   const int64_t need = (int64_t)plan->workspace_bytes;

@@ -208,17 +208,37 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCacheArgs a) {
   }
 }
 
+// A grid has fewer than 2^32 threads along an axis, 16 of them a token at most: one launch takes
+// 2^27 tokens.
+constexpr int64_t kLaunchTokens = int64_t(1) << 27;
+
 template <int D, int BITS>
-hipError_t launch(const KvCacheArgs& a, bool write, hipStream_t stream) {
+hipError_t launch(const KvCacheArgs& call, bool write, hipStream_t stream) {
   constexpr int kRows = kThreads / Row<D, BITS>::kLanes;
-  const dim3 grid(static_cast<unsigned>((a.tokens + kRows - 1) / kRows), static_cast<unsigned>(a.heads));
-  if (write)
-    kv_write_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
-  else if (2 * a.tokens * a.heads * D * (a.dt == kF32 ? 4 : 2) > kStreamBytes)
-    kv_read_kernel<D, BITS, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    kv_read_kernel<D, BITS, false><<<grid, kThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  const int es = call.dt == kF32 ? 4 : 2;
+  const bool past = 2 * call.tokens * call.heads * D * es > kStreamBytes;
+  hipError_t e = hipSuccess;
+  for (int64_t first = 0; e == hipSuccess && first < call.tokens; first += kLaunchTokens) {
+    KvCacheArgs a = call;
+    a.tokens = call.tokens - first < kLaunchTokens ? call.tokens - first : kLaunchTokens;
+    a.slots += first;
+    const int64_t k = first * a.k_token * es, v = first * a.v_token * es;
+    const dim3 grid(static_cast<unsigned>((a.tokens + kRows - 1) / kRows), static_cast<unsigned>(a.heads));
+    if (write) {
+      a.k += k;
+      a.v += v;
+      kv_write_kernel<D, BITS><<<grid, kThreads, 0, stream>>>(a);
+    } else {
+      a.k_out += k;
+      a.v_out += v;
+      if (past)
+        kv_read_kernel<D, BITS, true><<<grid, kThreads, 0, stream>>>(a);
+      else
+        kv_read_kernel<D, BITS, false><<<grid, kThreads, 0, stream>>>(a);
+    }
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
