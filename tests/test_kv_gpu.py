@@ -543,3 +543,21 @@ def test_more_tokens_than_one_launch_takes():
     K, V = rq.kv_cache_read(cache, slots, cfg, out=(rows_in, torch.empty_like(rows_in)))
     assert torch.equal(K[at.cuda()], want) and torch.equal(V[at.cuda()], want)
     assert not K[5:4096].any() and not K[-30:-1].any() and not V[-30:-1].any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q", [1, 5, 150])
+def test_a_query_that_is_no_number_stays_alone(q, bad):
+    """Its own row is no number either; the others', in its tile and elsewhere, keep their bits."""
+    kv_len = [200, 170]
+    rng, c, cfg = make(128, 4, 16, heads=2, pages=32)
+    pages = torch.from_numpy(fill(rng, c, kv_len)).cuda()
+    n, dev = torch.tensor(kv_len, dtype=torch.int32, device="cuda"), c.flat().cuda()
+    for dtype in (torch.float16, torch.bfloat16):
+        Q = torch.from_numpy(rng.normal(size=(2 * q, 4, 128))).to(dtype).cuda()
+        want, want_lse = rq.kv_attention(Q, dev, pages, n, cfg, return_lse=True)
+        Q[q, 1, 7] = bad
+        got, lse = rq.kv_attention(Q, dev, pages, n, cfg, return_lse=True)
+        assert got[q, 1].isnan().all()
+        got[q, 1], lse[q, 1] = want[q, 1], want_lse[q, 1]
+        assert torch.equal(got, want) and torch.equal(lse, want_lse)
