@@ -251,7 +251,8 @@ rq_status rq_check_rotq_linear_args(const void *X, int32_t x_dtype, int64_t M, i
  *   V scales   float [page_size]
  * Pages are independent of each other and can be moved or shared whole. A token's place is its
  * slot, page * page_size + (token within the page); nothing needs to be cleared: bytes of tokens
- * that were never written are not used.
+ * that were never written are not used by rows that do not attend to them (in attention a value's
+ * scale that is no finite number, which no write makes, counts as 0).
  *
  * Limits: bits 8 or 4; head_dim 64, 128 or 256; 1 <= kv_heads <= 65535; page_size a power of two
  * in [16, 1024]; 1 <= num_pages < 2^31, a cache of at most 2^46 bytes. Rows are

@@ -561,3 +561,58 @@ def test_a_query_that_is_no_number_stays_alone(q, bad):
         assert got[q, 1].isnan().all()
         got[q, 1], lse[q, 1] = want[q, 1], want_lse[q, 1]
         assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+def spoil(c, pages, b, tokens, value):
+    """Scales of a sequence's tokens as bytes that nobody wrote may read: `value`. What the reference takes
+    for these tokens is as bad."""
+    for t in tokens:
+        p, i = int(pages[b][t // c.page]), t % c.page
+        for part in range(2):
+            at = 2 * c.page * c.row + (part * c.page + i) * 4
+            c.bytes[p, :, at:at + 4] = np.frombuffer(np.float32(value).tobytes(), np.uint8)
+            c.scale[part, p * c.page + i] = value
+
+
+UNWRITTEN = [float("nan"), float("inf"), float("-inf"), 3.0e38]
+
+
+@pytest.mark.filterwarnings("ignore:invalid value")
+@pytest.mark.parametrize("value", UNWRITTEN)
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("dim,bits", [(128, 4), (64, 8), (256, 4)])
+@pytest.mark.parametrize("q_len,kv_len,window,split", [
+    ([2, 1, 1], [200, 75, 33], 40, False), ([70, 66, 3], [200, 150, 90], 33, False),
+    ([2, 1, 1], [2900, 70, 1], 1500, True), ([40, 33, 1], [2100, 70, 1], 1500, True)])
+def test_tokens_in_front_of_a_window_do_not_matter(q_len, kv_len, window, split, dim, bits, page, value):
+    """Tokens that no row attends to, in a tile with some that rows do: never written, or given back."""
+    rng, c, cfg = make(dim, bits, page, heads=1, pages=4096 // page)
+    pages = fill(rng, c, kv_len)
+    for b, (q, n) in enumerate(zip(q_len, kv_len)):
+        spoil(c, pages, b, range(max(0, n - q + 1 - window)), value)
+    need = rq.kv_attention_workspace_size(sum(q_len), 2, len(q_len), pages.shape[1], cfg, ragged=True, window=window,
+                                          max_q_len=max(q_len))
+    assert (need > 0) == split
+    Q = rng.normal(size=(sum(q_len), 2, dim))
+    for dtype in ("f16", "bf16"):
+        check(c, cfg, Q, pages, kv_len, q_len, dtype, window=window, max_q_len=max(q_len))
+
+
+@pytest.mark.parametrize("value", UNWRITTEN)
+@pytest.mark.parametrize("q,kv,pad", [(5, 100, 3), (3, 64, 1), (20, 2900, 6), (90, 90, 40), (150, 1000, 30)])
+def test_padding_at_a_sequences_end_does_not_matter(q, kv, pad, value):
+    """A batch of equal lengths whose shorter sequences end in padding tokens, skipped by their slots of -1: rows in
+    front of the padding keep their bits. (The padding's own rows attend to what nobody wrote.)"""
+    rng, c, cfg = make(128, 4, 16, heads=2, pages=400)
+    pages = fill(rng, c, [kv, kv])
+    args = [torch.from_numpy(pages).cuda(), torch.tensor([kv, kv], dtype=torch.int32).cuda(), cfg]
+    for dtype in (torch.float16, torch.bfloat16):
+        Q = torch.from_numpy(rng.normal(size=(2 * q, 4, 128))).to(dtype).cuda()
+        want, want_lse = rq.kv_attention(Q, c.flat().cuda(), *args, return_lse=True)
+        kept = c.bytes.copy()
+        spoil(c, pages, 0, range(kv - pad, kv), value)
+        got, lse = rq.kv_attention(Q, c.flat().cuda(), *args, return_lse=True)
+        c.bytes[:] = kept
+        real = torch.arange(2 * q) < q - pad
+        real[q:] = True
+        assert torch.equal(got[real], want[real]) and torch.equal(lse[real], want_lse[real])

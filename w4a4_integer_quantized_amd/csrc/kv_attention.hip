@@ -50,6 +50,11 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
+// A value's scale, 0 where it is no finite number. The writer makes no such scale, but a token that some
+// rows of a tile do not attend to need never have been written, and its scale may read as anything:
+// the weight of 0 that it has there, times infinity or NaN, would be NaN.
+__device__ __forceinline__ float value_scale(float s) { return __builtin_fabsf(s) < __builtin_inff() ? s : 0.0f; }
+
 __device__ __forceinline__ uint32_t add_h2(uint32_t a, float off) {
   const f16x2 d = {static_cast<_Float16>(off), static_cast<_Float16>(off)};
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) + d);
@@ -334,7 +339,10 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS>& t, const u32x4 (&q)[D
 #pragma unroll
     for (int i = 0; i < 4; i++) x[j][i] = acc[i];
   }
+  // No branch between the products and the first use of what they give: where two ways meet, the compiler
+  // (ROCm 7.2) counts the wait states after a matrix instruction along one of them only.
   times_scale(x, x, t.ks);
+  t.vs = value_scale(t.vs);
   if (!full) {   // the same in every lane
     asm volatile("");   // a branch, not selects in every tile
     const int mine = first + 16 * (r >> 2) + (r & 3);   // `first` includes 4 g
@@ -871,7 +879,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       if (lane == 0) lds_ok[half] = ok;
       lds_ks[half][lane] = raw_scale;
     } else if (wave == 1) {
-      lds_vs[half][lane] = raw_ok ? raw_scale : 0.0f;
+      lds_vs[half][lane] = raw_ok ? value_scale(raw_scale) : 0.0f;
     }
   };
   if (begin < end) {
