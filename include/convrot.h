@@ -298,7 +298,8 @@ rq_status rq_kv_cache_read(const void *cache, int64_t num_pages, const int64_t *
  *   causal    a query attends to the positions up to its own; a query before position 0 (more
  *             query rows than cached tokens) attends to nothing
  *   window    with causal: only to the last `window` of those (its own among them); 0: all
- * A row that attends to nothing gets O = 0 and lse = -inf. Rows of Q before q_start[0] or from
+ * A row that attends to nothing gets O = 0 and lse = -inf; one with a query that is not finite gets
+ * NaN in both, and no other row is touched by it. Rows of Q before q_start[0] or from
  * q_start[seqs] on are not read, and their O and lse are left as they were.
  * What the device tables hold is not trusted with memory: query rows outside [0, total_q) do not
  * exist, kv_len is cut to [0, max_pages * page_size], and the tokens of a page index outside

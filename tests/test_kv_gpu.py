@@ -616,3 +616,40 @@ def test_padding_at_a_sequences_end_does_not_matter(q, kv, pad, value):
         real = torch.arange(2 * q) < q - pad
         real[q:] = True
         assert torch.equal(got[real], want[real]) and torch.equal(lse[real], want_lse[real])
+
+
+@pytest.mark.parametrize("kv,split", [(200, False), (3000, True)])
+@pytest.mark.parametrize("q", [1, 5, 80])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_that_is_no_number_is_not_one_that_attends_to_nothing(bad, q, kv, split):
+    """O and lse of its row are NaN however the keys are split; all others keep their bits."""
+    rng, c, cfg = make(128, 4, 16, heads=1, pages=400)
+    pages = torch.from_numpy(fill(rng, c, [kv, kv - 30])).cuda()
+    n, dev = torch.tensor([kv, kv - 30], dtype=torch.int32, device="cuda"), c.flat().cuda()
+    assert (rq.kv_attention_workspace_size(2 * q, 2, 2, pages.shape[1], cfg) > 0) == split
+    for dtype in (torch.float16, torch.bfloat16):
+        Q = torch.from_numpy(rng.normal(size=(2 * q, 2, 128))).to(dtype).cuda()
+        want, want_lse = rq.kv_attention(Q, dev, pages, n, cfg, return_lse=True)
+        Q[q, 1, 7] = bad
+        got, lse = rq.kv_attention(Q, dev, pages, n, cfg, return_lse=True)
+        assert got[q, 1].isnan().all() and lse[q, 1].isnan()
+        got[q, 1], lse[q, 1] = want[q, 1], want_lse[q, 1]
+        assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("at", [3, 150])
+@pytest.mark.parametrize("kv,split", [(200, False), (3000, True)])
+@pytest.mark.parametrize("q", [1, 5, 80])
+def test_a_logit_beyond_binary32_is_not_dropped(q, kv, split, at):
+    """One key whose logits are infinite: no finite result of the other keys takes its place."""
+    rng, c, cfg = make(128, 4, 16, heads=1, pages=400)
+    pages = fill(rng, c, [kv])
+    k = np.zeros((1, 1, 128), np.float32)
+    k[0, 0, 0] = 3e38
+    c.write(k, np.ones((1, 1, 128), np.float32), pages[0][[at // 16]].astype(np.int64) * 16 + at % 16)
+    dev, n = c.flat().cuda(), torch.tensor([kv], dtype=torch.int32, device="cuda")
+    assert (rq.kv_attention_workspace_size(q, 2, 1, pages.shape[1], cfg) > 0) == split
+    for dtype in (torch.float16, torch.bfloat16):
+        Q = torch.from_numpy(np.abs(rng.normal(size=(q, 2, 128))) + 100.0).to(dtype).cuda()
+        out, lse = rq.kv_attention(Q, dev, torch.from_numpy(pages).cuda(), n, cfg, return_lse=True, causal=False)
+        assert out.isnan().all() and (lse.isnan() | lse.isposinf()).all()

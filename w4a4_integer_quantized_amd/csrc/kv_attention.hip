@@ -301,7 +301,8 @@ struct State {
   using G = Geometry<D, BITS>;
   f32x4 o[G::kTilesD];
   float b;   // the row's reference
-  float l;   // this lane's part of the row's sum of p'
+  float l;   // this lane's part of the row's sum of p': 0 if it has met no key, and only then (a sum that
+             // is no number is a result like any other, for the waves' and the splits' joins too)
 };
 
 template <int D, int BITS>
@@ -597,7 +598,7 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel
   // Join the waves.
   st.l = quad_sum(st.l);
   if (g == 0) {
-    lds_m[wave][r] = st.l > 0.0f ? st.b : neg_inf();
+    lds_m[wave][r] = st.l == 0.0f ? neg_inf() : st.b;
     lds_l[wave][r] = st.l;
   }
   __syncthreads();
@@ -649,13 +650,13 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel
         }
       }
     } else {
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int k = 0; k < R::kChunks; k++) {
 #pragma unroll
         for (int i = 0; i < 8; i++) v[k][i] *= inv;
       }
-      if (ok && a.lse && u == 0) a.lse[out_row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+      if (ok && a.lse && u == 0) a.lse[out_row] = sum == 0.0f ? neg_inf() : (best + __log2f(sum)) * kLn2;
       store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, chunk, ok);
     }
   }
@@ -1104,23 +1105,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       const int64_t out_row = (int64_t)(s.q0 + token) * a.q_heads + qh;
       if (a.splits > 1) {
         if (!ok) continue;
-        if (l > 0.0f) {
+        if (l != 0.0f) {
           float* to = a.part_out + (out_row * a.splits + split) * D;
 #pragma unroll
           for (int k = 0; k < R::kChunks; k++) store8(reinterpret_cast<uint8_t*>(to + k * 128 + cc * 8), kF32, v[k]);
         }
         if (u == 0) {
-          a.part_stat[(out_row * a.splits + split) * 2] = l > 0.0f ? rb : neg_inf();
+          a.part_stat[(out_row * a.splits + split) * 2] = l == 0.0f ? neg_inf() : rb;
           a.part_stat[(out_row * a.splits + split) * 2 + 1] = l;
         }
       } else {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int k = 0; k < R::kChunks; k++) {
 #pragma unroll
           for (int i = 0; i < 8; i++) v[k][i] *= inv;
         }
-        if (ok && a.lse && u == 0) a.lse[out_row] = l > 0.0f ? (rb + __log2f(l)) * kLn2 : neg_inf();
+        if (ok && a.lse && u == 0) a.lse[out_row] = l == 0.0f ? neg_inf() : (rb + __log2f(l)) * kLn2;
         store_row<D, BITS>(a.out + ((s.q0 + token) * a.out_token + qh * a.out_head) * 2, a.dt, v, cc, ok);
       }
     }
@@ -1190,14 +1191,14 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a) {
       for (int e = 0; e < 8; e++) v[k][e] = __builtin_fmaf(lds_o[i][k * 128 + chunk * 8 + e], f, v[k][e]);
     }
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int k = 0; k < R::kChunks; k++) {
 #pragma unroll
     for (int i = 0; i < 8; i++) v[k][i] *= inv;
   }
   const bool ok = group == 0;
-  if (ok && a.lse && u == 0) a.lse[row] = sum > 0.0f ? (best + __log2f(sum)) * kLn2 : neg_inf();
+  if (ok && a.lse && u == 0) a.lse[row] = sum == 0.0f ? neg_inf() : (best + __log2f(sum)) * kLn2;
   store_row<D, BITS>(a.out + (token * a.out_token + head * a.out_head) * 2, a.dt, v, chunk, ok);
 }
 
