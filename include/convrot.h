@@ -283,7 +283,9 @@ rq_status rq_kv_cache_write(const void *K, const void *V, int32_t dtype, int64_t
 /* Read `tokens` keys and values back, rotated back and rounded once to `dtype` (RQ_F32, RQ_F16 or
  * RQ_BF16).
  *   slots    [tokens] device; a slot outside the cache gives a row of zeros; slots may repeat
- *   K, V     out: [tokens, kv_heads, head_dim], strides in elements; no two rows may overlap */
+ *   K, V     out: [tokens, kv_heads, head_dim], strides in elements; no two rows may overlap. They may
+ *            be slices of one buffer; where they lie in each other the larger of their strides has to
+ *            be the same, and beyond 65536 rows the smaller too (else RQ_EUNSUPPORTED) */
 rq_status rq_kv_cache_read(const void *cache, int64_t num_pages, const int64_t *slots,
                            int64_t tokens, const rq_kv_config *cfg, void *K, void *V,
                            int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,

@@ -230,3 +230,78 @@ def test_attention_grids_beyond_the_hardwares():
     big = dict(total_q=1 << 18, seqs=512)
     assert attend(**big)[0] == rq.RQ_EUNSUPPORTED
     assert attend(**big, max_q=600, O=A)[0] == rq.RQ_EINVAL        # fits; refused later, for O on Q
+
+
+# K and V read back into one buffer: accepted where no row of one meets a row of the other. Such calls are
+# then refused for their missing slots.
+def apart(**kw):
+    st = read(**{**dict(tokens=5, slots=None), **kw})
+    detail = rq.load().rq_last_error_detail().decode()
+    assert st != rq.RQ_OK
+    return detail == "slots is NULL", st
+
+
+H, D, T, E = 8, 128, 5, 2      # heads, dim, tokens of the calls below, bytes an element
+
+
+@pytest.mark.parametrize("kw", [
+    dict(V=A + H * D * E, kt=2 * H * D, vt=2 * H * D),                                   # [T, 2, H, D]
+    dict(K=A + H * D * E, V=A, kt=2 * H * D, vt=2 * H * D),                              # V first
+    dict(V=A + D * E, kt=2 * H * D, vt=2 * H * D, kh=2 * D, vh=2 * D),                   # [T, H, 2, D]
+    dict(V=A + T * D * E, kt=D, vt=D, kh=2 * T * D, vh=2 * T * D),                       # [H, 2, T, D]
+    dict(V=A + H * 192 * E, kt=H * 320, vt=H * 320, kh=192, vh=128),                     # wider keys, a row of both a token
+    dict(V=A + 3 * D * E, kt=H * D * 4, vt=H * D * 4, kh=4 * D, vh=4 * D),               # the last of four parts
+    dict(V=A + T * H * D * E), dict(K=A + T * H * D * E, V=A),                           # one behind the other
+    dict(tokens=1, V=A + D * E, kh=2 * D, vh=2 * D, kt=0, vt=7),
+    dict(tokens=1 << 20, V=A + (D << 20) * E, kt=D, vt=D, kh=2 * D << 20, vh=2 * D << 20, cache=A + (1 << 43))])
+def test_outputs_beside_each_other(kw):
+    assert apart(**kw)[0]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(V=A + 4 * D * E, kt=12 * D, vt=12 * D), dict(K=A + 4 * D * E, V=A, kt=12 * D, vt=12 * D),   # heads 0 .. 7, 4 .. 11
+    dict(V=A + H * D * E), dict(V=A + 4 * H * D * E), dict(K=A + 4 * H * D * E, V=A),                # by whole tokens
+    dict(V=A + 16), dict(V=A + D * E - 16, kt=2 * H * D, vt=2 * H * D, kh=2 * D, vh=2 * D),          # by parts of a row
+    dict(tokens=1, V=A + 64 * E), dict(V=A + (7 * 192 + 120) * E, kt=H * 320, vt=H * 320, kh=192, vh=128),
+    dict(V=A + T * D * E - 16, kt=D, vt=D, kh=2 * T * D, vh=2 * T * D),
+    dict(tokens=1 << 20, V=A + (D << 20) * E - 16, kt=D, vt=D, kh=2 * D << 20, vh=2 * D << 20, cache=A + (1 << 43))])
+def test_outputs_that_meet_are_refused(kw):
+    assert apart(**kw) == (False, rq.RQ_EINVAL)
+
+
+def test_outputs_in_each_other_in_unlike_orders_are_refused():
+    assert apart(V=A + H * D * E, kt=4 * H * D, vt=D, vh=4 * T * D) == (False, rq.RQ_EUNSUPPORTED)
+
+
+def test_outputs_of_any_strides_against_their_elements():
+    """Every call that is let through has no element twice; every one refused as overlapping has one."""
+    rng = np.random.default_rng(0)
+    met = free = 0
+    for _ in range(4000):
+        tokens, heads, dim = int(rng.integers(1, 5)), int(rng.integers(1, 4)), 64
+        def strides():
+            a = dim + 16 * int(rng.integers(0, 6))
+            n = heads if rng.random() < 0.7 else tokens
+            b = a * n + 64 * int(rng.integers(0, 8))
+            return (b, a) if n == heads else (a, b)
+        k = strides()
+        v = k if rng.random() < 0.5 else ((k[0], k[1] + 16 * int(rng.integers(-3, 4))) if rng.random() < 0.5 else strides())
+        shift = 16 * int(rng.integers(-60, 60))
+        def elements(s):
+            return (np.arange(tokens)[:, None, None] * s[0] + np.arange(heads)[None, :, None] * s[1] + np.arange(dim)).ravel()
+        ke, ve = elements(k), elements(v) + shift
+        if len(np.unique(ke)) < ke.size or len(np.unique(ve)) < ve.size:
+            continue
+        got, st = apart(tokens=tokens, K=A + 65536, V=A + 65536 + shift * E, kt=k[0], kh=k[1], vt=v[0], vh=v[1],
+                        cfg=rq.make_kv_cfg(heads, dim))
+        if "rows overlap" in rq.load().rq_last_error_detail().decode():
+            continue        # neither axis lies inside the other: refused before
+        meet = np.intersect1d(ke, ve).size > 0
+        if got:
+            assert not meet
+        elif st == rq.RQ_EINVAL:
+            assert meet
+        else:
+            assert st == rq.RQ_EUNSUPPORTED and k != v
+        met, free = met + meet, free + (got and not meet)
+    assert met > 300 and free > 300

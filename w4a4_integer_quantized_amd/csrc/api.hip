@@ -334,6 +334,61 @@ rq_status check_kv_rows(const void* p, const char* name, int64_t tokens, int64_t
   return ok();
 }
 
+// Two sets of rows of `dim` elements in one buffer, each set's rows apart from one another: 1 if a row of one
+// meets a row of the other, 0 if none does, -1 if that is not worked out.
+// `n` rows at 0, ks, 2 ks, .. and at r, r + vs, ...
+int rows_meet(int64_t n, int64_t dim, int64_t ks, int64_t vs, int64_t r) {
+  if (n == 1) return r > -dim && r < dim;
+  if (ks == vs) {   // r plus a multiple of the stride, next to 0 on either side
+    int64_t j = r >= 0 ? -(r / ks) - 1 : -r / ks;
+    for (const int64_t last = j + 1; j <= last; j++)
+      if (j > -n && j < n && r + j * ks > -dim && r + j * ks < dim) return 1;
+    return 0;
+  }
+  if (n > 65536) return -1;
+  for (int64_t i = 0, j = 0; i < n && j < n;) {
+    const int64_t d = r + j * vs - i * ks;
+    if (d > -dim && d < dim) return 1;
+    if (d < 0)
+      j++;
+    else
+      i++;
+  }
+  return 0;
+}
+// `outer` groups of `inner` rows, the groups `stride` apart in both sets and each as long as that at most.
+int groups_meet(int64_t outer, int64_t stride, int64_t inner, int64_t dim, int64_t ks, int64_t vs, int64_t r) {
+  if (outer == 1) return rows_meet(inner, dim, ks, vs, r);
+  const int64_t k_len = (inner - 1) * ks + dim, v_len = (inner - 1) * vs + dim;
+  int64_t i = (-v_len - r) / stride - 1;   // the groups that may meet begin between -v_len and k_len
+  for (; r + i * stride < k_len; i++) {
+    if (i <= -outer || i >= outer) continue;
+    const int m = rows_meet(inner, dim, ks, vs, r + i * stride);
+    if (m) return m;
+  }
+  return 0;
+}
+
+// K and V as outputs: no row of one on a row of the other. (K's rows are apart already, V's too.)
+rq_status check_kv_apart(const void* K, int64_t kb, const void* V, int64_t vb, int64_t es, int64_t tokens, int64_t heads,
+                         int64_t dim, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head) {
+  if (!overlap(K, kb, V, vb)) return ok();
+  const int64_t r = (int64_t)(reinterpret_cast<intptr_t>(V) - reinterpret_cast<intptr_t>(K)) / es;   // both 16-byte aligned
+  // Groups of one axis inside the other's stride, in both sets.
+  auto inside = [&](int64_t inner, int64_t s, int64_t outer, int64_t stride) {
+    return outer == 1 || (inner == 1 ? stride >= dim : stride >= (inner - 1) * s + dim);
+  };
+  int m = -1;
+  if ((tokens == 1 || k_token == v_token) && inside(heads, k_head, tokens, k_token) && inside(heads, v_head, tokens, v_token))
+    m = groups_meet(tokens, k_token, heads, dim, heads == 1 ? 0 : k_head, heads == 1 ? 0 : v_head, r);
+  else if ((heads == 1 || k_head == v_head) && inside(tokens, k_token, heads, k_head) && inside(tokens, v_token, heads, v_head))
+    m = groups_meet(heads, k_head, tokens, dim, tokens == 1 ? 0 : k_token, tokens == 1 ? 0 : v_token, r);
+  if (m == 1) return fail(RQ_EINVAL, "K and V overlap");
+  if (m < 0) return fail(RQ_EUNSUPPORTED, "K and V lie in each other with strides (%lld, %lld) and (%lld, %lld)",
+                         (long long)k_token, (long long)k_head, (long long)v_token, (long long)v_head);
+  return ok();
+}
+
 rq_status check_kv_rw(const void* K, const void* V, int32_t dtype, int64_t tokens, int64_t k_token, int64_t k_head,
                       int64_t v_token, int64_t v_head, const int64_t* slots, const rq_kv_config* cfg, const void* cache,
                       int64_t num_pages, bool out) {
@@ -348,6 +403,8 @@ rq_status check_kv_rw(const void* K, const void* V, int32_t dtype, int64_t token
   int64_t kb = 0, vb = 0;
   if ((s = check_kv_rows(K, "K", tokens, cfg->kv_heads, cfg->head_dim, es, k_token, k_head, out, &kb))) return s;
   if ((s = check_kv_rows(V, "V", tokens, cfg->kv_heads, cfg->head_dim, es, v_token, v_head, out, &vb))) return s;
+  if (out && (s = check_kv_apart(K, kb, V, vb, es, tokens, cfg->kv_heads, cfg->head_dim, k_token, k_head, v_token, v_head)))
+    return s;
   if (!slots) return fail(RQ_EINVAL, "slots is NULL");
   if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return fail(RQ_EINVAL, "slots is not 8-byte aligned");
   const int64_t cb = num_pages * kv_head_bytes(cfg) * cfg->kv_heads;
@@ -355,8 +412,6 @@ rq_status check_kv_rw(const void* K, const void* V, int32_t dtype, int64_t token
     return fail(RQ_EINVAL, "the cache overlaps K, V or slots");
   if (out && (overlap(K, kb, slots, tokens * 8) || overlap(V, vb, slots, tokens * 8)))
     return fail(RQ_EINVAL, "K or V overlaps slots");
-  // Interleaved K and V (slices of one buffer) share an extent: only the same start is refused.
-  if (out && K == V) return fail(RQ_EINVAL, "K and V are the same buffer");
   return ok();
 }
 
