@@ -653,3 +653,95 @@ def test_a_logit_beyond_binary32_is_not_dropped(q, kv, split, at):
         Q = torch.from_numpy(np.abs(rng.normal(size=(q, 2, 128))) + 100.0).to(dtype).cuda()
         out, lse = rq.kv_attention(Q, dev, torch.from_numpy(pages).cuda(), n, cfg, return_lse=True, causal=False)
         assert out.isnan().all() and (lse.isnan() | lse.isposinf()).all()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 20, 2.0 ** 25, 2.0 ** 29, 2.0 ** 36, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("q,kv", [(1, 1), (1, 200), (5, 3000), (80, 150), (80, 3000)])
+@pytest.mark.parametrize("dim,bits", [(128, 4), (64, 8)])
+def test_logits_of_any_size(dim, bits, q, kv, size, sign):
+    """Logits so far apart that a row's result is one key's value (or the mean of two equal keys' values), whatever
+    the size of the logits and of the values. With a single weight (two equal ones) in the rotated domain: its
+    rounding u of each |value|, spread over the block by the way back, 16 roundings of binary32, the output's."""
+    rng, c, cfg = make(dim, bits, 16, heads=1, pages=400)
+    pages = fill(rng, c, [kv])
+    a = rng.normal(size=dim)
+    slots = pages[0][np.arange(kv) // 16].astype(np.int64) * 16 + np.arange(kv) % 16
+    m = sign * (1.0 + rng.permutation(kv) / max(kv, 2))
+    if kv > 1:
+        top2 = np.sort(m)[-2:]
+        m[m == top2[0]] = top2[1]                  # the two largest are equal: the same codes and scale
+    # |a|^2 dim^-1/2 m size, base 2: about `size`
+    k = (a[None] * (m * size / (np.dot(a, a) * dim ** -0.5 * np.log2(np.e)))[:, None])[:, None].astype(np.float32)
+    v = (rng.normal(size=(kv, 1, dim)) * 10.0 ** rng.uniform(-3, 3, size=(kv, 1, 1))).astype(np.float32)
+    c.write(k, v, slots)
+    assert (rq.kv_attention_workspace_size(q, 2, 1, pages.shape[1], cfg) > 0) == (kv > 1000)
+    R, B = kv_ref.matrix(dim), min(128, dim)
+    held = [(c.codes[p][slots, 0].astype(np.float64) * c.scale[p][slots, 0][:, None].astype(np.float64)) for p in range(2)]
+    for dtype in ("f16", "bf16"):
+        Q = torch.from_numpy(a[None, None] * (1.0 + rng.random((q, 2, 1)))).to(kv_ref.TORCH[dtype])
+        L = (Q.double().numpy() @ R) @ held[0].T * dim ** -0.5                      # q, 2, kv
+        order = np.sort(L, axis=-1)
+        best = order[..., -1:]
+        two = L == best
+        assert (two.sum(-1) == min(kv, 2)).all()
+        if kv > 2:
+            assert ((best - order[..., -3:-2]) >= 2.0 ** -13 * np.abs(best)).all() and ((best - order[..., -3:-2]) * size >= 0).all()
+        if kv > 2 and size < 2.0 ** 20:      # the others count for something: only the large ones are this test's
+            continue
+        P = two / two.sum(-1, keepdims=True)
+        want = P @ (held[1] @ R)
+        u = 2.0 ** -22 if dtype == "f16" else 2.0 ** -11
+        rot = (P @ np.abs(held[1])) * (u + 16 * kv_ref.U32)
+        e = np.repeat(rot.reshape(q, 2, -1, B).sum(-1) / np.sqrt(B), B, axis=-1)
+        tol = e + kv_ref.EPS[dtype] * (np.abs(want) + e) + (2.0 ** -25 if dtype == "f16" else 0.0)
+        out, lse = rq.kv_attention(Q.cuda(), c.flat().cuda(), torch.from_numpy(pages).cuda(),
+                                   torch.tensor([kv], dtype=torch.int32).cuda(), cfg, causal=False, return_lse=True)
+        assert np.all(np.abs(out.cpu().double().numpy() - want) <= tol)
+        # lse: the logit's own error, R q in fp16 and dim sums, and that of its logarithm to base 2
+        want_lse = best[..., 0] + np.log(two.sum(-1))
+        A = np.abs(Q.double().numpy() @ R) @ np.abs(held[0]).T * dim ** -0.5
+        assert np.all(np.abs(lse.cpu().double().numpy() - want_lse) <= (u + 2 * (dim + 32) * kv_ref.U32) * A.max(-1) + 2.0 ** -16)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 23, 2.0 ** 31, 2.0 ** 50])
+@pytest.mark.parametrize("behind", [False, True])
+@pytest.mark.parametrize("q,kv", [(1, 200), (5, 3200), (80, 160), (80, 3200)])
+def test_large_and_ordinary_logits_in_one_row(q, kv, behind, size):
+    """Keys with very negative logits, in front of or behind ordinary ones: as if they were not there. One with a very
+    large logit: as if the others were not there. And the same rows beside rows that are not touched by them."""
+    rng, c, cfg = make(128, 4, 16, heads=1, pages=400)
+    pages = fill(rng, c, [kv])
+    a = rng.normal(size=128)
+    a *= np.sqrt(128) / np.linalg.norm(a)                               # |a|^2 / sqrt(128) = 11.3
+    far = np.arange(kv - 64, kv) if behind else np.arange(64)           # whole pages
+    slots = lambda j: pages[0][j // 16].astype(np.int64) * 16 + j % 16
+    low = (a[None, None] * -size * (1.0 + rng.random((64, 1, 1)))).astype(np.float32)
+    c.write(low, rng.normal(size=(64, 1, 128)).astype(np.float32) * 100, slots(far))
+    near_pages = pages[:, :-4] if behind else pages[:, 4:]
+    n = torch.tensor([kv], dtype=torch.int32).cuda()
+    for dtype in ("f16", "bf16"):
+        Q = rng.normal(size=(q, 2, 128))
+        Q = Q - (Q @ a)[..., None] * a / 128 + a                         # each q . a = 128
+        Q = torch.from_numpy(Q).to(kv_ref.TORCH[dtype])
+        Qf = Q.float().numpy()
+        want, lse, _, tol, lse_tol = kv_ref.attention(Qf, c, near_pages, [kv - 64], [0, q], dtype, causal=False)
+        got, got_lse = rq.kv_attention(Q.cuda(), c.flat().cuda(), torch.from_numpy(pages).cuda(), n, cfg, causal=False, return_lse=True)
+        assert np.all(np.abs(got.cpu().double().numpy() - want) <= tol)
+        assert np.all(np.abs(got_lse.cpu().double().numpy() - lse) <= lse_tol)
+        # One row's queries turned to the other side: its logits are large, the other rows keep their bits.
+        Q2 = Q.clone()
+        Q2[q // 2, 1] = -Q2[q // 2, 1]
+        got2, lse2 = rq.kv_attention(Q2.cuda(), c.flat().cuda(), torch.from_numpy(pages).cuda(), n, cfg, causal=False, return_lse=True)
+        R = kv_ref.matrix(128)
+        L = Q2[q // 2, 1].double().numpy() @ (c.codes[0][slots(far), 0].astype(np.float64) * c.scale[0][slots(far), 0][:, None] @ R).T
+        best = np.argsort(L)
+        assert L[best[-1]] - L[best[-2]] > 1e-5 * L[best[-1]]
+        v = c.codes[1][slots(far[best[-1:]]), 0][0].astype(np.float64) * c.scale[1][slots(far[best[-1:]]), 0]
+        u = 2.0 ** -22 if dtype == "f16" else 2.0 ** -11
+        e = np.abs(v).sum() / np.sqrt(128) * (u + 16 * kv_ref.U32)
+        err = np.abs(got2[q // 2, 1].cpu().double().numpy() - v @ R)
+        if (L[best[-1]] - L[best[-2]]) * 128 ** -0.5 > 60:
+            assert np.all(err <= e + kv_ref.EPS[dtype] * (np.abs(v @ R) + e) + 2.0 ** -25)
+        got2[q // 2, 1], lse2[q // 2, 1] = got[q // 2, 1], got_lse[q // 2, 1]
+        assert torch.equal(got2, got) and torch.equal(lse2, got_lse)

@@ -15,7 +15,10 @@
 // weight met is 2^7, whatever share of that is the value's size (a key that takes nearly all of l
 // may have a value of next to nothing), and stays until a weight passes 2^15; then b moves and
 // what was summed is scaled. So weights down to 2^-21 of the largest are normal fp16 numbers, and
-// most tiles only compare. l may be far above 1.
+// most tiles only compare. l may be far above 1. Between logits beyond 2^22 binary32 has no such b
+// (and a b half a step off at 2^30 would have p' off by 2^32): there b is the largest logit rounded to
+// binary32, the others are rounded so too before b is taken off, and e, taken off after that, stands
+// for the value's size. Tiles of rows with an e always go the longer way.
 #include "kv_common.h"
 
 namespace convrot {
@@ -54,6 +57,29 @@ __device__ __forceinline__ float quad_sum(float x) {
 // rows of a tile do not attend to need never have been written, and its scale may read as anything:
 // the weight of 0 that it has there, times infinity or NaN, would be NaN.
 __device__ __forceinline__ float value_scale(float s) { return __builtin_fabsf(s) < __builtin_inff() ? s : 0.0f; }
+
+// The reference of a row: p' = 2^(t - b), or, for large logits, 2^((t - b) - e) (e not 0).
+struct Ref {
+  float b, e;
+};
+constexpr float kLarge = 0x1p22f;   // logits: their steps are 1/4 here
+__device__ __forceinline__ bool is_large(float logit) { return __builtin_fabsf(logit) >= kLarge && logit != kNoRef; }
+// x c - b: one rounding, or for large logits two, x c first.
+__device__ __forceinline__ float from_logit(float x, float c, float b, bool large) {
+  return __builtin_fmaf(x, c, large ? 0.0f : -b) - (large ? b : 0.0f);
+}
+// The reference after a tile. `top`, `wl`: the largest logit (x c, rounded) and, counted from `near`,
+// the largest logarithm of a weight; near: the larger of top and the reference there was.
+__device__ __forceinline__ Ref moved(const Ref& r, float near, float top, float wl) {
+  const float from = (near - r.b) - r.e;
+  const bool moves = wl + from > 15.0f || (top - near) + from > kMostExp;
+  const float off = fmaxf(wl - kTop, (top - near) - kMostExp);
+  const bool large = is_large(near);
+  const float e = off == 0.0f ? 0x1p-20f : off;
+  Ref n = {moves ? large ? near : near + off : r.b, moves ? large ? e : 0.0f : r.e};
+  asm volatile("" : "+v"(n.b));   // or the differences from r.b are kept for the case that it has not moved
+  return n;
+}
 
 __device__ __forceinline__ uint32_t add_h2(uint32_t a, float off) {
   const f16x2 d = {static_cast<_Float16>(off), static_cast<_Float16>(off)};
@@ -209,6 +235,18 @@ __device__ __forceinline__ void times_scale(float (&a)[kSteps][4], const float (
   }
 }
 
+// The largest of x[n] c - near plus the value that lane FIRST + n of the row holds. LARGE: some row's
+// logits are.
+template <bool LARGE, int FIRST, int COUNT, int N = 0>
+__device__ __forceinline__ float largest(const float (&x)[COUNT], float c, float near, float per_key, float so_far) {
+  if constexpr (N < COUNT) {
+    const float t = from_logit(x[N], c, near, LARGE && is_large(near));
+    return largest<LARGE, FIRST, COUNT, N + 1>(x, c, near, per_key, fmaxf(so_far, row_lane<FIRST + N>(per_key) + t));
+  } else {
+    return so_far;
+  }
+}
+
 // Page table entries of a tile's steps, read through the scalar cache. Steps past the table's end
 // take its last entry (their tokens are masked: they lie behind kv_len).
 struct Pages {
@@ -300,7 +338,7 @@ template <int D, int BITS>
 struct State {
   using G = Geometry<D, BITS>;
   f32x4 o[G::kTilesD];
-  float b;   // the row's reference
+  Ref ref;   // the row's reference
   float l;   // this lane's part of the row's sum of p': 0 if it has met no key, and only then (a sum that
              // is no number is a result like any other, for the waves' and the splits' joins too)
 };
@@ -309,7 +347,7 @@ template <int D, int BITS>
 __device__ __forceinline__ void start(State<D, BITS>& s) {
 #pragma unroll
   for (int m = 0; m < D / 16; m++) s.o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  s.b = kNoRef;
+  s.ref = {kNoRef, 0.0f};
   s.l = 0.0f;
 }
 
@@ -359,17 +397,17 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS>& t, const u32x4 (&q)[D
       }
     }
   }
-  // Weights for the present b; true if they fit: none above kMost, and no p' so large that l might
-  // come near its range's end (a first key's is infinite: b is kNoRef).
+  // Weights for the present reference; true if they fit: none above kMost, and no p' so large that l
+  // might come near its range's end (a first key's is infinite: b is kNoRef).
   float l;
-  auto weigh = [&]() {
+  auto weigh = [&](auto exponent_of) {
     float wtop = 0.0f;
     l = s.l;
 #pragma unroll
     for (int j = 0; j < kSteps; j++) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        p[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], c, -s.b));
+        p[j][i] = __builtin_amdgcn_exp2f(exponent_of(x[j][i]));
         l += p[j][i];
       }
     }
@@ -381,34 +419,35 @@ __device__ __forceinline__ void attend_tile(Tile<D, BITS>& t, const u32x4 (&q)[D
     }
     return wtop <= kMost && l < kMostSum;
   };
-  if (!__all(weigh())) {
+  const bool fits = weigh([&](float y) { return __builtin_fmaf(y, c, -s.ref.b); });
+  if (!__all(fits && s.ref.e == 0.0f)) {
     // The logarithm of the tile's largest weight, and its largest logit, over the row's four lanes.
     const float lv = t.vs > 0.0f ? __builtin_amdgcn_logf(t.vs) : neg_inf();
-    float one[kSteps][4], wl = neg_inf(), top = neg_inf();
+    float top = neg_inf();
 #pragma unroll
     for (int j = 0; j < kSteps; j++) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) one[j][i] = 1.0f;
+      for (int i = 0; i < 4; i++) top = fmaxf(top, x[j][i]);
     }
-    times_scale(p, one, lv);
-#pragma unroll
-    for (int j = 0; j < kSteps; j++) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        top = fmaxf(top, x[j][i]);
-        wl = fmaxf(wl, __builtin_fmaf(x[j][i], c, p[j][i]));
-      }
-    }
-    wl = quad_max(wl);
     top = quad_max(top) * c;
-    const bool moves = wl - s.b > 15.0f || top - s.b > kMostExp;
-    const float b = moves ? fmaxf(wl - kTop, top - kMostExp) : s.b;
-    const float alpha = __builtin_amdgcn_exp2f(s.b - b);   // 0 for a row that had no reference
-    s.b = b;
+    const float near = fmaxf(top, s.ref.b);
+    const bool large = __any(is_large(near));
+    static_assert(kSteps == 2, "");
+    float wl;
+    if (large)
+      wl = largest<true, 4>(x[1], c, near, lv, largest<true, 0>(x[0], c, near, lv, neg_inf()));
+    else
+      wl = largest<false, 4>(x[1], c, near, lv, largest<false, 0>(x[0], c, near, lv, neg_inf()));
+    const Ref n = moved(s.ref, near, top, quad_max(wl));
+    const float alpha = __builtin_amdgcn_exp2f((s.ref.b - n.b) + (s.ref.e - n.e));   // 0 for a row that had no reference
+    s.ref = n;
     s.l *= alpha;
 #pragma unroll
     for (int m = 0; m < G::kTilesD; m++) s.o[m] *= alpha;
-    weigh();
+    if (large)
+      weigh([&](float y) { return from_logit(y, c, s.ref.b, s.ref.e != 0.0f) - s.ref.e; });
+    else
+      weigh([&](float y) { return __builtin_fmaf(y, c, -s.ref.b); });
   }
   s.l = l;
 #pragma unroll
@@ -596,9 +635,9 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel
   }
 
   // Join the waves.
-  st.l = quad_sum(st.l);
+  st.l = quad_sum(st.l) * __builtin_amdgcn_exp2f(st.ref.e);   // counted from b, as o will be
   if (g == 0) {
-    lds_m[wave][r] = st.l == 0.0f ? neg_inf() : st.b;
+    lds_m[wave][r] = st.l == 0.0f ? neg_inf() : st.ref.b;
     lds_l[wave][r] = st.l;
   }
   __syncthreads();
@@ -607,7 +646,7 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) void kv_attend_kernel
   for (int w = 1; w < WAVES; w++) top = fmaxf(top, lds_m[w][r]);
   {
     const float m = lds_m[wave][r];
-    const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+    const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f((m - top) + st.ref.e);
 #pragma unroll
     for (int m16 = 0; m16 < G::kTilesD; m16++) {
 #pragma unroll
@@ -698,8 +737,10 @@ __device__ __forceinline__ void times_scale16(float (&a)[16], const float (&b)[1
   }
 }
 
+// At head_dim 64 in bf16 three waves a SIMD: 168 registers, two of them spilled with 8-bit codes (2 x 4096 x 4096,
+// 12 heads: 169 us; 188 with 170 registers and two waves).
 template <int D, int BITS, bool SPLIT>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(KvAttentionArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 64 && !SPLIT ? 3 : 2) void kv_attend_block_kernel(KvAttentionArgs a) {
   using R = Row<D, BITS>;
   constexpr int kUnits = R::kBytes / 32;        // 16-byte pieces of a tile's codes a thread loads
   constexpr int kPieces = 4 * R::kBytes;        // of K, and as many of V
@@ -941,7 +982,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
 #pragma unroll
     for (int i = 0; i < 16; i++) o[t][i] = 0.0f;
   }
-  float ref = kNoRef, sum = 0.0f;
+  Ref ref = {kNoRef, 0.0f};
+  float sum = 0.0f;
 
   lds_barrier();   // the queries' region has been read
   if (begin < end) {
@@ -1009,14 +1051,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       }
     }
     float l, w[2][16];
-    auto weigh = [&]() {
+    auto weigh = [&](auto exponent_of) {
       l = sum;
       float wtop = 0.0f;
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-          p[sub][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[sub][i], c, -ref));
+          p[sub][i] = __builtin_amdgcn_exp2f(exponent_of(x[sub][i]));
           l += p[sub][i];
         }
         times_scale16(w[sub], p[sub], vs[sub]);
@@ -1025,30 +1067,35 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       }
       return wtop <= kMost && l < kMostSum;
     };
-    if (!__all(weigh())) {   // as in attend_tile
+    const bool fits = weigh([&](float y) { return __builtin_fmaf(y, c, -ref.b); });
+    if (!__all(fits && ref.e == 0.0f)) {   // as in attend_tile
       float wl = neg_inf(), top = neg_inf();
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
-        const float lv = vs[sub] > 0.0f ? __builtin_amdgcn_logf(vs[sub]) : neg_inf();
 #pragma unroll
-        for (int i = 0; i < 16; i++) p[sub][i] = 1.0f;
-        times_scale16(p[sub], p[sub], lv);
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          top = fmaxf(top, x[sub][i]);
-          wl = fmaxf(wl, __builtin_fmaf(x[sub][i], c, p[sub][i]));
-        }
+        for (int i = 0; i < 16; i++) top = fmaxf(top, x[sub][i]);
       }
-      wl = fmaxf(wl, __shfl_xor(wl, 32, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
-      const bool moves = wl - ref > 15.0f || top - ref > kMostExp;
-      const float next = moves ? fmaxf(wl - kTop, top - kMostExp) : ref;
-      const float alpha = __builtin_amdgcn_exp2f(ref - next);
-      ref = next;
+      const float near = fmaxf(top, ref.b);
+      const bool large = __any(is_large(near));
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const float lv = vs[sub] > 0.0f ? __builtin_amdgcn_logf(vs[sub]) : neg_inf();
+        if (large)
+          wl = largest<true, 0>(x[sub], c, near, lv, wl);
+        else
+          wl = largest<false, 0>(x[sub], c, near, lv, wl);
+      }
+      const Ref n = moved(ref, near, top, fmaxf(wl, __shfl_xor(wl, 32, 64)));
+      const float alpha = __builtin_amdgcn_exp2f((ref.b - n.b) + (ref.e - n.e));
+      ref = n;
       sum *= alpha;
 #pragma unroll
       for (int t = 0; t < kTilesD; t++) o[t] *= alpha;
-      weigh();
+      if (large)
+        weigh([&](float y) { return from_logit(y, c, ref.b, ref.e != 0.0f) - ref.e; });
+      else
+        weigh([&](float y) { return __builtin_fmaf(y, c, -ref.b); });
     }
     sum = l;
 #pragma unroll
@@ -1073,6 +1120,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
 
   // Outputs, a wave its own rows, 16 at a time through its quarter of the LDS.
   sum += __shfl_xor(sum, 32, 64);
+  const float back = __builtin_amdgcn_exp2f(ref.e);   // to what is counted from b
   float* region = reinterpret_cast<float*>(lds) + wave * (16 * D);
   const int u = lane % R::kLanes, cc = chunk_of_lane(u);
   for (int part = 0; part < 2; part++) {
@@ -1091,7 +1139,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
       const int row = k0 + lane / R::kLanes, n = w_first + part * 16 + row;
       const bool ok = n < rows;
       const int token = ok ? token_of(a, n) : 0, qh = head * a.group + (ok ? n - token * a.group : 0);
-      const float l = __shfl(sum, part * 16 + row, 64), rb = __shfl(ref, part * 16 + row, 64);
+      const float g = __shfl(back, part * 16 + row, 64);
+      const float l = __shfl(sum, part * 16 + row, 64) * g, rb = __shfl(ref.b, part * 16 + row, 64);
       float v[R::kChunks][8];
 #pragma unroll
       for (int k = 0; k < R::kChunks; k++) {
@@ -1099,7 +1148,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attend_block_kernel(
         for (int e = 0; e < 2; e++) {
           const f32x4 y = *reinterpret_cast<const f32x4*>(region + row * D + ((k * 32 + cc * 2 + e) ^ row) * 4);
 #pragma unroll
-          for (int i = 0; i < 4; i++) v[k][4 * e + i] = y[i];
+          for (int i = 0; i < 4; i++) v[k][4 * e + i] = y[i] * g;
         }
       }
       const int64_t out_row = (int64_t)(s.q0 + token) * a.q_heads + qh;
