@@ -4,7 +4,6 @@ import numpy as np
 import pytest
 import torch
 
-import oracle
 import w4a4_integer_quantized_amd as rq
 from tests import kv_ref
 from tests.gpu_util import need_gpu

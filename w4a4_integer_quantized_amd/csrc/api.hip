@@ -483,8 +483,7 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
     if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
       return fail(RQ_EINVAL, "kv_len, pages, q_start or lse is not 4-byte aligned");
   *max_q_len = max_q;
-  *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
-                                     p->window);
+  *plan = convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q, max_kv, p->window);
   // A grid has fewer than 2^32 threads, 256 a workgroup. (Splits come with few rows: the join's fits.)
   if (((int64_t)p->seqs * plan->splits + 8) * cfg->kv_heads >= ((int64_t)1 << 24) / plan->row_tiles)
     return fail(RQ_EUNSUPPORTED, "%d sequences of up to %lld query rows: too many workgroups (give max_q_len)", p->seqs,
@@ -677,8 +676,7 @@ rq_status rq_kv_cache_read(const void* cache, int64_t num_pages, const int64_t* 
 size_t rq_kv_attention_workspace_size(const rq_kv_attention_params* p, const rq_kv_config* cfg) {
   int64_t max_q = 0, max_kv = 0;
   if (check_kv_shape(p, cfg, &max_q, &max_kv) != RQ_OK || p->total_q == 0) return 0;
-  return convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, cfg->bits, max_q, max_kv,
-                                    p->window)
+  return convrot::plan_kv_attention(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q, max_kv, p->window)
       .workspace_bytes;
 }
 

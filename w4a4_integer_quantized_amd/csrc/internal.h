@@ -95,7 +95,7 @@ struct KvAttentionPlan {
   int splits, row_tiles, chunk, block;
   size_t workspace_bytes;
 };
-KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int bits,
+KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim,
                                   int64_t max_q_len, int64_t max_kv_len, int window);
 hipError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, int bits, hipStream_t stream);
 

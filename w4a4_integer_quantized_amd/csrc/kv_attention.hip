@@ -1292,7 +1292,7 @@ hipError_t launch(const KvAttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int bits,
+KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int heads, int head_dim,
                                   int64_t max_q_len, int64_t max_kv_len, int window) {
   const int64_t group = q_heads / heads;
   KvAttentionPlan p;
