@@ -738,7 +738,9 @@ __device__ __forceinline__ void times_scale16(float (&a)[16], const float (&b)[1
 }
 
 // At head_dim 64 in bf16 three waves a SIMD: 168 registers, two of them spilled with 8-bit codes (2 x 4096 x 4096,
-// 12 heads: 169 us; 188 with 170 registers and two waves).
+// 12 heads: 169 us; 188 with 170 registers and two waves). In fp16 the rests of queries and weights do not
+// all fit: 57 registers are spilled at head_dim 256 with 8-bit codes, 46 with 4-bit ones, 2 at 128 with 8-bit
+// ones (that shape in fp16 and bf16: 1141 and 698 us, 1071 and 666, 408 and 287).
 template <int D, int BITS, bool SPLIT>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 64 && !SPLIT ? 3 : 2) void kv_attend_block_kernel(KvAttentionArgs a) {
   using R = Row<D, BITS>;
