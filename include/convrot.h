@@ -340,8 +340,9 @@ size_t rq_kv_attention_workspace_size(const rq_kv_attention_params *p, const rq_
 /*   workspace  ws_bytes >= rq_kv_attention_workspace_size() bytes, or NULL if that is 0; nothing
  *              in it needs to start at zero, nothing is kept in it between calls. Limit:
  *              total_q * q_heads <= 2^30. A ragged batch of many sequences should give max_q_len:
- *              without it every sequence is launched as if it had all rows, and 2^24 workgroups
- *              or more are refused (RQ_EUNSUPPORTED). */
+ *              without it every sequence is launched as if it had all rows (64 single tokens of 32
+ *              heads over up to 8192: 325 us in place of 75), and 2^24 workgroups or more are
+ *              refused (RQ_EUNSUPPORTED). */
 rq_status rq_kv_attention(const rq_kv_attention_params *p, const rq_kv_config *cfg,
                           const void *cache, int64_t num_pages, void *workspace, size_t ws_bytes,
                           void *stream);
