@@ -30,8 +30,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTop = 7.0f;        // log2 of the largest weight when b is set
 constexpr float kMost = 32768.0f;   // weights above this move b
-constexpr float kMostExp = 90.0f;   // log2 of the p' that a moved b allows, and the sum that
-constexpr float kMostSum = 0x1p120f;   // moves it
+// log2 of the p' that a moved b allows (beside a key of that p' whose value is zero, what others add is
+// lost below 2^-115 of l), and the sum that moves b.
+constexpr float kMostExp = 90.0f;
+constexpr float kMostSum = 0x1p120f;
 constexpr float kNoRef = -3.0e38f;  // b of a row that has met no key
 constexpr int kMinChunk = 1024;     // keys
 // More query rows of a sequence and key head than this go by blocks of 128. Measured at 8 heads of 128,
