@@ -168,6 +168,37 @@ rq_status rq_quantize_weights(const void *W, int32_t w_dtype, int64_t N, int64_t
 rq_status rq_rotate_quantize(const void *X, int32_t x_dtype, int64_t M, int64_t K,
                              const rq_qconfig *cfg, void *Xq, float *x_scale, void *stream);
 
+/* Root-mean-square norm with the residual's addition in front of a linear, rotated and quantized in
+ * one pass over the rows:
+ *   h = X + residual, rounded to the rows' type (without a residual h = X),
+ *   v[k] = fl(h[k] * weight[k]), codes of v as rq_rotate_quantize gives them for v in binary32,
+ *   x_scale = fl(scale * fl(1 / fl(sqrt(fl(sum h^2 / K + eps))))), scale that of v.
+ * The norm's factor is one positive number a row, which the quantizer divides out again: codes do
+ * not depend on it and are exact, bit for bit; the scale carries the rounding of the sum of squares
+ * (binary32, in no fixed order; in binary64 where squares leave binary32's range). A row that is
+ * quantized as a zero row has scale 0. Codes and scales go to rq_gemm_dequant or rq_gemm_gated. */
+typedef struct {
+  const void *X;             /* [M, K] device, of dtype */
+  const void *residual;      /* [M, K] of dtype, or NULL */
+  const void *weight;        /* [K] of w_dtype, or NULL (ones) */
+  void *H;                   /* out: h [M, K] of dtype, or NULL (not kept). May be X or residual
+                                itself (same address and stride); its rows must not overlap
+                                theirs in another way, nor one another */
+  void *Xq;                  /* out: rq_codes_bytes(M, K, cfg) bytes in cfg->x_layout */
+  float *x_scale;            /* out: [M] */
+  int64_t M, K;
+  int64_t x_stride, residual_stride, h_stride;   /* of rows, in elements: multiples of 16 bytes, at
+                                                    most 2^27 bytes; X and residual may repeat rows
+                                                    (any value >= 0) */
+  int32_t dtype;             /* RQ_F32, RQ_F16 or RQ_BF16 */
+  int32_t w_dtype;           /* RQ_F32 or dtype (not looked at without a weight) */
+  float eps;                 /* finite and >= 0 */
+} rq_norm_params;
+
+/* A launch has fewer than 2^32 threads: M below 2^23 always fits (more with smaller K); a larger call
+ * returns RQ_EUNSUPPORTED. */
+rq_status rq_norm_rotate_quantize(const rq_norm_params *p, const rq_qconfig *cfg, void *stream);
+
 /* Bytes of device workspace rq_rotq_linear needs: Xq in RQ_X_TILED layout (RQ_X_FP6 when
  * cfg->w_layout is RQ_W_FP6; rq_codes_bytes(M, K) with that x_layout) followed by x_scale [M],
  * each rounded up to 256 bytes. Returns 0 if cfg is invalid. */

@@ -13,7 +13,7 @@ from .binding import (  # noqa: F401
     rq_kv_attention, rq_kv_attention_params, rq_kv_attention_workspace_size, rq_kv_cache_read, rq_kv_cache_write,
     rq_kv_config, rq_kv_page_bytes,
     make_cfg, rq_codes_bytes, rq_weight_bytes,
-    quantize_weights, rotate_quantize, rotq_linear, rq_check_rotq_linear_args, rq_gemm_dequant,
+    norm_rotate_quantize, quantize_weights, rotate_quantize, rotq_linear, rq_norm_params, rq_norm_rotate_quantize, rq_check_rotq_linear_args, rq_gemm_dequant,
     rq_gemm_s32, rq_qconfig, rq_quantize_weights, rq_rotate_quantize, rq_rotq_linear,
     rq_rotq_linear_noalloc,
     rq_rotq_linear_workspace_size, rq_status_string, workspace_size,

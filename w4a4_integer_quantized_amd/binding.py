@@ -6,8 +6,8 @@ the library is missing or a call fails, a ConvRotError is raised.
 
 Two layers:
   * ``rq_*`` -- the C entry points under their own names, taking integer device pointers;
-  * ``quantize_weights``, ``rotq_linear``, ``rotate_quantize``, ``gemm_dequant``,
-    ``gemm_s32``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
+  * ``quantize_weights``, ``rotq_linear``, ``rotate_quantize``, ``norm_rotate_quantize``,
+    ``gemm_dequant``, ``gemm_s32``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
     stream.
 """
 from __future__ import annotations
@@ -38,6 +38,12 @@ class rq_qconfig(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("rot_kind", ctypes.c_int32), ("rot_block", ctypes.c_int32),
                 ("x_layout", ctypes.c_int32), ("w_scale_mode", ctypes.c_int32), ("w_layout", ctypes.c_int32),
                 ("act", ctypes.c_int32)]
+
+
+class rq_norm_params(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("X", "residual", "weight", "H", "Xq", "x_scale")]
+                + [(n, ctypes.c_int64) for n in ("M", "K", "x_stride", "residual_stride", "h_stride")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "w_dtype")] + [("eps", ctypes.c_float)])
 
 
 class rq_kv_config(ctypes.Structure):
@@ -76,6 +82,7 @@ def load():
     sig = {
         "rq_quantize_weights": [P, I32, I64, I64, CFG, P, P, P],
         "rq_rotate_quantize": [P, I32, I64, I64, CFG, P, P, P],
+        "rq_norm_rotate_quantize": [ctypes.POINTER(rq_norm_params), CFG, P],
         "rq_rotq_linear": [P, I32, I64, I64, P, P, I64, P, CFG, P, P, SZ, P],
         "rq_rotq_linear_noalloc": [P, I32, I64, I64, P, P, I64, P, CFG, P, P],
         "rq_gemm_dequant": [P, P, P, P, P, I64, I64, I64, CFG, P, I32, P],
@@ -134,6 +141,10 @@ def rq_quantize_weights(W, w_dtype, N, K, cfg, Wq, w_scale, stream) -> int:
 
 def rq_rotate_quantize(X, x_dtype, M, K, cfg, Xq, x_scale, stream) -> int:
     return load().rq_rotate_quantize(X, x_dtype, M, K, ctypes.byref(cfg), Xq, x_scale, stream)
+
+
+def rq_norm_rotate_quantize(params, cfg, stream) -> int:
+    return load().rq_norm_rotate_quantize(ctypes.byref(params), ctypes.byref(cfg), stream)
 
 
 def rq_rotq_linear(X, x_dtype, M, K, Wq, w_scale, N, bias, cfg, Y, ws, ws_bytes, stream) -> int:
@@ -317,6 +328,57 @@ def rotate_quantize(X, bits: int = 8, rot: int = 128, stream=None, x_layout: int
     return Xq, xs
 
 
+def _norm_rows(t, name, shape, dtype):
+    """The row stride of rows [M, K]."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be a %s tensor of shape %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    row, last = t.stride()
+    if last != 1:
+        raise ValueError("%s must be contiguous along its last axis" % name)
+    return row
+
+
+def norm_rotate_quantize(X, residual=None, weight=None, eps: float = 1e-6, bits: int = 8, rot: int = 128,
+                         x_layout: int = RQ_X_ROWS, out=None, stream=None):
+    """Root-mean-square norm with the residual's addition in front of a linear: (Xq, x_scale, H).
+
+    H = X + residual in X's dtype, [M, K] (f32/f16/bf16; rows of any stride that is a multiple of 16
+    bytes, last axis contiguous); Xq and x_scale are codes and scales of the rotated rows
+    H / rms(H) * weight, as rotate_quantize gives them, for gemm_dequant or gemm_gated. weight [K] is
+    float32 or X's dtype (None: ones). Without a residual H is X itself, and nothing is stored. out:
+    where H goes; it may be X or residual itself."""
+    kv = _kv()
+    dtype, shape = X.dtype, X.shape
+    if len(shape) != 2 or dtype not in kv.rows:
+        raise ValueError("X must be a 2-D float32, float16 or bfloat16 tensor, got %s %s" % (dtype, tuple(shape)))
+    M, K = shape
+    xs = _norm_rows(X, "X", shape, dtype)
+    rs = _norm_rows(residual, "residual", shape, dtype) if residual is not None else 0
+    hs = _norm_rows(out, "out", shape, dtype) if out is not None else K
+    if weight is not None and (weight.shape != (K,) or weight.dtype not in (kv.float32, dtype) or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous float32 or %s vector of %d elements, got %s %s"
+                         % (dtype, K, weight.dtype, tuple(weight.shape)))
+    index = _kv_device(X, residual, weight, out)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return norm_rotate_quantize(X, residual, weight, eps, bits, rot, x_layout, out)
+    cfg = make_cfg(bits, rot, x_layout=x_layout)
+    if x_layout == RQ_X_ROWS:
+        Xq = X.new_empty(code_shape(M, K, bits), dtype=kv.int8 if bits == 8 else kv.uint8)
+    else:
+        Xq = X.new_empty((max(rq_codes_bytes(M, K, cfg), 1),), dtype=kv.uint8)
+    x_scale = X.new_empty((M,), dtype=kv.float32)
+    H = out
+    if out is None:
+        H = X if residual is None else X.new_empty(shape)
+    p = rq_norm_params(X.data_ptr(), None if residual is None else residual.data_ptr(),
+                       None if weight is None else weight.data_ptr(),
+                       None if out is None and residual is None else H.data_ptr(), Xq.data_ptr(), x_scale.data_ptr(), M, K, xs, rs,
+                       hs, kv.rows[dtype], kv.rows[dtype if weight is None else weight.dtype], eps)
+    _check(rq_norm_rotate_quantize(p, cfg, kv.raw_stream(index)), "rq_norm_rotate_quantize")
+    return Xq, x_scale, H
+
+
 def _check_weights(Wq, w_scale, bias, N, K, cfg):
     _check_vec(w_scale, "w_scale", N)
     if bias is not None:
@@ -426,6 +488,7 @@ class _Kv:
         self.rows = {torch.float32: RQ_F32, torch.float16: RQ_F16, torch.bfloat16: RQ_BF16}
         self.halves = {torch.float16: RQ_F16, torch.bfloat16: RQ_BF16}
         self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
+        self.int8, self.float32 = torch.int8, torch.float32
         self.empty_like, self.cuda = torch.empty_like, torch.cuda
         self.current_device, self.raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
 

@@ -266,6 +266,73 @@ rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const
   return ok();
 }
 
+// ---- the norm in front of a linear
+constexpr int64_t kMaxNormStride = int64_t(1) << 27;    // bytes: a workgroup's rows (up to 16) span less than 2^31
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1; // of a launch
+
+int rows_meet(int64_t n, int64_t dim, int64_t ks, int64_t vs, int64_t r);
+
+// Rows [M, K] with a stride in elements of `es` bytes; returns what they span.
+rq_status check_norm_rows(const void* p, const char* name, int64_t M, int64_t K, int64_t es, int64_t stride, bool out,
+                          int64_t* bytes) {
+  rq_status s = check_ptr(p, name);
+  if (s) return s;
+  if (M == 1) stride = 0;   // never taken
+  if (stride < 0 || stride > kMaxNormStride / es || stride * es % 16 != 0)
+    return fail(RQ_EINVAL, "%s stride %lld (need a multiple of 16 bytes in [0, 2^27] bytes)", name, (long long)stride);
+  if (out && M > 1 && stride < K) return fail(RQ_EINVAL, "%s stride %lld < K: rows overlap", name, (long long)stride);
+  *bytes = ((M - 1) * stride + K) * es;
+  return ok();
+}
+
+// H next to an input: the same rows, or none of the same.
+rq_status check_norm_apart(const rq_norm_params* p, int64_t es, int64_t hb, const void* in, int64_t in_bytes,
+                           int64_t in_stride, const char* name) {
+  if (!overlap(p->H, hb, in, in_bytes)) return ok();
+  const int64_t hs = p->M == 1 ? 0 : p->h_stride, is = p->M == 1 ? 0 : in_stride;
+  if (p->H == in && hs == is) return ok();
+  const int64_t r = (int64_t)(reinterpret_cast<intptr_t>(in) - reinterpret_cast<intptr_t>(p->H)) / es;
+  if (rows_meet(p->M, p->K, hs, is, r) != 0)
+    return fail(RQ_EINVAL, "H overlaps %s without being the same rows", name);
+  return ok();
+}
+
+rq_status check_norm(const rq_norm_params* p, const rq_qconfig* cfg) {
+  rq_status s = check_cfg(cfg);
+  if (s) return s;
+  if (!p) return fail(RQ_EINVAL, "params is NULL");
+  if (p->dtype != RQ_F32 && p->dtype != RQ_F16 && p->dtype != RQ_BF16) return fail(RQ_EINVAL, "bad X dtype %d", p->dtype);
+  if (p->weight && p->w_dtype != RQ_F32 && p->w_dtype != p->dtype)
+    return fail(RQ_EINVAL, "weight dtype %d (need RQ_F32 or that of X, %d)", p->w_dtype, p->dtype);
+  if (!(p->eps >= 0.0f) || p->eps > 3.4028234e38f) return fail(RQ_EINVAL, "eps = %g (need a finite value >= 0)", (double)p->eps);
+  if ((s = check_rows_k(p->M, p->K, "X"))) return s;
+  if (p->M == 0) return ok();
+  if (convrot::norm_quant_threads(p->M, p->K) > kMaxThreads)
+    return fail(RQ_EUNSUPPORTED, "M = %lld rows of K = %lld: 2^32 threads or more", (long long)p->M, (long long)p->K);
+  const int64_t es = elem_size(p->dtype);
+  int64_t xb = 0, rb = 0, hb = 0;
+  if ((s = check_norm_rows(p->X, "X", p->M, p->K, es, p->x_stride, false, &xb))) return s;
+  if (p->residual && (s = check_norm_rows(p->residual, "residual", p->M, p->K, es, p->residual_stride, false, &rb))) return s;
+  if (p->H && (s = check_norm_rows(p->H, "H", p->M, p->K, es, p->h_stride, true, &hb))) return s;
+  if ((s = check_ptr(p->weight, "weight", false))) return s;
+  if ((s = check_ptr(p->Xq, "Xq"))) return s;
+  if (!p->x_scale) return fail(RQ_EINVAL, "x_scale is NULL");
+  if ((reinterpret_cast<uintptr_t>(p->x_scale) & 3u) != 0) return fail(RQ_EINVAL, "x_scale is not 4-byte aligned");
+  const int64_t qb = x_code_bytes(p->M, p->K, cfg->bits, cfg->x_layout), wb = p->K * elem_size(p->w_dtype);
+  const struct { const void* at; int64_t bytes; } outs[2] = {{p->Xq, qb}, {p->x_scale, p->M * 4}},
+                                                 others[4] = {{p->X, xb}, {p->residual, rb}, {p->weight, wb}, {p->H, hb}};
+  for (const auto& o : outs)
+    for (const auto& i : others)
+      if (overlap(o.at, o.bytes, i.at, i.bytes)) return fail(RQ_EINVAL, "Xq or x_scale overlaps an input or H");
+  if (overlap(p->Xq, qb, p->x_scale, p->M * 4)) return fail(RQ_EINVAL, "Xq overlaps x_scale");
+  if (p->H) {
+    if (overlap(p->H, hb, p->weight, wb)) return fail(RQ_EINVAL, "H overlaps the weight");
+    if ((s = check_norm_apart(p, es, hb, p->X, xb, p->x_stride, "X"))) return s;
+    if (p->residual && (s = check_norm_apart(p, es, hb, p->residual, rb, p->residual_stride, "residual"))) return s;
+  }
+  return ok();
+}
+
 // ---- the cache operators
 constexpr int64_t kMaxKvTokens = int64_t(1) << 30;   // of a sequence's page table
 constexpr int64_t kMaxKvBytes = int64_t(1) << 46;    // of a cache, and of what strided rows span
@@ -570,6 +637,30 @@ rq_status rq_rotate_quantize(const void* X, int32_t x_dtype, int64_t M, int64_t 
   return from_hip(convrot::launch_rotate_quant(X, x_dtype, M, K, cfg->bits, code_layout(cfg->x_layout),
                                                Xq, x_scale, static_cast<hipStream_t>(stream)),
                   "rotate_quant launch");
+}
+
+rq_status rq_norm_rotate_quantize(const rq_norm_params* p, const rq_qconfig* cfg, void* stream) {
+  rq_status s = check_norm(p, cfg);
+  if (s || p->M == 0) return s;
+  const int64_t es = elem_size(p->dtype);
+  convrot::NormQuantArgs a = {};
+  a.x = static_cast<const uint8_t*>(p->X);
+  a.res = static_cast<const uint8_t*>(p->residual);
+  a.weight = static_cast<const uint8_t*>(p->weight);
+  a.weight_f32 = p->w_dtype == RQ_F32;
+  a.h = static_cast<uint8_t*>(p->H);
+  a.codes = static_cast<uint8_t*>(p->Xq);
+  a.scales = p->x_scale;
+  if (p->M > 1) {   // a single row's strides are never taken
+    a.x_stride = p->x_stride * es;
+    a.res_stride = p->residual_stride * es;
+    a.h_stride = p->h_stride * es;
+  }
+  a.M = p->M;
+  a.K = static_cast<int>(p->K);
+  a.layout = code_layout(cfg->x_layout);
+  a.eps = p->eps;
+  return from_hip(convrot::launch_norm_quant(a, p->dtype, cfg->bits, static_cast<hipStream_t>(stream)), "norm_quant launch");
 }
 
 rq_status rq_check_rotq_linear_args(const void* X, int32_t x_dtype, int64_t M, int64_t K,

@@ -21,6 +21,22 @@ enum CodeLayout { kCodeRows = 0, kCodeTiled = 1, kCodeFp6X = 2, kCodeFp6W = 3 };
 hipError_t launch_rotate_quant(const void* X, int dt, int64_t rows, int64_t K, int bits,
                                int layout, void* Q, float* S, hipStream_t stream);
 
+// The norm with the residual's addition, rotated and quantized (norm_quant.hip). Strides in bytes,
+// below 2^27; pre-validated, fewer than 2^32 threads.
+struct NormQuantArgs {
+  const uint8_t *x, *res;      // [M, K]; res null: none
+  const uint8_t* weight;       // [K], binary32 (weight_f32) or the rows' type; null: ones
+  uint8_t* h;                  // out: x + res; null: not kept
+  uint8_t* codes;
+  float* scales;
+  int64_t x_stride, res_stride, h_stride, M;
+  int K, weight_f32, layout;   // layout: a CodeLayout
+  int lanes;                   // of a row (set by the launcher)
+  float eps;
+};
+int64_t norm_quant_threads(int64_t M, int64_t K);   // of the launch
+hipError_t launch_norm_quant(const NormQuantArgs& a, int dt, int bits, hipStream_t stream);
+
 // The weight quantizer's MSE-clipped (kWScaleMse) or tensor-wise (kWScaleTensor) scale rule:
 // codes Wq (row-major int8 / packed int4, or FP6 tiles of 128-row panels when fp6) and one fp32
 // scale per row. Arguments are pre-validated; N < 2^31.
