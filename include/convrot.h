@@ -118,8 +118,11 @@ enum { RQ_W_ABSMAX = 0, RQ_W_MSE = 1, RQ_W_TENSOR = 2 };
  *   RQ_ACT_GELU_TANH  v * logistic(2u), u = sqrt(2/pi) (v + 0.044715 v^3)   (the tanh form,
  *                     0.5 v (1 + tanh u)), the logistic as 1/(1+e) or e/(1+e), e = exp(-2|u|)
  * which is within a few binary32 ulps of the exact value: the output is the correctly rounded
- * GELU except, rarely, one ulp away next to a rounding midpoint. RQ_ACT_NONE stores v itself. */
-enum { RQ_ACT_NONE = 0, RQ_ACT_GELU_ERF = 1, RQ_ACT_GELU_TANH = 2 };
+ * GELU except, rarely, one ulp away next to a rounding midpoint. RQ_ACT_NONE stores v itself.
+ *
+ *   RQ_ACT_SILU       v * logistic(v), only for the gated products (rq_gemm_gated,
+ *                     rq_rotq_gated_linear); rq_gemm_dequant and rq_rotq_linear refuse it */
+enum { RQ_ACT_NONE = 0, RQ_ACT_GELU_ERF = 1, RQ_ACT_GELU_TANH = 2, RQ_ACT_SILU = 3 };
 
 typedef struct {
   int32_t bits;       /* 8 (W8A8) or 4 (W4A4) */
@@ -136,8 +139,9 @@ typedef struct {
                            RQ_W_FP6; rq_rotq_linear picks its workspace layout to match. */
   int32_t act;          /* RQ_ACT_NONE, RQ_ACT_GELU_ERF or RQ_ACT_GELU_TANH: activation applied
                            by the epilogue of rq_rotq_linear and rq_gemm_dequant to each fp32
-                           value before its fp16/bf16 rounding (below); ignored by the other
-                           entry points. */
+                           value before its fp16/bf16 rounding (below); these or RQ_ACT_SILU: the
+                           gate's, of rq_rotq_gated_linear and rq_gemm_gated; ignored by the
+                           other entry points. */
 } rq_qconfig;
 
 /* Bytes of activation codes for `rows` rows of length K in cfg's bits and x_layout
@@ -245,6 +249,33 @@ rq_status rq_gemm_dequant(const void *Xq, const float *x_scale, const void *Wq,
                           const float *w_scale, const float *bias, int64_t M, int64_t N,
                           int64_t K, const rq_qconfig *cfg, void *Y, int32_t y_dtype,
                           void *stream);
+
+/* The gated product of a feed-forward block: both projections, the activation and the product in
+ * one kernel,
+ *   Y[m, n] = act(g) * u,  g = fma(f32(acc_g), fl(s_g * x_scale[m]), b_g), u likewise,
+ * acc_g, s_g, b_g of the gate projection's row n and acc_u, s_u, b_u of the up projection's, act
+ * cfg->act (RQ_ACT_NONE: g itself), evaluated in binary32 as above, the product rounded to binary32
+ * and then to y_dtype.
+ *   Wq       codes of ONE matrix of 2 N rows in cfg->w_layout: row 32 i + r is the gate projection's
+ *            row 16 i + r and row 32 i + 16 + r the up projection's (0 <= r < 16), so that both
+ *            values of an output come out in one lane. rq_quantize_weights of the matrix laid out so
+ *            gives it (rows are quantized by themselves)
+ *   w_scale, bias   [2 N] in the same order (bias NULL: none)
+ *   Xq, x_scale     M rows of codes in cfg->x_layout, as rq_rotate_quantize or
+ *                   rq_norm_rotate_quantize write them
+ *   Y        out: [M, N] of y_dtype (RQ_F16 or RQ_BF16), must not overlap an input
+ * N % 16 == 0, 2 N < 2^31, and ceil(M / 256) * ceil(2 N / 128) < 2^23. */
+rq_status rq_gemm_gated(const void *Xq, const float *x_scale, const void *Wq, const float *w_scale,
+                        const float *bias, int64_t M, int64_t N, int64_t K, const rq_qconfig *cfg,
+                        void *Y, int32_t y_dtype, void *stream);
+
+/* The same from the activations themselves: rotate + quantize X, then the gated product.
+ *   X         [M, K] device, x_dtype RQ_F16 or RQ_BF16; Y has its dtype
+ *   workspace ws_bytes >= rq_rotq_linear_workspace_size(M, K, cfg) */
+rq_status rq_rotq_gated_linear(const void *X, int32_t x_dtype, int64_t M, int64_t K, const void *Wq,
+                               const float *w_scale, int64_t N, const float *bias,
+                               const rq_qconfig *cfg, void *Y, void *workspace, size_t ws_bytes,
+                               void *stream);
 
 /* The exact int32 accumulators acc[M, N] = sum_k Xq[m,k] * Wq[n,k] (for bit-exact checks);
  * Xq in cfg->x_layout. For every shape, bits and layout this runs the kernel, launch geometry

@@ -7,7 +7,7 @@ the library is missing or a call fails, a ConvRotError is raised.
 Two layers:
   * ``rq_*`` -- the C entry points under their own names, taking integer device pointers;
   * ``quantize_weights``, ``rotq_linear``, ``rotate_quantize``, ``norm_rotate_quantize``,
-    ``gemm_dequant``, ``gemm_s32``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
+    ``gemm_dequant``, ``gemm_s32``, ``rotq_gated_linear``, ``gemm_gated``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
     stream.
 """
 from __future__ import annotations
@@ -25,7 +25,7 @@ RQ_ROT_WHT = 1
 RQ_X_ROWS, RQ_X_TILED, RQ_X_FP6 = 0, 1, 2
 RQ_W_ROWS, RQ_W_FP6 = 0, 1
 RQ_W_ABSMAX, RQ_W_MSE, RQ_W_TENSOR = 0, 1, 2
-RQ_ACT_NONE, RQ_ACT_GELU_ERF, RQ_ACT_GELU_TANH = 0, 1, 2
+RQ_ACT_NONE, RQ_ACT_GELU_ERF, RQ_ACT_GELU_TANH, RQ_ACT_SILU = 0, 1, 2, 3
 
 
 class ConvRotError(RuntimeError):
@@ -86,6 +86,8 @@ def load():
         "rq_rotq_linear": [P, I32, I64, I64, P, P, I64, P, CFG, P, P, SZ, P],
         "rq_rotq_linear_noalloc": [P, I32, I64, I64, P, P, I64, P, CFG, P, P],
         "rq_gemm_dequant": [P, P, P, P, P, I64, I64, I64, CFG, P, I32, P],
+        "rq_gemm_gated": [P, P, P, P, P, I64, I64, I64, CFG, P, I32, P],
+        "rq_rotq_gated_linear": [P, I32, I64, I64, P, P, I64, P, CFG, P, P, SZ, P],
         "rq_gemm_s32": [P, P, I64, I64, I64, CFG, P, P],
         "rq_check_rotq_linear_args": [P, I32, I64, I64, P, P, I64, P, CFG, P, P, SZ],
         "rq_kv_cache_write": [P, P, I32, I64, I64, I64, I64, I64, P, KV, P, I64, P],
@@ -162,6 +164,14 @@ def rq_rotq_linear_noalloc(X, x_dtype, M, K, Wq, w_scale, N, bias, cfg, Y, strea
 def rq_gemm_dequant(Xq, x_scale, Wq, w_scale, bias, M, N, K, cfg, Y, y_dtype, stream) -> int:
     return load().rq_gemm_dequant(Xq, x_scale, Wq, w_scale, bias, M, N, K, ctypes.byref(cfg), Y,
                                   y_dtype, stream)
+
+
+def rq_gemm_gated(Xq, x_scale, Wq, w_scale, bias, M, N, K, cfg, Y, y_dtype, stream) -> int:
+    return load().rq_gemm_gated(Xq, x_scale, Wq, w_scale, bias, M, N, K, ctypes.byref(cfg), Y, y_dtype, stream)
+
+
+def rq_rotq_gated_linear(X, x_dtype, M, K, Wq, w_scale, N, bias, cfg, Y, ws, ws_bytes, stream) -> int:
+    return load().rq_rotq_gated_linear(X, x_dtype, M, K, Wq, w_scale, N, bias, ctypes.byref(cfg), Y, ws, ws_bytes, stream)
 
 
 def rq_gemm_s32(Xq, Wq, M, N, K, cfg, acc, stream) -> int:
@@ -446,6 +456,111 @@ def gemm_dequant(Xq, x_scale, Wq, w_scale, bias=None, bits: int = 8, K: Optional
                            _dev(bias, "bias") if bias is not None else None, M, N, K, cfg, Y.data_ptr(),
                            _dtype_code(Y), _stream(stream)), "rq_gemm_dequant")
     return Y
+
+
+def interleave_gated(gate, up):
+    """The order in which a gated product takes its rows: 16 of gate and 16 of up in turn. gate and up
+    are matrices [N, K] or vectors [N] (scales, biases) of one shape and dtype, N a multiple of 16;
+    the result has 2 N rows."""
+    torch = _torch()
+    if gate.shape != up.shape or gate.dtype != up.dtype or gate.dim() not in (1, 2):
+        raise ValueError("gate and up must be two matrices or vectors of one shape and dtype, got %s %s and %s %s"
+                         % (gate.dtype, tuple(gate.shape), up.dtype, tuple(up.shape)))
+    if gate.shape[0] % 16:
+        raise ValueError("gate and up need a multiple of 16 rows, got %d" % gate.shape[0])
+    _same_device(gate, up)
+    both = torch.stack((gate.unflatten(0, (-1, 16)), up.unflatten(0, (-1, 16))), dim=1)
+    return both.flatten(0, 2)
+
+
+def quantize_gated_weights(gate, up, bits: int = 8, rot: int = 128, stream=None, w_scale_mode: int = RQ_W_ABSMAX,
+                           w_layout: int = RQ_W_ROWS):
+    """Offline: the weights gate and up [N, K] of a gated product -> (Wq, w_scale f32 [2 N]) of their
+    interleaved rows, as quantize_weights gives them (RQ_W_TENSOR: one scale for both)."""
+    torch = _torch()
+    _check_2d(gate, "gate", (torch.float32, torch.float16, torch.bfloat16))
+    _check_2d(up, "up", (gate.dtype,))
+    if stream is None:
+        return quantize_weights(interleave_gated(gate, up), bits, rot, None, w_scale_mode, w_layout)
+    with torch.cuda.stream(stream):
+        return quantize_weights(interleave_gated(gate, up), bits, rot, None, w_scale_mode, w_layout)
+
+
+def _check_gated(Wq, w_scale, bias, K, cfg):
+    """N of a gated product's operands."""
+    rows = w_scale.shape[0] if w_scale.dim() == 1 else -1
+    if rows < 0 or rows % 32:
+        raise ValueError("w_scale must be a vector of 2 N elements, N a multiple of 16, got %s" % (tuple(w_scale.shape),))
+    _check_weights(Wq, w_scale, bias, rows, K, cfg)
+    return rows // 2
+
+
+def gemm_gated(Xq, x_scale, Wq, w_scale, bias=None, bits: int = 8, K: Optional[int] = None, out_dtype=None, stream=None,
+               x_layout: int = RQ_X_ROWS, w_layout: int = RQ_W_ROWS, act: int = RQ_ACT_SILU, out=None):
+    """Y [M, N] = act(gate) * up of two projections' rows from codes (rotate_quantize's or
+    norm_rotate_quantize's); Wq, w_scale and bias have 2 N rows in interleave_gated's order. M =
+    len(x_scale), K from Wq unless given (give K for FP6 weight tiles). out_dtype float16 (default)
+    or bfloat16, or that of out."""
+    kv = _kv()
+    M = x_scale.shape[0] if x_scale.dim() == 1 else -1
+    K = _gemm_k(Wq, bits, K)
+    cfg = make_cfg(bits, x_layout=x_layout, w_layout=w_layout, act=act)
+    _check_vec(x_scale, "x_scale", M)
+    N = _check_gated(Wq, w_scale, bias, K, cfg)
+    _check_bytes(Xq, "Xq", rq_codes_bytes(M, K, cfg), exact=False)
+    if out is not None:
+        if out_dtype not in (None, out.dtype) or out.shape != (M, N) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of shape (%d, %d) and of out_dtype, got %s %s"
+                             % (M, N, out.dtype, tuple(out.shape)))
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = _torch().float16
+    if out_dtype not in kv.halves:
+        raise ValueError("out_dtype must be float16 or bfloat16")
+    index = _kv_device(Xq, x_scale, Wq, w_scale, bias, out)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return gemm_gated(Xq, x_scale, Wq, w_scale, bias, bits, K, out_dtype, None, x_layout, w_layout, act, out)
+    if out is None:
+        out = Xq.new_empty((M, N), dtype=out_dtype)
+    _check(rq_gemm_gated(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
+                         None if bias is None else bias.data_ptr(), M, N, K, cfg, out.data_ptr(), kv.halves[out_dtype],
+                         kv.raw_stream(index)), "rq_gemm_gated")
+    return out
+
+
+def rotq_gated_linear(X, Wq, w_scale, bias=None, bits: int = 8, rot: int = 128, workspace=None, out=None, stream=None,
+                      w_layout: int = RQ_W_ROWS, act: int = RQ_ACT_SILU):
+    """Y [M, N] = act(gate) * up of two projections of X [M, K] (f16/bf16), in X's dtype: rotate +
+    quantize, then both products, the activation and the product in one kernel. Wq, w_scale and bias
+    have 2 N rows in interleave_gated's order (quantize_gated_weights); act is RQ_ACT_SILU,
+    RQ_ACT_GELU_ERF, RQ_ACT_GELU_TANH or RQ_ACT_NONE. workspace: a uint8 tensor of
+    workspace_size(M, K, bits, w_layout) bytes or more."""
+    kv = _kv()
+    dtype, shape = X.dtype, X.shape
+    if len(shape) != 2 or dtype not in kv.halves or not X.is_contiguous():
+        raise ValueError("X must be a contiguous 2-D float16 or bfloat16 tensor, got %s %s" % (dtype, tuple(shape)))
+    M, K = shape
+    cfg = make_cfg(bits, rot, w_layout=w_layout, act=act)
+    N = _check_gated(Wq, w_scale, bias, K, cfg)
+    need = rq_rotq_linear_workspace_size(M, K, cfg)
+    if workspace is not None:
+        _check_bytes(workspace, "workspace", need, exact=False)
+    if out is not None and (out.shape != (M, N) or out.dtype != dtype or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous %s tensor of shape (%d, %d), got %s %s"
+                         % (dtype, M, N, out.dtype, tuple(out.shape)))
+    index = _kv_device(X, Wq, w_scale, bias, workspace, out)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return rotq_gated_linear(X, Wq, w_scale, bias, bits, rot, workspace, out, None, w_layout, act)
+    if workspace is None:
+        workspace = X.new_empty((max(need, 256),), dtype=kv.uint8)
+    if out is None:
+        out = X.new_empty((M, N))
+    _check(rq_rotq_gated_linear(X.data_ptr(), kv.halves[dtype], M, K, Wq.data_ptr(), w_scale.data_ptr(), N,
+                                None if bias is None else bias.data_ptr(), cfg, out.data_ptr(), workspace.data_ptr(),
+                                _nbytes(workspace), kv.raw_stream(index)), "rq_rotq_gated_linear")
+    return out
 
 
 def gemm_s32(Xq, Wq, bits: int = 8, K: Optional[int] = None, stream=None,

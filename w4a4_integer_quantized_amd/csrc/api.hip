@@ -72,7 +72,8 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
-rq_status check_cfg(const rq_qconfig* cfg) {
+// `act`: whether the entry point applies cfg->act to a plain linear, which has no SiLU.
+rq_status check_cfg(const rq_qconfig* cfg, bool act = false) {
   if (!cfg) return fail(RQ_EINVAL, "cfg is NULL");
   if (cfg->bits != 8 && cfg->bits != 4)
     return fail(RQ_EUNSUPPORTED, "bits = %d (supported: 8, 4)", cfg->bits);
@@ -90,8 +91,9 @@ rq_status check_cfg(const rq_qconfig* cfg) {
       cfg->w_scale_mode != RQ_W_TENSOR)
     return fail(RQ_EINVAL, "w_scale_mode = %d (RQ_W_ABSMAX, RQ_W_MSE or RQ_W_TENSOR)",
                 cfg->w_scale_mode);
-  if (cfg->act != RQ_ACT_NONE && cfg->act != RQ_ACT_GELU_ERF && cfg->act != RQ_ACT_GELU_TANH)
-    return fail(RQ_EINVAL, "act = %d (RQ_ACT_NONE, RQ_ACT_GELU_ERF or RQ_ACT_GELU_TANH)", cfg->act);
+  if (cfg->act != RQ_ACT_NONE && cfg->act != RQ_ACT_GELU_ERF && cfg->act != RQ_ACT_GELU_TANH && (act || cfg->act != RQ_ACT_SILU))
+    return fail(RQ_EINVAL, "act = %d (RQ_ACT_NONE, RQ_ACT_GELU_ERF or RQ_ACT_GELU_TANH%s)", cfg->act,
+                act ? "" : ", or RQ_ACT_SILU for the gated products");
   return ok();
 }
 
@@ -146,7 +148,7 @@ rq_status check_rotate_args(const void* X, int32_t dt, int64_t rows, int64_t K, 
 rq_status check_linear_core(const void* X, int32_t x_dtype, int64_t M, int64_t K, const void* Wq,
                             const float* w_scale, int64_t N, const float* bias,
                             const rq_qconfig* cfg, const void* Y) {
-  rq_status s = check_cfg(cfg);
+  rq_status s = check_cfg(cfg, true);
   if (s) return s;
   if (x_dtype != RQ_F16 && x_dtype != RQ_BF16)
     return fail(x_dtype == RQ_F32 ? RQ_EUNSUPPORTED : RQ_EINVAL,
@@ -244,7 +246,7 @@ rq_status scratch_of_current_device(void** out) {
 rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const float* w_scale,
                      const float* bias, int64_t M, int64_t N, int64_t K, const rq_qconfig* cfg,
                      const void* out, int64_t out_elem) {
-  rq_status s = check_cfg(cfg);
+  rq_status s = check_cfg(cfg, out_elem != 4);
   if (s) return s;
   if ((s = check_gemm_shape(M, N, K))) return s;
   if (M == 0) return ok();
@@ -264,6 +266,39 @@ rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const
       overlap(out, ob, x_scale, M * 4) || overlap(out, ob, w_scale, N * 4) || overlap(out, ob, bias, N * 4))
     return fail(RQ_EINVAL, "output overlaps an input");
   return ok();
+}
+
+// ---- the gated product
+rq_status check_gated_shape(int64_t M, int64_t N, int64_t K) {
+  rq_status s = check_gemm_shape(M, N, K);
+  if (s) return s;
+  if (2 * N > kMaxRowsOrCols) return fail(RQ_EUNSUPPORTED, "N = %lld: the weights have 2 N >= 2^31 rows", (long long)N);
+  if ((M + 255) / 256 * ((2 * N + 127) / 128) >= (int64_t(1) << 23))   // a launch has fewer than 2^32 threads, 512 a tile at most
+    return fail(RQ_EUNSUPPORTED, "M = %lld, N = %lld: 2^23 tiles or more", (long long)M, (long long)N);
+  return ok();
+}
+
+// Weights, scales, bias and output of a gated product (M > 0).
+rq_status check_gated_operands(int64_t M, int64_t N, int64_t K, const void* Wq, const float* w_scale, const float* bias,
+                               const rq_qconfig* cfg, const void* Y) {
+  rq_status s;
+  if ((s = check_ptr(Wq, "Wq"))) return s;
+  if ((s = check_ptr(w_scale, "w_scale"))) return s;
+  if ((s = check_ptr(bias, "bias", false))) return s;
+  if ((s = check_ptr(Y, "Y"))) return s;
+  const int64_t yb = M * N * 2;
+  if (overlap(Y, yb, Wq, w_code_bytes(2 * N, K, cfg->bits, cfg->w_layout)) || overlap(Y, yb, w_scale, N * 8) || overlap(Y, yb, bias, N * 8))
+    return fail(RQ_EINVAL, "Y overlaps an input");
+  return ok();
+}
+
+rq_status launch_gated(const void* Xq, const float* sx, int32_t x_layout, const void* Wq, const float* sw, const float* bias,
+                       int64_t M, int64_t N, int64_t K, const rq_qconfig* cfg, void* Y, int32_t y_dtype, hipStream_t st) {
+  if (cfg->w_layout == RQ_W_FP6)
+    return from_hip(convrot::launch_gemm_gated_fp6(Xq, sx, Wq, sw, bias, M, N, K, Y, y_dtype, cfg->act, st), "gemm launch");
+  return from_hip(convrot::launch_gemm_gated(Xq, sx, Wq, sw, bias, M, N, K, cfg->bits, x_layout == RQ_X_TILED, Y, y_dtype,
+                                             cfg->act, st),
+                  "gemm launch");
 }
 
 // ---- the norm in front of a linear
@@ -684,7 +719,7 @@ rq_status rq_rotq_linear_noalloc(const void* X, int32_t x_dtype, int64_t M, int6
                                  const void* Wq, const float* w_scale, int64_t N, const float* bias,
                                  const rq_qconfig* cfg, void* Y, void* stream) {
   // The size limit first, so that an oversized call gets this status whatever its pointers.
-  rq_status s = check_cfg(cfg);
+  rq_status s = check_cfg(cfg, true);
   if (s) return s;
   if ((s = check_gemm_shape(M, N, K))) return s;
   const size_t need = rq_rotq_linear_workspace_size(M, K, cfg);
@@ -715,6 +750,52 @@ rq_status rq_gemm_dequant(const void* Xq, const float* x_scale, const void* Wq,
                                        cfg->x_layout == RQ_X_TILED, Y, y_dtype, nullptr, cfg->act,
                                        static_cast<hipStream_t>(stream)),
                   "gemm launch");
+}
+
+rq_status rq_gemm_gated(const void* Xq, const float* x_scale, const void* Wq, const float* w_scale, const float* bias,
+                        int64_t M, int64_t N, int64_t K, const rq_qconfig* cfg, void* Y, int32_t y_dtype, void* stream) {
+  rq_status s = check_cfg(cfg);
+  if (s) return s;
+  if (y_dtype != RQ_F16 && y_dtype != RQ_BF16)
+    return fail(y_dtype == RQ_F32 ? RQ_EUNSUPPORTED : RQ_EINVAL, "Y dtype %d (supported: RQ_F16, RQ_BF16)", y_dtype);
+  if ((cfg->x_layout == RQ_X_FP6) != (cfg->w_layout == RQ_W_FP6))
+    return fail(RQ_EINVAL, "FP6 activation codes go with FP6 weight codes (x_layout %d, w_layout %d)", cfg->x_layout, cfg->w_layout);
+  if ((s = check_gated_shape(M, N, K)) || M == 0) return s;
+  if ((s = check_ptr(Xq, "Xq"))) return s;
+  if (!x_scale || (reinterpret_cast<uintptr_t>(x_scale) & 3u)) return fail(RQ_EINVAL, "x_scale is NULL or misaligned");
+  if ((s = check_gated_operands(M, N, K, Wq, w_scale, bias, cfg, Y))) return s;
+  if (overlap(Y, M * N * 2, Xq, x_code_bytes(M, K, cfg->bits, cfg->x_layout)) || overlap(Y, M * N * 2, x_scale, M * 4))
+    return fail(RQ_EINVAL, "Y overlaps an input");
+  return launch_gated(Xq, x_scale, cfg->x_layout, Wq, w_scale, bias, M, N, K, cfg, Y, y_dtype, static_cast<hipStream_t>(stream));
+}
+
+rq_status rq_rotq_gated_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, const void* Wq, const float* w_scale,
+                               int64_t N, const float* bias, const rq_qconfig* cfg, void* Y, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  rq_status s = check_cfg(cfg);
+  if (s) return s;
+  if (x_dtype != RQ_F16 && x_dtype != RQ_BF16)
+    return fail(x_dtype == RQ_F32 ? RQ_EUNSUPPORTED : RQ_EINVAL,
+                "X dtype %d (supported: RQ_F16, RQ_BF16; Y has X's dtype)", x_dtype);
+  if ((s = check_gated_shape(M, N, K)) || M == 0) return s;
+  if ((s = check_ptr(X, "X"))) return s;
+  if ((s = check_gated_operands(M, N, K, Wq, w_scale, bias, cfg, Y))) return s;
+  if ((s = check_ptr(workspace, "workspace"))) return s;
+  const size_t need = rq_rotq_linear_workspace_size(M, K, cfg);
+  if (ws_bytes < need) return fail(RQ_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if (overlap(Y, M * N * 2, X, M * K * 2)) return fail(RQ_EINVAL, "Y overlaps an input");
+  if (overlap(workspace, (int64_t)need, Y, M * N * 2) || overlap(workspace, (int64_t)need, X, M * K * 2) ||
+      overlap(workspace, (int64_t)need, Wq, w_code_bytes(2 * N, K, cfg->bits, cfg->w_layout)) ||
+      overlap(workspace, (int64_t)need, w_scale, N * 8) || overlap(workspace, (int64_t)need, bias, N * 8))
+    return fail(RQ_EINVAL, "the workspace overlaps Y or an input");
+  // As in rq_rotq_linear: the codes in the tiled layout (FP6 tiles with FP6 weights), then x_scale.
+  const int32_t xl = fused_x_layout(cfg);
+  uint8_t* Xq = static_cast<uint8_t*>(workspace);
+  float* sx = reinterpret_cast<float*>(Xq + round256(x_code_bytes(M, K, cfg->bits, xl)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if ((s = from_hip(convrot::launch_rotate_quant(X, x_dtype, M, K, cfg->bits, code_layout(xl), Xq, sx, st), "rotate_quant launch")))
+    return s;
+  return launch_gated(Xq, sx, xl, Wq, w_scale, bias, M, N, K, cfg, Y, x_dtype, st);
 }
 
 rq_status rq_gemm_s32(const void* Xq, const void* Wq, int64_t M, int64_t N, int64_t K,

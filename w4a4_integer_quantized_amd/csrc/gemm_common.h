@@ -19,7 +19,9 @@ constexpr int kBM = 256;                       // tokens per tile
 constexpr int kBN = 128;                       // output features per tile
 constexpr int kNumCUs = 256;                   // MI355X
 
-enum OutKind { kOutS32 = 0, kOutF16 = 1, kOutBF16 = 2 };
+// kOutGate*: the gated product of two projections, half as many outputs as weight rows.
+enum OutKind { kOutS32 = 0, kOutF16 = 1, kOutBF16 = 2, kOutGateF16 = 3, kOutGateBF16 = 4 };
+constexpr bool out_gated(int out) { return out >= kOutGateF16; }
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -30,12 +32,12 @@ typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ uint32_t pack2(float a, float b, int out) {
   asm volatile("" : "+v"(a), "+v"(b));
   const f32x2 v = {a, b};
-  if (out == kOutF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  if (out == kOutF16 || out == kOutGateF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 // The MLP activation applied to the binary32 pre-activation v before the fp16/bf16 rounding
-// (act 0: none; 1: GELU, erf form; 2: GELU, tanh form), with the native v_exp_f32 (2^x) and
+// (act 0: none; 1: GELU, erf form; 2: GELU, tanh form; 3: SiLU), with the native v_exp_f32 (2^x) and
 // v_rcp_f32 (1/x), each within about 1 ulp, so that the epilogue's extra VALU work stays small:
 //  * erf form: x Phi(x) = 0.5 x erfc(-x / sqrt 2), erfc by the Chebyshev-fitted form of Press et
 //    al., Numerical Recipes, section 6.2 ("erfcc"): for z = |y|, t = 1 / (1 + z/2),
@@ -44,11 +46,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int out) {
 //  * tanh form: 0.5 x (1 + tanh u) = x logistic(2u), u = sqrt(2/pi) (x + 0.044715 x^3), the
 //    logistic taken as 1 / (1 + e) or e / (1 + e) with e = exp(-2|u|) <= 1, which never
 //    overflows.
-// Neither form cancels for negative x, so the relative error is a few binary32 ulps plus the
+//  * SiLU (gated products only): x logistic(x), the logistic as in the tanh form.
+// No form cancels for negative x, so the relative error is a few binary32 ulps plus the
 // rounding of the exponent's argument, amplified as the tail steepens (about z^2 and 2|u|
 // ulps); the rounded output can differ from the correctly rounded one only next to a rounding
 // midpoint. Results below the binary32 normal range may come out as zero.
-enum ActKind { kActNone = 0, kActGeluErf = 1, kActGeluTanh = 2 };
+enum ActKind { kActNone = 0, kActGeluErf = 1, kActGeluTanh = 2, kActSilu = 3 };
 
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
@@ -77,6 +80,11 @@ __device__ __forceinline__ float activate(float v) {
     const float e32 = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.30220819814432500f, fabsf(m), 32.0f));
     const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(0x1p-32f, e32, 1.0f));
     if (m >= 0.0f) return v * r;
+    return ((0x1p-32f * v) * e32) * r;
+  } else if constexpr (ACT == kActSilu) {
+    const float e32 = __builtin_amdgcn_exp2f(__builtin_fmaf(-kLog2e, fabsf(v), 32.0f));   // 2^32 exp(-|v|)
+    const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(0x1p-32f, e32, 1.0f));
+    if (v >= 0.0f) return v * r;
     return ((0x1p-32f * v) * e32) * r;
   } else {
     return v;
@@ -198,6 +206,70 @@ __device__ __forceinline__ void tile_epilogue(AccBlk (&acc)[4][NB], const float*
   }
 }
 
+// The epilogue of a gated product. Weight rows come as 16 gate rows and 16 up rows in turn, so a
+// 32-row block of W holds both values of 16 outputs, and in this lane's elements of it (see above)
+// r = 0..7 are gates and r + 8 the up rows of the same outputs: act(g) * u needs no exchange. The
+// wave's outputs, 64 to a row, are staged in rows of 128 bytes: 16-byte chunk c of row r at
+// c ^ ((r >> 1) & 7), the 8-byte halves swapped on rows with bit 4 set, so the 32 lanes of a write
+// hit distinct banks (two rows share a pass over all 64).
+template <int BITS, int OUT, int NB, int ACT, typename AccBlk>
+__device__ __forceinline__ void gated_epilogue(AccBlk (&acc)[4][NB], const float* scales, uint8_t* stage, int row0, int lane,
+                                               int m0, int n0, int M, int N, void* __restrict__ Y) {
+  const int msub = lane & 31, half = lane >> 5;
+  const float* e_sw = scales;
+  const float* e_b = e_sw + kBN;
+  const float* e_sx = e_b + kBN;
+  float xs[NB];
+#pragma unroll
+  for (int b = 0; b < NB; b++) xs[b] = e_sx[row0 + b * 32 + msub];
+#pragma unroll
+  for (int a = 0; a < 4; a++) {
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+      const int col = a * 32 + 8 * g + 4 * half;   // tile-local gate row; its up row 16 further
+      const float4 sg = *reinterpret_cast<const float4*>(e_sw + col), su = *reinterpret_cast<const float4*>(e_sw + col + 16);
+      const float4 bg = *reinterpret_cast<const float4*>(e_b + col), bu = *reinterpret_cast<const float4*>(e_b + col + 16);
+      const float wg[4] = {sg.x, sg.y, sg.z, sg.w}, wu[4] = {su.x, su.y, su.z, su.w};
+      const float cg[4] = {bg.x, bg.y, bg.z, bg.w}, cu[4] = {bu.x, bu.y, bu.z, bu.w};
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float gate = __builtin_fmaf(acc_float<BITS>(acc[a][b], 4 * g + e), __fmul_rn(wg[e], xs[b]), cg[e]);
+          const float up = __builtin_fmaf(acc_float<BITS>(acc[a][b], 8 + 4 * g + e), __fmul_rn(wu[e], xs[b]), cu[e]);
+          y[e] = __fmul_rn(activate<ACT>(gate), up);
+        }
+        uint2 o;
+        o.x = pack2(y[0], y[1], OUT);
+        o.y = pack2(y[2], y[3], OUT);
+        const int row = b * 32 + msub;
+        const int chunk = (a * 2 + g) ^ ((row >> 1) & 7);
+        const int hpos = half ^ ((row >> 4) & 1);
+        *reinterpret_cast<uint2*>(stage + row * 128 + chunk * 16 + hpos * 8) = o;
+      }
+    }
+  }
+  // Whole rows back (8 lanes x 16 B = one 128-byte row segment, 8 rows per read), then the stores,
+  // ordinary ones: the outputs are the next linear's input.
+  constexpr int kIt = 4 * NB;
+  uint4 v[kIt];
+#pragma unroll
+  for (int it = 0; it < kIt; it++) {
+    const int row = it * 8 + (lane >> 3);
+    v[it] = *reinterpret_cast<const uint4*>(stage + row * 128 + (lane & 7) * 16);
+    if ((it >> 1) & 1) v[it] = make_uint4(v[it].z, v[it].w, v[it].x, v[it].y);   // row bit 4
+  }
+  const int outs = N >> 1;
+#pragma unroll
+  for (int it = 0; it < kIt; it++) {
+    const int row = it * 8 + (lane >> 3);
+    const int m = m0 + row0 + row;
+    const int n = (n0 >> 1) + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+    if (m < M && n < outs) *reinterpret_cast<v4i*>(static_cast<uint16_t*>(Y) + (int64_t)m * outs + n) = __builtin_bit_cast(v4i, v[it]);
+  }
+}
+
 // tile_epilogue with the launch's activation: one uniform branch per tile, so the variant
 // without an activation carries no activation code.
 template <int BITS, int OUT, int NB, typename AccBlk>
@@ -206,6 +278,16 @@ __device__ __forceinline__ void tile_epilogue_act(int act, AccBlk (&acc)[4][NB],
                                                   int M, int N, void* __restrict__ Y) {
   if constexpr (OUT == kOutS32) {
     tile_epilogue<BITS, OUT, NB, kActNone>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);
+  } else if constexpr (out_gated(OUT)) {
+    if (act == kActSilu) {
+      gated_epilogue<BITS, OUT, NB, kActSilu>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);
+    } else if (act == kActGeluErf) {
+      gated_epilogue<BITS, OUT, NB, kActGeluErf>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);
+    } else if (act == kActGeluTanh) {
+      gated_epilogue<BITS, OUT, NB, kActGeluTanh>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);
+    } else {
+      gated_epilogue<BITS, OUT, NB, kActNone>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);
+    }
   } else {
     if (act == kActNone) {
       tile_epilogue<BITS, OUT, NB, kActNone>(acc, scales, stage, row0, lane, m0, n0, M, N, Y);

@@ -312,4 +312,11 @@ hipError_t launch_gemm_fp6(const void* Xt, const float* sx, const void* Wt, cons
   return launch6<kOutBF16>(Xt, sx, Wt, sw, bias, M, N, K, Y, act, stream);
 }
 
+hipError_t launch_gemm_gated_fp6(const void* Xt, const float* sx, const void* Wt, const float* sw, const float* bias, int64_t M,
+                                 int64_t N, int64_t K, void* Y, int out_dt, int act, hipStream_t stream) {
+  if (M == 0 || N == 0) return hipSuccess;
+  return out_dt == kF16 ? launch6<kOutGateF16>(Xt, sx, Wt, sw, bias, M, 2 * N, K, Y, act, stream)
+                        : launch6<kOutGateBF16>(Xt, sx, Wt, sw, bias, M, 2 * N, K, Y, act, stream);
+}
+
 }  // namespace convrot

@@ -785,7 +785,26 @@ hipError_t launch_layout(const void* Xq, const float* sx, const void* Wq, const 
                    : launch<4, kOutBF16, XT>(Xq, sx, Wq, sw, bias, M, N, Kb, Y, act, stream);
 }
 
+template <bool XT>
+hipError_t launch_gated(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
+                        int64_t rows, int64_t Kb, int bits, void* Y, int out_dt, int act, hipStream_t st) {
+  if (out_dt == kF16)
+    return bits == 8 ? launch<8, kOutGateF16, XT>(Xq, sx, Wq, sw, bias, M, rows, Kb, Y, act, st)
+                     : launch<4, kOutGateF16, XT>(Xq, sx, Wq, sw, bias, M, rows, Kb, Y, act, st);
+  return bits == 8 ? launch<8, kOutGateBF16, XT>(Xq, sx, Wq, sw, bias, M, rows, Kb, Y, act, st)
+                   : launch<4, kOutGateBF16, XT>(Xq, sx, Wq, sw, bias, M, rows, Kb, Y, act, st);
+}
+
 }  // namespace
+
+// The gated product on the tile kernels: the same launch rule, with the weights' 2 N rows for N.
+hipError_t launch_gemm_gated(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
+                             int64_t N, int64_t K, int bits, bool x_tiled, void* Y, int out_dt, int act, hipStream_t stream) {
+  if (M == 0 || N == 0) return hipSuccess;
+  const int64_t Kb = bits == 8 ? K : K / 2;
+  return x_tiled ? launch_gated<true>(Xq, sx, Wq, sw, bias, M, 2 * N, Kb, bits, Y, out_dt, act, stream)
+                 : launch_gated<false>(Xq, sx, Wq, sw, bias, M, 2 * N, Kb, bits, Y, out_dt, act, stream);
+}
 
 hipError_t launch_gemm(const void* Xq, const float* sx, const void* Wq, const float* sw,
                        const float* bias, int64_t M, int64_t N, int64_t K, int bits,

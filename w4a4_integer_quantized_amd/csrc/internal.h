@@ -58,6 +58,13 @@ hipError_t launch_gemm_fp6(const void* Xt, const float* sx, const void* Wt, cons
                            const float* bias, int64_t M, int64_t N, int64_t K, void* Y,
                            int out_dt, int32_t* acc32, int act, hipStream_t stream);
 
+// Y[m, n] = act(g) * u, g and u the dequantized values of gate row n and up row n of Wq: 2 N rows, 16 gate
+// rows and 16 up rows in turn (as are sw and bias). act: any gemm::ActKind.
+hipError_t launch_gemm_gated(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
+                             int64_t N, int64_t K, int bits, bool x_tiled, void* Y, int out_dt, int act, hipStream_t stream);
+hipError_t launch_gemm_gated_fp6(const void* Xt, const float* sx, const void* Wt, const float* sw, const float* bias, int64_t M,
+                                 int64_t N, int64_t K, void* Y, int out_dt, int act, hipStream_t stream);
+
 // The same GEMM with each CU's weight tile resident in LDS and eight independent waves
 // (int8 codes in the tiled layout, K = 1024; gemm_rw.hip). launch_gemm takes it where
 // gemm_rw_supported() holds.
