@@ -264,7 +264,7 @@ rq_status rq_gemm_dequant(const void *Xq, const float *x_scale, const void *Wq,
  *   Xq, x_scale     M rows of codes in cfg->x_layout, as rq_rotate_quantize or
  *                   rq_norm_rotate_quantize write them
  *   Y        out: [M, N] of y_dtype (RQ_F16 or RQ_BF16), must not overlap an input
- * N % 16 == 0, 2 N < 2^31, and ceil(M / 256) * ceil(2 N / 128) < 2^23. */
+ * N % 16 == 0, N < 2^27, and ceil(M / 256) * ceil(2 N / 128) < 2^23. */
 rq_status rq_gemm_gated(const void *Xq, const float *x_scale, const void *Wq, const float *w_scale,
                         const float *bias, int64_t M, int64_t N, int64_t K, const rq_qconfig *cfg,
                         void *Y, int32_t y_dtype, void *stream);

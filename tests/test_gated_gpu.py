@@ -59,7 +59,7 @@ LAYOUTS = [(8, rq.RQ_X_ROWS), (8, rq.RQ_X_TILED), (4, rq.RQ_X_ROWS), (4, rq.RQ_X
 
 @pytest.mark.parametrize("bits,layout", LAYOUTS)
 @pytest.mark.parametrize("M,K,N", [(1, 128, 16), (1, 4096, 528), (2, 2176, 80), (5, 384, 48), (16, 1024, 1040), (17, 640, 16),
-                                   (31, 8192, 32), (33, 1152, 272), (64, 2048, 528), (65, 1024, 64), (127, 512, 112),
+                                   (31, 8192, 32), (33, 1152, 272), (64, 2048, 528), (65, 1024, 64), (127, 512, 112), (90, 1152, 528),
                                    (255, 1536, 16), (256, 256, 144), (300, 1024, 1040), (700, 896, 1024)])
 def test_sizes(M, K, N, bits, layout):
     need_gpu()
@@ -74,6 +74,15 @@ def test_more_tiles_than_cus(M, K, N, bits, layout):
     need_gpu()
     print("gated", M, K, N, bits, layout, flush=True)
     _run(M, K, N, bits, layout, "f16" if bits == 8 else "bf16", "silu")
+
+
+@pytest.mark.parametrize("M", [1, 20, 40, 64, 90, 128])
+@pytest.mark.parametrize("N", [4096, 4112, 6144, 11264, 16000])
+def test_few_tokens_over_many_rows(M, N):
+    """Workgroups of one to four blocks, the last of them not full; 128 tokens on either side of the tiles."""
+    need_gpu()
+    _run(M, 640, N, 8, rq.RQ_X_TILED, "bf16", "silu")
+    _run(M, 384, N, 4, rq.RQ_X_ROWS, "f16", "none")
 
 
 @pytest.mark.parametrize("act", gated_ref.ACTS)

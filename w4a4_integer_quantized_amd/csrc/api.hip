@@ -272,8 +272,9 @@ rq_status check_gemm(const void* Xq, const float* x_scale, const void* Wq, const
 rq_status check_gated_shape(int64_t M, int64_t N, int64_t K) {
   rq_status s = check_gemm_shape(M, N, K);
   if (s) return s;
-  if (2 * N > kMaxRowsOrCols) return fail(RQ_EUNSUPPORTED, "N = %lld: the weights have 2 N >= 2^31 rows", (long long)N);
-  if ((M + 255) / 256 * ((2 * N + 127) / 128) >= (int64_t(1) << 23))   // a launch has fewer than 2^32 threads, 512 a tile at most
+  // A launch has fewer than 2^32 threads: 512 for 16 outputs of few tokens, or for a tile at most.
+  if (N >= (int64_t(1) << 27)) return fail(RQ_EUNSUPPORTED, "N = %lld >= 2^27", (long long)N);
+  if ((M + 255) / 256 * ((2 * N + 127) / 128) >= (int64_t(1) << 23))
     return fail(RQ_EUNSUPPORTED, "M = %lld, N = %lld: 2^23 tiles or more", (long long)M, (long long)N);
   return ok();
 }

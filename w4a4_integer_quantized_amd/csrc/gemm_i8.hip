@@ -802,6 +802,8 @@ hipError_t launch_gemm_gated(const void* Xq, const float* sx, const void* Wq, co
                              int64_t N, int64_t K, int bits, bool x_tiled, void* Y, int out_dt, int act, hipStream_t stream) {
   if (M == 0 || N == 0) return hipSuccess;
   const int64_t Kb = bits == 8 ? K : K / 2;
+  if (gated_skinny_supported(M, N))
+    return launch_gated_skinny(Xq, sx, Wq, sw, bias, M, N, Kb, bits, x_tiled, Y, out_dt, act, stream);
   return x_tiled ? launch_gated<true>(Xq, sx, Wq, sw, bias, M, 2 * N, Kb, bits, Y, out_dt, act, stream)
                  : launch_gated<false>(Xq, sx, Wq, sw, bias, M, 2 * N, Kb, bits, Y, out_dt, act, stream);
 }
