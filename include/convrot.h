@@ -409,6 +409,62 @@ rq_status rq_kv_attention(const rq_kv_attention_params *p, const rq_kv_config *c
                           const void *cache, int64_t num_pages, void *workspace, size_t ws_bytes,
                           void *stream);
 
+/* Attention weights added up for each cached token: how much each one was attended to, for
+ * rq_kv_evict. With p[t, h, j] the softmax weight of token j for query row t and head h of the call that
+ * rq_kv_attention made of the same params (0 where t does not attend to j),
+ *   weights[s, g, j] = keep * weights[s, g, j] + sum over t and the heads h of key head g of p[t, h, j]
+ * for the tokens j < kv_len[s]; others' are left as they were.
+ *   p         as for rq_kv_attention: Q, q_start, kv_len, pages, strides of Q, dtype, causal, window,
+ *             softmax_scale, max_q_len, max_kv_len. lse is read: the logarithms of sums that
+ *             rq_kv_attention wrote for these queries. O and its strides are not looked at
+ *   weights   in/out: float [seqs, kv_heads, max_pages * page_size]
+ *   keep      finite and >= 0. 0: weights are not read. With causal the query rows are the newest
+ *             tokens, which had no weight before this call: what lies in their places is not read
+ *             either, so nothing needs to be cleared when a token is appended
+ * Rows whose lse or query is no finite number (a row that attends to nothing has lse = -inf) count for
+ * nothing. Query rows beyond max_q_len do not exist here. What the tables hold is not trusted with
+ * memory, as in rq_kv_attention; a token of a page outside the cache gets keep * weights.
+ * Arithmetic: rotated queries as two fp16 (leading and remainder), products and sums fp32, one
+ * exponential of logit - lse, which is as exact as lse itself (half a step of binary32 at its size).
+ * Calls with equal arguments give equal bits.
+ *   workspace as for rq_kv_attention, of rq_kv_attention_weights_workspace_size() bytes */
+size_t rq_kv_attention_weights_workspace_size(const rq_kv_attention_params *p, const rq_kv_config *cfg);
+rq_status rq_kv_attention_weights(const rq_kv_attention_params *p, const rq_kv_config *cfg,
+                                  const void *cache, int64_t num_pages, float *weights, float keep,
+                                  void *workspace, size_t ws_bytes, void *stream);
+
+/* Eviction: the sequences' caches brought down to a budget of tokens, by the weights above. For each
+ * sequence of more than `budget` cached tokens and each key head, the first `first` tokens stay, the last
+ * `recent`, and of the others those with the largest weights, as many as the budget has room for (of equal
+ * weights the first; a NaN is below all others). A sequence of at most `budget` tokens keeps all. What stays
+ * is written, in its order, into the places 0, 1, .. of the sequence's new pages: bytes of codes and scales as
+ * they are, so a head's token i is what its token kept[i] was. Heads choose for themselves and keep the same
+ * number of tokens. Afterwards the caller takes new_pages and new_kv_len for pages and kv_len; the old
+ * pages are left as they were and can be given back.
+ * (Causality goes by a token's place: queries at or behind the last one still attend to all.) */
+typedef struct {
+  void *cache;                 /* in/out: device, num_pages * rq_kv_page_bytes(cfg) bytes */
+  const int32_t *kv_len;       /* [seqs] device */
+  const int32_t *pages;        /* [seqs, max_pages] device */
+  const int32_t *new_pages;    /* [seqs, new_max_pages] device: pages that no sequence of the call has in
+                                  `pages`, each given once */
+  const float *weights;        /* [seqs, kv_heads, max_pages * page_size] device */
+  float *new_weights;          /* out: [seqs, kv_heads, new_max_pages * page_size], or NULL: the weights of what
+                                  stays, in its places (others are left as they were) */
+  int32_t *new_kv_len;         /* out: [seqs]: min(kv_len, budget) */
+  int32_t *kept;               /* out: [seqs, kv_heads, budget]: the old places of what stays, ascending, then -1 */
+  int64_t num_pages;
+  int32_t seqs, max_pages, new_max_pages;   /* limits as for rq_kv_attention */
+  int32_t budget;              /* 1 .. new_max_pages * page_size */
+  int32_t first, recent;       /* >= 0, together at most the budget */
+} rq_kv_evict_params;
+
+/* What the tables hold is not trusted with memory: kv_len is cut to [0, max_pages * page_size], a token of a
+ * page outside the cache is moved as a row of zeros (codes and scales), and a new page outside the
+ * cache is not written. No two outputs may overlap, nor an output an input. seqs * kv_heads < 2^22 and
+ * seqs * kv_heads * ceil(budget / 64) < 2^24. */
+rq_status rq_kv_evict(const rq_kv_evict_params *p, const rq_kv_config *cfg, void *stream);
+
 /* Static text for a status code. */
 const char *rq_status_string(rq_status s);
 

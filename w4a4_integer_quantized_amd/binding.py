@@ -7,8 +7,8 @@ the library is missing or a call fails, a ConvRotError is raised.
 Two layers:
   * ``rq_*`` -- the C entry points under their own names, taking integer device pointers;
   * ``quantize_weights``, ``rotq_linear``, ``rotate_quantize``, ``norm_rotate_quantize``,
-    ``gemm_dequant``, ``gemm_s32``, ``rotq_gated_linear``, ``gemm_gated``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention`` -- tensor wrappers that allocate outputs with torch and pass the current
-    stream.
+    ``gemm_dequant``, ``gemm_s32``, ``rotq_gated_linear``, ``gemm_gated``, ``kv_cache_write``, ``kv_cache_read``, ``kv_attention``, ``kv_attention_weights``,
+    ``kv_evict`` -- tensor wrappers that allocate outputs with torch and pass the current stream.
 """
 from __future__ import annotations
 
@@ -59,6 +59,13 @@ class rq_kv_attention_params(ctypes.Structure):
                 + [("softmax_scale", ctypes.c_float)])
 
 
+class rq_kv_evict_params(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("cache", "kv_len", "pages", "new_pages", "weights", "new_weights", "new_kv_len",
+                                                "kept")]
+                + [("num_pages", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("seqs", "max_pages", "new_max_pages", "budget", "first", "recent")])
+
+
 _lib = None
 
 
@@ -93,6 +100,8 @@ def load():
         "rq_kv_cache_write": [P, P, I32, I64, I64, I64, I64, I64, P, KV, P, I64, P],
         "rq_kv_cache_read": [P, I64, P, I64, KV, P, P, I32, I64, I64, I64, I64, P],
         "rq_kv_attention": [ATT, KV, P, I64, P, SZ, P],
+        "rq_kv_attention_weights": [ATT, KV, P, I64, P, ctypes.c_float, P, SZ, P],
+        "rq_kv_evict": [ctypes.POINTER(rq_kv_evict_params), KV, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -108,6 +117,8 @@ def load():
     lib.rq_kv_page_bytes.restype = SZ
     lib.rq_kv_attention_workspace_size.argtypes = [ATT, KV]
     lib.rq_kv_attention_workspace_size.restype = SZ
+    lib.rq_kv_attention_weights_workspace_size.argtypes = [ATT, KV]
+    lib.rq_kv_attention_weights_workspace_size.restype = SZ
     lib.rq_status_string.argtypes = [ctypes.c_int]
     lib.rq_status_string.restype = ctypes.c_char_p
     lib.rq_last_error_detail.argtypes = []
@@ -217,6 +228,19 @@ def rq_kv_attention_workspace_size(params, cfg) -> int:
 
 def rq_kv_attention(params, cfg, cache, num_pages, workspace, ws_bytes, stream) -> int:
     return load().rq_kv_attention(ctypes.byref(params), ctypes.byref(cfg), cache, num_pages, workspace, ws_bytes, stream)
+
+
+def rq_kv_attention_weights_workspace_size(params, cfg) -> int:
+    return load().rq_kv_attention_weights_workspace_size(ctypes.byref(params), ctypes.byref(cfg))
+
+
+def rq_kv_attention_weights(params, cfg, cache, num_pages, weights, keep, workspace, ws_bytes, stream) -> int:
+    return load().rq_kv_attention_weights(ctypes.byref(params), ctypes.byref(cfg), cache, num_pages, weights, keep, workspace,
+                                          ws_bytes, stream)
+
+
+def rq_kv_evict(params, cfg, stream) -> int:
+    return load().rq_kv_evict(ctypes.byref(params), ctypes.byref(cfg), stream)
 
 
 def rq_status_string(s: int) -> str:
@@ -376,8 +400,8 @@ def norm_rotate_quantize(X, residual=None, weight=None, eps: float = 1e-6, bits:
     if x_layout == RQ_X_ROWS:
         Xq = X.new_empty(code_shape(M, K, bits), dtype=kv.int8 if bits == 8 else kv.uint8)
     else:
-        Xq = X.new_empty((max(rq_codes_bytes(M, K, cfg), 1),), dtype=kv.uint8)
-    x_scale = X.new_empty((M,), dtype=kv.float32)
+        Xq = X.new_empty(max(rq_codes_bytes(M, K, cfg), 1), dtype=kv.uint8)
+    x_scale = X.new_empty(M, dtype=kv.float32)
     H = out
     if out is None:
         H = X if residual is None else X.new_empty(shape)
@@ -486,12 +510,20 @@ def quantize_gated_weights(gate, up, bits: int = 8, rot: int = 128, stream=None,
         return quantize_weights(interleave_gated(gate, up), bits, rot, None, w_scale_mode, w_layout)
 
 
-def _check_gated(Wq, w_scale, bias, K, cfg):
-    """N of a gated product's operands."""
-    rows = w_scale.shape[0] if w_scale.dim() == 1 else -1
-    if rows < 0 or rows % 32:
-        raise ValueError("w_scale must be a vector of 2 N elements, N a multiple of 16, got %s" % (tuple(w_scale.shape),))
-    _check_weights(Wq, w_scale, bias, rows, K, cfg)
+def _check_gated(kv, Wq, w_scale, bias, K, bits, w_layout):
+    """N of a gated product's operands. (The checks of the plain linears in fewer steps: a decode loop
+    waits for them.)"""
+    shape = w_scale.shape
+    rows = shape[0] if len(shape) == 1 else -1
+    if rows < 0 or rows % 32 or w_scale.dtype != kv.float32 or not w_scale.is_contiguous():
+        raise ValueError("w_scale must be a contiguous float32 vector of 2 N elements, N a multiple of 16, got %s %s"
+                         % (w_scale.dtype, tuple(shape)))
+    if bias is not None and (bias.shape != shape or bias.dtype != kv.float32 or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 vector of %d elements, got %s %s"
+                         % (rows, bias.dtype, tuple(bias.shape)))
+    need = (rows + 127) // 128 * 128 * (K // 64) * 48 if w_layout == RQ_W_FP6 else rows * K * bits // 8
+    if not Wq.is_contiguous() or Wq.numel() * Wq.element_size() != need:
+        raise ValueError("Wq must be contiguous and hold %d bytes, got %s %s" % (need, Wq.dtype, tuple(Wq.shape)))
     return rows // 2
 
 
@@ -502,12 +534,17 @@ def gemm_gated(Xq, x_scale, Wq, w_scale, bias=None, bits: int = 8, K: Optional[i
     len(x_scale), K from Wq unless given (give K for FP6 weight tiles). out_dtype float16 (default)
     or bfloat16, or that of out."""
     kv = _kv()
-    M = x_scale.shape[0] if x_scale.dim() == 1 else -1
-    K = _gemm_k(Wq, bits, K)
-    cfg = make_cfg(bits, x_layout=x_layout, w_layout=w_layout, act=act)
-    _check_vec(x_scale, "x_scale", M)
-    N = _check_gated(Wq, w_scale, bias, K, cfg)
-    _check_bytes(Xq, "Xq", rq_codes_bytes(M, K, cfg), exact=False)
+    if K is None:
+        K = _gemm_k(Wq, bits, K)
+    cfg = make_cfg(bits, 128, RQ_ROT_WHT, x_layout, RQ_W_ABSMAX, w_layout, act)
+    shape = x_scale.shape
+    if len(shape) != 1 or x_scale.dtype != kv.float32 or not x_scale.is_contiguous():
+        raise ValueError("x_scale must be a contiguous float32 vector, got %s %s" % (x_scale.dtype, tuple(shape)))
+    M = shape[0]
+    N = _check_gated(kv, Wq, w_scale, bias, K, bits, w_layout)
+    if not Xq.is_contiguous() or Xq.numel() * Xq.element_size() < rq_codes_bytes(M, K, cfg):
+        raise ValueError("Xq must be contiguous and hold %d bytes, got %s %s"
+                         % (rq_codes_bytes(M, K, cfg), Xq.dtype, tuple(Xq.shape)))
     if out is not None:
         if out_dtype not in (None, out.dtype) or out.shape != (M, N) or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor of shape (%d, %d) and of out_dtype, got %s %s"
@@ -541,8 +578,8 @@ def rotq_gated_linear(X, Wq, w_scale, bias=None, bits: int = 8, rot: int = 128, 
     if len(shape) != 2 or dtype not in kv.halves or not X.is_contiguous():
         raise ValueError("X must be a contiguous 2-D float16 or bfloat16 tensor, got %s %s" % (dtype, tuple(shape)))
     M, K = shape
-    cfg = make_cfg(bits, rot, w_layout=w_layout, act=act)
-    N = _check_gated(Wq, w_scale, bias, K, cfg)
+    cfg = make_cfg(bits, rot, RQ_ROT_WHT, RQ_X_ROWS, RQ_W_ABSMAX, w_layout, act)
+    N = _check_gated(kv, Wq, w_scale, bias, K, bits, w_layout)
     need = rq_rotq_linear_workspace_size(M, K, cfg)
     if workspace is not None:
         _check_bytes(workspace, "workspace", need, exact=False)
@@ -554,12 +591,12 @@ def rotq_gated_linear(X, Wq, w_scale, bias=None, bits: int = 8, rot: int = 128, 
         with _kv_placed(kv, index, stream):
             return rotq_gated_linear(X, Wq, w_scale, bias, bits, rot, workspace, out, None, w_layout, act)
     if workspace is None:
-        workspace = X.new_empty((max(need, 256),), dtype=kv.uint8)
+        workspace = X.new_empty(max(need, 256), dtype=kv.uint8)
     if out is None:
         out = X.new_empty((M, N))
     _check(rq_rotq_gated_linear(X.data_ptr(), kv.halves[dtype], M, K, Wq.data_ptr(), w_scale.data_ptr(), N,
-                                None if bias is None else bias.data_ptr(), cfg, out.data_ptr(), workspace.data_ptr(),
-                                _nbytes(workspace), kv.raw_stream(index)), "rq_rotq_gated_linear")
+                                None if bias is None else bias.data_ptr(), cfg, out.data_ptr(), workspace.data_ptr(), need,
+                                kv.raw_stream(index)), "rq_rotq_gated_linear")
     return out
 
 
@@ -808,3 +845,102 @@ def kv_attention_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages
     p = rq_kv_attention_params(None, None, None, 4 if ragged else None, None, None, total_q, 0, 0, 0, 0, max_q_len,
                                max_kv_len, RQ_BF16, q_heads, seqs, max_pages, 1, _kv_window(window), 1.0)
     return rq_kv_attention_workspace_size(p, cfg)
+
+
+def kv_attention_weights(Q, lse, cache, pages, kv_len, cfg: rq_kv_config, weights, keep: float = 1.0, q_start=None,
+                         causal: bool = True, window: int = 0, softmax_scale: Optional[float] = None, max_q_len: int = 0,
+                         max_kv_len: int = 0, workspace=None, stream=None):
+    """How much each cached token is attended to, added up in place: weights [seqs, kv_heads, max_pages *
+    page_size] (f32) become keep * weights + the sums of the softmax weights over a sequence's query
+    rows and the heads of each key head. lse [total_q, q_heads] (f32) is what kv_attention returned with
+    return_lse for the same Q, tables and options (see there for the others). With causal the query rows are
+    the newest tokens, whose weight before is taken as 0; with keep = 0 nothing is read. Tokens
+    from kv_len on are left as they were. See rq_kv_attention_weights in convrot.h."""
+    kv = _kv()
+    num_pages = _kv_cache(kv, cache, cfg)
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != cfg.head_dim:
+        raise ValueError("Q must be [total_q, q_heads, %d], got %s" % (cfg.head_dim, tuple(shape)))
+    total, q_heads, dim = shape
+    qt, qh = _kv_rows(Q, "Q", shape, kv.halves)
+    dtype = Q.dtype
+    tables = pages.shape
+    if len(tables) != 2:
+        raise ValueError("pages must be [seqs, max_pages], got %s" % (tuple(tables),))
+    seqs, max_pages = tables
+    _kv_table(pages, "pages", kv.int32, tables)
+    _kv_table(kv_len, "kv_len", kv.int32, (seqs,))
+    _kv_table(lse, "lse", kv.float32, (total, q_heads))
+    _kv_table(weights, "weights", kv.float32, (seqs, cfg.kv_heads, max_pages * cfg.page_size))
+    if q_start is not None:
+        _kv_table(q_start, "q_start", kv.int32, (seqs + 1,))
+    index = _kv_device(Q, lse, cache, pages, kv_len, weights, q_start, workspace)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return kv_attention_weights(Q, lse, cache, pages, kv_len, cfg, weights, keep, q_start, causal, window, softmax_scale,
+                                        max_q_len, max_kv_len, workspace)
+    p = rq_kv_attention_params(
+        Q.data_ptr(), None, lse.data_ptr(), None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
+        pages.data_ptr(), total, qt, qh, 0, 0, max_q_len, max_kv_len, kv.halves[dtype], q_heads, seqs, max_pages, bool(causal),
+        _kv_window(window), dim ** -0.5 if softmax_scale is None else softmax_scale)
+    at, handle = cache.data_ptr(), kv.raw_stream(index)
+    if workspace is None:
+        # Few query rows need none: asked for only when the call says so (nothing is launched then).
+        status = rq_kv_attention_weights(p, cfg, at, num_pages, weights.data_ptr(), keep, None, 0, handle)
+        if status == RQ_EWORKSPACE:
+            need = rq_kv_attention_weights_workspace_size(p, cfg)
+            workspace = cache.new_empty((need,))
+            status = rq_kv_attention_weights(p, cfg, at, num_pages, weights.data_ptr(), keep, workspace.data_ptr(), need, handle)
+    else:
+        _check_bytes(workspace, "workspace", rq_kv_attention_weights_workspace_size(p, cfg), exact=False)
+        status = rq_kv_attention_weights(p, cfg, at, num_pages, weights.data_ptr(), keep, workspace.data_ptr(), _nbytes(workspace),
+                                         handle)
+    _check(status, "rq_kv_attention_weights")
+
+
+def kv_attention_weights_workspace_size(total_q: int, q_heads: int, seqs: int, max_pages: int, cfg: rq_kv_config,
+                                        max_q_len: int = 0, max_kv_len: int = 0, ragged: bool = False) -> int:
+    """Bytes of workspace a kv_attention_weights call of these sizes needs (0: none). ragged: the call
+    passes q_start."""
+    p = rq_kv_attention_params(None, None, None, 4 if ragged else None, None, None, total_q, 0, 0, 0, 0, max_q_len,
+                               max_kv_len, RQ_BF16, q_heads, seqs, max_pages, 1, 0, 1.0)
+    return rq_kv_attention_weights_workspace_size(p, cfg)
+
+
+def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_pages, new_weights=None, first: int = 0,
+             recent: int = 0, kept=None, new_kv_len=None, stream=None):
+    """The sequences' caches brought down to `budget` tokens, written into new_pages [seqs, new_max_pages]
+    (int32; pages that `pages` does not have, each once): for each key head the first `first` tokens, the last
+    `recent`, and of the others those with the largest weights [seqs, kv_heads, max_pages * page_size] (f32), in
+    their order. Returns (kept, new_kv_len): kept [seqs, kv_heads, budget] (int32) are the old places,
+    then -1, and new_kv_len [seqs] goes with new_pages from here on. new_weights [seqs, kv_heads,
+    new_max_pages * page_size]: where the weights of what stays go. See rq_kv_evict in convrot.h."""
+    kv = _kv()
+    num_pages = _kv_cache(kv, cache, cfg)
+    if len(pages.shape) != 2 or len(new_pages.shape) != 2:
+        raise ValueError("pages and new_pages must be [seqs, pages], got %s and %s" % (tuple(pages.shape), tuple(new_pages.shape)))
+    seqs, max_pages = pages.shape
+    new_max = new_pages.shape[1]
+    _kv_table(pages, "pages", kv.int32, (seqs, max_pages))
+    _kv_table(new_pages, "new_pages", kv.int32, (seqs, new_max))
+    _kv_table(kv_len, "kv_len", kv.int32, (seqs,))
+    _kv_table(weights, "weights", kv.float32, (seqs, cfg.kv_heads, max_pages * cfg.page_size))
+    if new_weights is not None:
+        _kv_table(new_weights, "new_weights", kv.float32, (seqs, cfg.kv_heads, new_max * cfg.page_size))
+    if kept is not None:
+        _kv_table(kept, "kept", kv.int32, (seqs, cfg.kv_heads, budget))
+    if new_kv_len is not None:
+        _kv_table(new_kv_len, "new_kv_len", kv.int32, (seqs,))
+    index = _kv_device(cache, pages, kv_len, weights, new_pages, new_weights, kept, new_kv_len)
+    if stream is not None or index != kv.current_device():
+        with _kv_placed(kv, index, stream):
+            return kv_evict(cache, pages, kv_len, weights, cfg, budget, new_pages, new_weights, first, recent, kept, new_kv_len)
+    if kept is None:
+        kept = pages.new_empty((seqs, cfg.kv_heads, max(budget, 0)))
+    if new_kv_len is None:
+        new_kv_len = kv.empty_like(kv_len)
+    p = rq_kv_evict_params(cache.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), new_pages.data_ptr(), weights.data_ptr(),
+                           None if new_weights is None else new_weights.data_ptr(), new_kv_len.data_ptr(), kept.data_ptr(),
+                           num_pages, seqs, max_pages, new_max, budget, first, recent)
+    _check(rq_kv_evict(p, cfg, kv.raw_stream(index)), "rq_kv_evict")
+    return kept, new_kv_len

@@ -29,7 +29,8 @@ FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-ffp-contract=
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-function", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["rotate_quant.hip", "norm_quant.hip", "gemm_i8.hip", "gemm_rw.hip", "gemm_i8_wide.hip", "gemm_fp6.hip", "gemm_skinny.hip", "weight_quant.hip",
-           "kv_cache.hip", "kv_attention.hip", "api.hip"]
+           "kv_cache.hip", "kv_attention.hip", "kv_weigh.hip",
+           "kv_evict.hip", "api.hip"]
 
 
 def _compile(src: str) -> str:

@@ -613,6 +613,141 @@ rq_status check_kv_attention(const rq_kv_attention_params* p, const rq_kv_config
   return ok();
 }
 
+// What the kernels that take queries to the cache are told of a call, but for the outputs and the plan.
+convrot::KvAttentionArgs kv_query_args(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache,
+                                       int64_t num_pages, int64_t max_q) {
+  convrot::KvAttentionArgs a = {};
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.q = static_cast<const uint8_t*>(p->Q);
+  a.lse = p->lse;
+  a.q_start = p->q_start;
+  a.kv_len = p->kv_len;
+  a.pages = p->pages;
+  a.q_token = p->q_token_stride;
+  a.q_head = p->q_head_stride;
+  a.total_q = p->total_q;
+  a.num_pages = num_pages;
+  a.head_bytes = kv_head_bytes(cfg);
+  a.seqs = p->seqs;
+  a.q_heads = p->q_heads;
+  a.heads = cfg->kv_heads;
+  a.group = p->q_heads / cfg->kv_heads;
+  a.even_q = p->q_start ? 0 : static_cast<int>(p->total_q / p->seqs);
+  a.group_shift = log2_of(a.group);
+  a.group_mul = static_cast<uint32_t>((((uint64_t)1 << 32) * (((uint64_t)1 << a.group_shift) - a.group)) / a.group + 1);
+  a.max_pages = p->max_pages;
+  a.lps = log2_of(cfg->page_size);
+  a.dt = p->dtype;
+  a.causal = p->causal;
+  // Positions are below 2^30: a wider window is no other, and the kernels' differences stay in 32 bits.
+  a.window = p->window < kMaxKvTokens ? p->window : static_cast<int>(kMaxKvTokens);
+  a.max_q = static_cast<int>(max_q);
+  a.scale = p->softmax_scale;
+  return a;
+}
+
+// ---- attention weights of cached tokens
+rq_status check_kv_weigh(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache, int64_t num_pages,
+                         const float* weights, float keep, const void* ws, size_t ws_bytes, convrot::KvWeighPlan* plan,
+                         int64_t* max_q_len) {
+  int64_t max_q = 0, max_kv = 0;
+  rq_status s = check_kv_shape(p, cfg, &max_q, &max_kv);
+  if (s) return s;
+  if ((s = check_kv_cache(cache, num_pages, cfg))) return s;
+  if (!(keep >= 0.0f) || keep > 3.4028234e38f) return fail(RQ_EINVAL, "keep = %g (need a finite value >= 0)", (double)keep);
+  if (p->seqs == 0 || p->max_pages == 0) return ok();
+  int64_t qb = 0;
+  if (p->total_q > 0) {
+    if ((s = check_kv_rows(p->Q, "Q", p->total_q, p->q_heads, cfg->head_dim, 2, p->q_token_stride, p->q_head_stride, false, &qb)))
+      return s;
+    if (!p->lse) return fail(RQ_EINVAL, "lse is NULL");
+  }
+  if (!p->kv_len || !p->pages || !weights) return fail(RQ_EINVAL, "kv_len, pages or weights is NULL");
+  const void* words[5] = {p->kv_len, p->pages, p->q_start, p->lse, weights};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
+      return fail(RQ_EINVAL, "kv_len, pages, q_start, lse or weights is not 4-byte aligned");
+  const int64_t span = (int64_t)p->max_pages * cfg->page_size;
+  if (span > kMaxKvBytes / 4 / ((int64_t)p->seqs * cfg->kv_heads))
+    return fail(RQ_EUNSUPPORTED, "weights of %d sequences, %d heads and %lld tokens have over 2^46 bytes", p->seqs, cfg->kv_heads,
+                (long long)span);
+  *max_q_len = max_q;
+  *plan = convrot::plan_kv_weigh(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q, max_kv, span);
+  // A grid has fewer than 2^32 threads, 256 a workgroup.
+  constexpr int64_t kMost = int64_t(1) << 24;
+  if ((int64_t)p->seqs * plan->splits + 8 >= kMost / (cfg->kv_heads * plan->row_splits) ||
+      (plan->prep && plan->query_tiles_seq * p->seqs >= kMost / cfg->kv_heads))
+    return fail(RQ_EUNSUPPORTED, "%d sequences of up to %lld query rows over up to %lld tokens: too many workgroups (give "
+                                 "max_q_len and max_kv_len)",
+                p->seqs, (long long)max_q, (long long)max_kv);
+  const int64_t need = plan->query_bytes + plan->part_bytes;
+  if (need > 0) {
+    if (ws_bytes < (size_t)need) return fail(RQ_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, (size_t)need);
+    if ((s = check_ptr(ws, "workspace"))) return s;
+  }
+  const struct { const void* at; int64_t bytes; } outs[2] = {{weights, span * p->seqs * cfg->kv_heads * 4}, {ws, need}},
+                                                 ins[6] = {{p->Q, qb},
+                                                           {cache, num_pages * kv_head_bytes(cfg) * cfg->kv_heads},
+                                                           {p->kv_len, (int64_t)p->seqs * 4},
+                                                           {p->q_start, (int64_t)(p->seqs + 1) * 4},
+                                                           {p->pages, (int64_t)p->seqs * p->max_pages * 4},
+                                                           {p->lse, p->total_q * p->q_heads * 4}};
+  for (const auto& o : outs)
+    for (const auto& in : ins)
+      if (overlap(o.at, o.bytes, in.at, in.bytes)) return fail(RQ_EINVAL, "weights or the workspace overlaps an input");
+  if (overlap(outs[0].at, outs[0].bytes, outs[1].at, outs[1].bytes)) return fail(RQ_EINVAL, "weights overlap the workspace");
+  return ok();
+}
+
+// ---- eviction
+rq_status check_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg) {
+  rq_status s = check_kv_cfg(cfg);
+  if (s) return s;
+  if (!p) return fail(RQ_EINVAL, "params is NULL");
+  if (p->seqs < 0 || p->max_pages < 0 || p->new_max_pages < 0 || p->first < 0 || p->recent < 0)
+    return fail(RQ_EINVAL, "seqs = %d, max_pages = %d, new_max_pages = %d, first = %d, recent = %d: none may be negative", p->seqs,
+                p->max_pages, p->new_max_pages, p->first, p->recent);
+  if (p->seqs > 65535) return fail(RQ_EUNSUPPORTED, "seqs = %d > 65535", p->seqs);
+  const int64_t span = (int64_t)p->max_pages * cfg->page_size, new_span = (int64_t)p->new_max_pages * cfg->page_size;
+  if (span > kMaxKvTokens || new_span > kMaxKvTokens)
+    return fail(RQ_EUNSUPPORTED, "max_pages = %d or new_max_pages = %d of %d tokens: over 2^30", p->max_pages, p->new_max_pages, cfg->page_size);
+  if (p->budget < 1 || p->budget > new_span)
+    return fail(RQ_EINVAL, "budget = %d (need 1 .. new_max_pages * page_size = %lld)", p->budget, (long long)new_span);
+  if ((int64_t)p->first + p->recent > p->budget)
+    return fail(RQ_EINVAL, "first = %d and recent = %d are more than budget = %d", p->first, p->recent, p->budget);
+  if ((s = check_kv_cache(p->cache, p->num_pages, cfg))) return s;
+  if (p->seqs == 0) return ok();
+  const int64_t groups = (int64_t)p->seqs * cfg->kv_heads;
+  // Launches of fewer than 2^32 threads: 1024 a (sequence, head), 256 for 64 tokens.
+  if (groups >= (int64_t(1) << 22) || convrot::kv_evict_chunks(p->budget) >= (int64_t(1) << 24) / groups)
+    return fail(RQ_EUNSUPPORTED, "seqs = %d, kv_heads = %d, budget = %d: too many workgroups", p->seqs, cfg->kv_heads, p->budget);
+  if (span > kMaxKvBytes / 4 / groups || new_span > kMaxKvBytes / 4 / groups)
+    return fail(RQ_EUNSUPPORTED, "weights of %lld heads and %lld tokens have over 2^46 bytes", (long long)groups,
+                (long long)(span > new_span ? span : new_span));
+  if (!p->kv_len || !p->new_pages || !p->new_kv_len || !p->kept || (p->max_pages > 0 && (!p->pages || !p->weights)))
+    return fail(RQ_EINVAL, "kv_len, pages, new_pages, weights, new_kv_len or kept is NULL");
+  const void* words[6] = {p->kv_len, p->pages, p->new_pages, p->new_weights, p->new_kv_len, p->kept};
+  for (const void* w : words)
+    if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
+      return fail(RQ_EINVAL, "kv_len, pages, new_pages, new_weights, new_kv_len or kept is not 4-byte aligned");
+  if ((s = check_ptr(p->weights, "weights", false))) return s;
+  const struct { const void* at; int64_t bytes; } outs[4] = {{p->cache, p->num_pages * kv_head_bytes(cfg) * cfg->kv_heads},
+                                                             {p->new_weights, groups * new_span * 4},
+                                                             {p->new_kv_len, (int64_t)p->seqs * 4},
+                                                             {p->kept, groups * p->budget * 4}},
+                                                 ins[4] = {{p->kv_len, (int64_t)p->seqs * 4},
+                                                           {p->pages, (int64_t)p->seqs * p->max_pages * 4},
+                                                           {p->new_pages, (int64_t)p->seqs * p->new_max_pages * 4},
+                                                           {p->weights, groups * span * 4}};
+  for (int i = 0; i < 4; i++) {
+    for (const auto& in : ins)
+      if (overlap(outs[i].at, outs[i].bytes, in.at, in.bytes)) return fail(RQ_EINVAL, "the cache or an output overlaps an input");
+    for (int j = 0; j < i; j++)
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return fail(RQ_EINVAL, "the cache and the outputs must not overlap");
+  }
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -859,44 +994,74 @@ rq_status rq_kv_attention(const rq_kv_attention_params* p, const rq_kv_config* c
   int64_t max_q = 0;
   rq_status s = check_kv_attention(p, cfg, cache, num_pages, workspace, ws_bytes, &plan, &max_q);
   if (s || p->total_q == 0) return s;
-  convrot::KvAttentionArgs a = {};
-  a.cache = static_cast<const uint8_t*>(cache);
-  a.q = static_cast<const uint8_t*>(p->Q);
+  convrot::KvAttentionArgs a = kv_query_args(p, cfg, cache, num_pages, max_q);
   a.out = static_cast<uint8_t*>(p->O);
-  a.lse = p->lse;
-  a.q_start = p->q_start;
-  a.kv_len = p->kv_len;
-  a.pages = p->pages;
   a.part_out = static_cast<float*>(workspace);
   if (plan.splits > 1) a.part_stat = a.part_out + p->total_q * p->q_heads * plan.splits * cfg->head_dim;
-  a.q_token = p->q_token_stride;
-  a.q_head = p->q_head_stride;
   a.out_token = p->o_token_stride;
   a.out_head = p->o_head_stride;
-  a.total_q = p->total_q;
-  a.num_pages = num_pages;
-  a.head_bytes = kv_head_bytes(cfg);
-  a.seqs = p->seqs;
-  a.q_heads = p->q_heads;
-  a.heads = cfg->kv_heads;
-  a.group = p->q_heads / cfg->kv_heads;
-  a.even_q = p->q_start ? 0 : static_cast<int>(p->total_q / p->seqs);
-  a.group_shift = log2_of(a.group);
-  a.group_mul = static_cast<uint32_t>((((uint64_t)1 << 32) * (((uint64_t)1 << a.group_shift) - a.group)) / a.group + 1);
-  a.max_pages = p->max_pages;
-  a.lps = log2_of(cfg->page_size);
-  a.dt = p->dtype;
-  a.causal = p->causal;
-  // Positions are below 2^30: a wider window is no other, and the kernels' differences stay in 32 bits.
-  a.window = p->window < kMaxKvTokens ? p->window : static_cast<int>(kMaxKvTokens);
   a.splits = plan.splits;
   a.row_tiles = plan.row_tiles;
   a.chunk = plan.chunk;
   a.block = plan.block;
-  a.max_q = static_cast<int>(max_q);
-  a.scale = p->softmax_scale;
   return from_hip(convrot::launch_kv_attention(a, cfg->head_dim, cfg->bits, static_cast<hipStream_t>(stream)),
                   "kv_attention launch");
+}
+
+size_t rq_kv_attention_weights_workspace_size(const rq_kv_attention_params* p, const rq_kv_config* cfg) {
+  int64_t max_q = 0, max_kv = 0;
+  if (check_kv_shape(p, cfg, &max_q, &max_kv) != RQ_OK || p->seqs == 0 || p->max_pages == 0) return 0;
+  const convrot::KvWeighPlan plan = convrot::plan_kv_weigh(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q,
+                                                           max_kv, (int64_t)p->max_pages * cfg->page_size);
+  return (size_t)(plan.query_bytes + plan.part_bytes);
+}
+
+rq_status rq_kv_attention_weights(const rq_kv_attention_params* p, const rq_kv_config* cfg, const void* cache,
+                                  int64_t num_pages, float* weights, float keep, void* workspace, size_t ws_bytes, void* stream) {
+  convrot::KvWeighPlan plan = {};
+  int64_t max_q = 0;
+  rq_status s = check_kv_weigh(p, cfg, cache, num_pages, weights, keep, workspace, ws_bytes, &plan, &max_q);
+  if (s || p->seqs == 0 || p->max_pages == 0) return s;
+  convrot::KvWeighArgs w = {};
+  w.a = kv_query_args(p, cfg, cache, num_pages, max_q);
+  w.a.splits = static_cast<int>(plan.splits);
+  w.a.row_tiles = static_cast<int>(plan.row_splits);
+  w.weights = weights;
+  w.keep = keep;
+  w.queries = static_cast<uint8_t*>(workspace);
+  if (plan.part_bytes > 0) w.parts = reinterpret_cast<float*>(w.queries + plan.query_bytes);
+  w.part_stride = (int64_t)p->seqs * cfg->kv_heads * p->max_pages * cfg->page_size;
+  w.query_tiles_seq = plan.query_tiles_seq;
+  const int64_t blocks = ((int64_t)p->max_pages * cfg->page_size + 255) / 256;
+  w.join_blocks = static_cast<int>(blocks < 1024 ? blocks : 1024);
+  return from_hip(convrot::launch_kv_weigh(w, cfg->head_dim, cfg->bits, plan.kt, plan.prep, static_cast<hipStream_t>(stream)),
+                  "kv_weigh launch");
+}
+
+rq_status rq_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg, void* stream) {
+  rq_status s = check_kv_evict(p, cfg);
+  if (s || p->seqs == 0) return s;
+  convrot::KvEvictArgs a = {};
+  a.cache = static_cast<uint8_t*>(p->cache);
+  a.kv_len = p->kv_len;
+  a.pages = p->pages;
+  a.new_pages = p->new_pages;
+  a.weights = p->weights;
+  a.new_weights = p->new_weights;
+  a.new_kv_len = p->new_kv_len;
+  a.kept = p->kept;
+  a.num_pages = p->num_pages;
+  a.head_bytes = kv_head_bytes(cfg);
+  a.seqs = p->seqs;
+  a.heads = cfg->kv_heads;
+  a.max_pages = p->max_pages;
+  a.new_max_pages = p->new_max_pages;
+  a.lps = log2_of(cfg->page_size);
+  a.budget = p->budget;
+  a.first = p->first;
+  a.recent = p->recent;
+  a.chunks = static_cast<int>(convrot::kv_evict_chunks(p->budget));
+  return from_hip(convrot::launch_kv_evict(a, cfg->head_dim * cfg->bits / 8, static_cast<hipStream_t>(stream)), "kv_evict launch");
 }
 
 }  // extern "C"

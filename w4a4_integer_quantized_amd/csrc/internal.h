@@ -128,4 +128,39 @@ KvAttentionPlan plan_kv_attention(int64_t total_q, int seqs, int q_heads, int he
                                   int64_t max_q_len, int64_t max_kv_len, int window);
 hipError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, int bits, hipStream_t stream);
 
+// Attention weights added up for each cached token (kv_weigh.hip). `a` as for attention, without `out` and
+// parts, lse read; a.splits: ranges of tokens, a.row_tiles: shares of the query rows.
+struct KvWeighArgs {
+  KvAttentionArgs a;
+  float* weights;             // [seqs, heads, max_pages << lps]
+  float* parts;               // [row_tiles] times that, where row_tiles > 1
+  uint8_t* queries;           // rotated queries (prep)
+  int64_t part_stride;        // elements of one share
+  int64_t query_tiles_seq;    // tiles of 16 rows of the longest sequence
+  int join_blocks;
+  float keep;
+};
+struct KvWeighPlan {
+  int64_t splits, row_splits, query_tiles_seq, query_bytes, part_bytes;
+  int kt;                     // 16-token steps of a wave
+  bool prep;                  // queries are rotated by a kernel of their own
+};
+KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len,
+                          int64_t span);
+hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool prep, hipStream_t stream);
+
+// A cache brought down to a budget (kv_evict.hip). Pre-validated: first + recent <= budget <= new_max_pages << lps.
+struct KvEvictArgs {
+  uint8_t* cache;
+  const int32_t *kv_len, *pages, *new_pages;   // [seqs], [seqs, max_pages], [seqs, new_max_pages]
+  const float* weights;                        // [seqs, heads, max_pages << lps]
+  float* new_weights;                          // [seqs, heads, new_max_pages << lps], or null
+  int32_t *new_kv_len, *kept;                  // [seqs], [seqs, heads, budget]
+  int64_t num_pages, head_bytes;
+  int seqs, heads, max_pages, new_max_pages, lps, budget, first, recent;
+  int chunks;                                  // kv_evict_chunks(budget)
+};
+int64_t kv_evict_chunks(int budget);           // workgroups that move a (sequence, head)
+hipError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, hipStream_t stream);
+
 }  // namespace convrot
