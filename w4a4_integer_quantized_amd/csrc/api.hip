@@ -676,7 +676,7 @@ rq_status check_kv_weigh(const rq_kv_attention_params* p, const rq_kv_config* cf
   // A grid has fewer than 2^32 threads, 256 a workgroup.
   constexpr int64_t kMost = int64_t(1) << 24;
   if ((int64_t)p->seqs * plan->splits + 8 >= kMost / (cfg->kv_heads * plan->row_splits) ||
-      (plan->prep && plan->query_tiles_seq * p->seqs >= kMost / cfg->kv_heads))
+      (plan->many && plan->query_tiles_seq * p->seqs >= kMost / cfg->kv_heads))
     return fail(RQ_EUNSUPPORTED, "%d sequences of up to %lld query rows over up to %lld tokens: too many workgroups (give "
                                  "max_q_len and max_kv_len)",
                 p->seqs, (long long)max_q, (long long)max_kv);
@@ -1034,7 +1034,7 @@ rq_status rq_kv_attention_weights(const rq_kv_attention_params* p, const rq_kv_c
   w.query_tiles_seq = plan.query_tiles_seq;
   const int64_t blocks = ((int64_t)p->max_pages * cfg->page_size + 255) / 256;
   w.join_blocks = static_cast<int>(blocks < 1024 ? blocks : 1024);
-  return from_hip(convrot::launch_kv_weigh(w, cfg->head_dim, cfg->bits, plan.kt, plan.prep, static_cast<hipStream_t>(stream)),
+  return from_hip(convrot::launch_kv_weigh(w, cfg->head_dim, cfg->bits, plan.kt, plan.many, static_cast<hipStream_t>(stream)),
                   "kv_weigh launch");
 }
 

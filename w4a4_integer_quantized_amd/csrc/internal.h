@@ -134,7 +134,7 @@ struct KvWeighArgs {
   KvAttentionArgs a;
   float* weights;             // [seqs, heads, max_pages << lps]
   float* parts;               // [row_tiles] times that, where row_tiles > 1
-  uint8_t* queries;           // rotated queries (prep)
+  uint8_t* queries;           // rotated queries (many)
   int64_t part_stride;        // elements of one share
   int64_t query_tiles_seq;    // tiles of 16 rows of the longest sequence
   int join_blocks;
@@ -143,11 +143,11 @@ struct KvWeighArgs {
 struct KvWeighPlan {
   int64_t splits, row_splits, query_tiles_seq, query_bytes, part_bytes;
   int kt;                     // 16-token steps of a wave
-  bool prep;                  // queries are rotated by a kernel of their own
+  bool many;                  // queries are rotated by a kernel of their own
 };
 KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len,
                           int64_t span);
-hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool prep, hipStream_t stream);
+hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool many, hipStream_t stream);
 
 // A cache brought down to a budget (kv_evict.hip). Pre-validated: first + recent <= budget <= new_max_pages << lps.
 struct KvEvictArgs {

@@ -12,10 +12,18 @@
 // taken as two fp16 (leading and remainder), scaled by a power of two a row. Codes are exact.
 //
 // A wave keeps KT times 16 tokens as fp16 operands, converted once, and walks over the query rows in tiles
-// of 16, which the workgroup's four waves (four ranges of tokens) share through LDS. Few rows (a
-// decode step): bound by the K codes' bytes; the workgroup rotates the queries itself. Many: bound by the
-// matrix instructions (two a product) and one exponential for each pair beside them; queries are rotated once, by
-// weigh_query_kernel, into operand order, and tiles are copied to LDS one ahead.
+// of 16, which the workgroup's four waves (four ranges of tokens) share through LDS.
+//   Few rows (a decode step): bound by the K codes' bytes and the latency of reaching them through the page table.
+//   The workgroup rotates the queries itself, once for all its ranges, and loads the next range's codes before it
+//   works on one. 64 sequences of 8192 tokens, 8 heads of 128, 4-bit codes: 67 us, 2.6 TB/s. KT = 2 and 4096
+//   workgroups; 72 us with KT = 4 (184 registers, half the waves), 79 us with one range a workgroup.
+//   Many: bound by the matrix instructions (two a product), and one exponential for each pair beside them. Queries are
+//   rotated once, by weigh_query_kernel, into operand order. Chunks of 2048 rows over 9000 tokens, 32 heads over 8 of
+//   128, four sequences: 465 us a call, 26 us of it the queries; the products, 504 GFLOP of fp16, take 403 us at the
+//   rate of a large library product. Rows are shared out until there are 6000 workgroups: with 1152 of them, of which 768 run at
+//   once, the second turn leaves half the card without work, 636 us. Weights of one tile computed between the next
+//   one's products, a barrier for two tiles, a higher priority while products run: no gain. 128 registers instead of
+//   150, for a fourth workgroup on a CU, with operands read one step ahead: 512 us.
 #include "kv_common.h"
 #include "kv_query.h"
 
@@ -29,7 +37,10 @@ constexpr int kRows = 16;      // query rows of a tile: (token, head of the grou
 constexpr int kWaves = 4;
 
 // A tile of queries in memory or LDS: operand words [op][leading, rest][lane][16 B], then for each of the 16
-// rows its log2-sum of exponentials (+inf: the row counts for nothing) and 1 / (its power of two).
+// rows its log2-sum of exponentials (+inf: the row counts for nothing) and kCommon / (its power of two). Rows whose
+// largest rotated element lies in [1/8, 1024) are scaled by kCommon, which leaves [2, 2^14) and a remainder's step
+// of 2^-25 beside it; others each by a power of their own. A tile of the former only needs no factor a row.
+constexpr float kCommon = 16.0f;
 template <int D>
 struct QueryTile {
   static constexpr int kWords = D / 32 * 2 * 1024;        // bytes of the operands
@@ -61,7 +72,7 @@ __device__ __forceinline__ void make_query_tile(const KvAttentionArgs& a, const 
   }
   top = row_max<R::kLanes>(top);
   const bool ok = there && fabsf(lse) < __builtin_inff() && top < __builtin_inff();
-  const float up = ok ? query_scale(top) : 1.0f;
+  const float up = !ok || (top >= 0.125f && top < 1024.0f) ? kCommon : query_scale(top);
   if (row >= kRows) return;
 #pragma unroll
   for (int k = 0; k < R::kChunks; k++) {
@@ -82,7 +93,7 @@ __device__ __forceinline__ void make_query_tile(const KvAttentionArgs& a, const 
   if (u == 0) {
     float* info = reinterpret_cast<float*>(dst + QueryTile<D>::kWords);
     info[row] = ok ? lse * kLog2e : __builtin_inff();
-    info[16 + row] = ok ? 1.0f / up : 0.0f;
+    info[16 + row] = kCommon / up;
   }
 }
 
@@ -111,16 +122,241 @@ __global__ __launch_bounds__(256) void weigh_query_kernel(const KvWeighArgs w) {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// Tokens of the workgroup's range number `split` (and, past a hint that was too small, every a.splits-th after).
-// PREP: query tiles come from memory; else the workgroup makes them.
-template <int D, int BITS, int KT, bool PREP>
-__global__ __launch_bounds__(256, 2) void weigh_kernel(const KvWeighArgs w) {
+// A wave's tokens as they come from memory.
+template <int D, int BITS, int KT>
+struct Raw {
+  using G = Geometry<D, BITS>;
+  uint32_t k[KT][G::kLoads][G::kWords];
+  float scale[KT];
+  uint32_t there;   // bit k: step k's page is in the cache and some of its tokens in the sequence
+};
+
+// Codes and scales of the tokens first .. first + 16 KT - 1. Lane (r, g): token r's bytes, chunk g of every 4 * kLoad.
+template <int D, int BITS, int KT>
+__device__ __forceinline__ void load_keys(const KvAttentionArgs& a, ConstTable table, int head, int kv_len, int first, int r, int g,
+                                          Raw<D, BITS, KT>& t) {
   using R = Row<D, BITS>;
   using G = Geometry<D, BITS>;
+  const int page = 1 << a.lps;
+  t.there = 0;
+#pragma unroll
+  for (int k = 0; k < KT; k++) {
+    const int j = (first + 16 * k) >> a.lps;      // past the table's end: its last entry, not used
+    const int pg = table[j < a.max_pages ? j : a.max_pages - 1];
+    const bool ok = pg >= 0 && pg < a.num_pages;
+    t.there |= ok && first + 16 * k < kv_len ? 1u << k : 0u;
+    const uint8_t* block = a.cache + ((int64_t)(ok ? pg : 0) * a.heads + head) * a.head_bytes;
+    const int off = (first + 16 * k) & (page - 1);
+#pragma unroll
+    for (int l = 0; l < G::kLoads; l++) load_words(block + (off + r) * R::kBytes + g * G::kLoad + l * 4 * G::kLoad, t.k[k][l]);
+    t.scale[k] = *reinterpret_cast<const float*>(block + 2 * page * R::kBytes + (off + r) * 4);
+  }
+}
+
+// The same as operands: codes in fp16, and for each token what takes a product to a logit in base 2.
+template <int D, int BITS, int KT>
+struct Keys {
+  u32x4 op[KT][D / 32];
+  float factor[KT];
+};
+template <int D, int BITS, int KT>
+__device__ __forceinline__ void convert_keys(const KvAttentionArgs& a, const Raw<D, BITS, KT>& t, Keys<D, BITS, KT>& key) {
+  using R = Row<D, BITS>;
+  using G = Geometry<D, BITS>;
+#pragma unroll
+  for (int k = 0; k < KT; k++) {
+    // A scale that is no finite number belongs to a token that was never written.
+    key.factor[k] = fabsf(t.scale[k]) < __builtin_inff() ? t.scale[k] * (a.scale * (kLog2e * R::kNorm / kCommon)) : 0.0f;
+#pragma unroll
+    for (int op = 0; op < G::kOps; op++) {
+      if constexpr (BITS == 4) {
+        uint32_t h[4];
+        nibbles_f16(t.k[k][op / G::kWords][op % G::kWords], h);
+        key.op[k][op] = u32x4{h[0], h[1], h[2], h[3]};
+      } else {
+        uint32_t h[2], i[2];
+        bytes_f16(t.k[k][2 * op / G::kWords][2 * op % G::kWords], h);
+        bytes_f16(t.k[k][(2 * op + 1) / G::kWords][(2 * op + 1) % G::kWords], i);
+        key.op[k][op] = u32x4{h[0], h[1], i[0], i[1]};
+      }
+    }
+  }
+}
+
+// The products of a tile of queries at `q` (LDS) with a wave's keys. Operands are read four steps at a time, ahead of
+// the products: read one by one, each waits for LDS.
+template <int D, int BITS, int KT>
+__device__ __forceinline__ void multiply(const uint8_t* q, const Keys<D, BITS, KT>& key, int lane, f32x4 (&acc)[KT]) {
+  constexpr int kAhead = D / 32 < 4 ? D / 32 : 4;
+#pragma unroll
+  for (int k = 0; k < KT; k++) acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int o = 0; o < D / 32; o += kAhead) {
+    u32x4 lead[kAhead], rest[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      lead[i] = *reinterpret_cast<const u32x4*>(q + (o + i) * 2048 + lane * 16);
+      rest[i] = *reinterpret_cast<const u32x4*>(q + (o + i) * 2048 + 1024 + lane * 16);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+#pragma unroll
+      for (int k = 0; k < KT; k++) acc[k] = mfma(lead[i], key.op[k][o + i], acc[k]);
+#pragma unroll
+      for (int k = 0; k < KT; k++) acc[k] = mfma(rest[i], key.op[k][o + i], acc[k]);
+    }
+  }
+}
+
+// The rows' numbers of a tile that a lane needs: of rows 4 g .. 4 g + 3.
+struct RowInfo {
+  f32x4 lse, down;
+};
+template <int D>
+__device__ __forceinline__ RowInfo row_info(const uint8_t* q, int g) {
+  RowInfo i;
+  i.lse = *reinterpret_cast<const f32x4*>(q + QueryTile<D>::kWords + g * 16);
+  i.down = *reinterpret_cast<const f32x4*>(q + QueryTile<D>::kWords + 64 + g * 16);
+  return i;
+}
+
+// Whether every row of a tile (those past the last add nothing anyway) attends to all of the tokens first .. last.
+__device__ __forceinline__ int whole_tile(const KvAttentionArgs& a, int tile, int rows, int before, int first, int last) {
+  int all = 1;
+  if (a.causal) {
+    const int n1 = tile * kRows + kRows < rows ? tile * kRows + kRows - 1 : rows - 1;
+    all = before + token_of(a, tile * kRows) >= last && (a.window == 0 || before + token_of(a, n1) + 1 - a.window <= first);
+  }
+  return __builtin_amdgcn_readfirstlane(all);
+}
+
+// Whether all rows of a tile have the common scale.
+__device__ __forceinline__ int common_scale(const RowInfo& i) {
+  const bool own = i.down[0] != 1.0f || i.down[1] != 1.0f || i.down[2] != 1.0f || i.down[3] != 1.0f;
+  return __builtin_amdgcn_readfirstlane(__ballot(own) == 0);
+}
+
+// A zero row's product is 0 and its lse +inf: a weight of 0 whatever the scale.
+template <int KT>
+__device__ __forceinline__ void weights_of(f32x4 (&acc)[KT], const RowInfo& info, int common, const float (&factor)[KT], float (&p)[KT][4]) {
+  // The wait that a read of the last product needs, before the branch: it is not added across one.
+#pragma unroll
+  for (int k = 0; k < KT; k++) asm volatile("" : "+v"(acc[k]));
+  asm volatile("s_nop 7\n\ts_nop 3" : "+v"(acc[KT - 1]));
+  if (!common) {
+#pragma unroll
+    for (int k = 0; k < KT; k++) acc[k] *= info.down;
+  }
+#pragma unroll
+  for (int k = 0; k < KT; k++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) p[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[k][i], factor[k], -info.lse[i]));
+}
+
+template <int KT>
+__device__ __forceinline__ void add_weights(const KvAttentionArgs& a, const Seq& s, int tile, int all, int first, int r, int g,
+                                            float (&p)[KT][4], float (&sum)[KT]) {
+  if (!all) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      int lo, hi;
+      key_range(a, s, token_of(a, tile * kRows + 4 * g + i), lo, hi);
+#pragma unroll
+      for (int k = 0; k < KT; k++) {
+        const int j = first + 16 * k + r;
+        p[k][i] = j >= lo && j < hi ? p[k][i] : 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < KT; k++) sum[k] += (p[k][0] + p[k][1]) + (p[k][2] + p[k][3]);
+}
+
+// Over the four lanes of a token; then lane (r, g) writes token r of step g.
+template <int KT>
+__device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at, const Seq& s, int first, uint32_t there, int r, int g,
+                                           const float (&sum)[KT]) {
+  const KvAttentionArgs& a = w.a;
+  float mine = 0.0f;
+#pragma unroll
+  for (int k = 0; k < KT; k++) {
+    float x = there >> k & 1 ? sum[k] : 0.0f;
+    x += __shfl_xor(x, 16, 64);
+    x += __shfl_xor(x, 32, 64);
+    mine = g == k ? x : mine;
+  }
+  const int j = first + 16 * g + r;
+  if (g < KT && j < s.kv_len) {
+    const int64_t out = ((int64_t)at.seq * a.heads + at.head) * ((int64_t)a.max_pages << a.lps) + j;
+    if (a.row_tiles > 1) {
+      w.parts[at.tile * w.part_stride + out] = mine;
+    } else {
+      const bool had = w.keep != 0.0f && !(a.causal && j >= s.kv_len - s.q_len);
+      w.weights[out] = had ? __builtin_fmaf(w.keep, w.weights[out], mine) : mine;
+    }
+  }
+}
+
+constexpr int kFewTiles = 2;   // query tiles that a workgroup makes itself
+
+// Few query rows: the workgroup makes the query tiles once and walks over its ranges of tokens (number `split`
+// and every a.splits-th after), the next range's codes on their way meanwhile.
+template <int D, int BITS, int KT>
+__global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) {
   using Q = QueryTile<D>;
   constexpr int kKeys = kWaves * KT * 16;
-  constexpr int kBuffers = PREP ? 2 : 1;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuffers * Q::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kFewTiles * Q::kBytes];
+  const KvAttentionArgs& a = w.a;
+  const Place at = place(a);
+  if (at.seq >= a.seqs) return;
+  const Seq s = sequence(a, at.seq);
+  const int64_t step = (int64_t)a.splits * kKeys;
+  int64_t base = (int64_t)at.split * kKeys;
+  if (base >= s.kv_len) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int rows = rows_of(a, s), before = s.kv_len - s.q_len, tiles = (rows + kRows - 1) / kRows;   // at most kFewTiles
+  const ConstTable table = const_table(a.pages) + (int64_t)at.seq * a.max_pages;
+  Raw<D, BITS, KT> next;
+  load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, static_cast<int>(base) + wave * (KT * 16), r, g, next);
+  for (int tile = 0; tile < tiles; tile++) make_query_tile<D, BITS>(a, s, at.head, tile * kRows, rows, lds + tile * Q::kBytes);
+  __syncthreads();
+  for (; base < s.kv_len; base += step) {
+    const int first = static_cast<int>(base) + wave * (KT * 16);
+    Keys<D, BITS, KT> key;
+    convert_keys<D, BITS, KT>(a, next, key);
+    const uint32_t there = next.there;
+    // (Past the last range this one is loaded again: a load under a condition is waited for at once.)
+    const int64_t ahead = base + step < s.kv_len ? base + step : base;
+    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, static_cast<int>(ahead) + wave * (KT * 16), r, g, next);
+    float sum[KT];
+#pragma unroll
+    for (int k = 0; k < KT; k++) sum[k] = 0.0f;
+    for (int tile = 0; tile < tiles; tile++) {
+      int all = whole_tile(a, tile, rows, before, first, first + KT * 16 - 1);
+      const uint8_t* q = lds + tile * Q::kBytes;
+      const RowInfo info = row_info<D>(q, g);
+      int common = common_scale(info);
+      asm volatile("" : "+s"(all), "+s"(common));   // settled before the products
+      f32x4 acc[KT];
+      float p[KT][4];
+      multiply<D, BITS, KT>(q, key, lane, acc);
+      weights_of<KT>(acc, info, common, key.factor, p);
+      add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
+    }
+    write_sums<KT>(w, at, s, first, there, r, g, sum);
+  }
+}
+
+// Many query rows: tiles come from memory, made by weigh_query_kernel, copied to a ring in LDS three ahead.
+// a.row_tiles workgroups share a range's rows.
+template <int D, int BITS>
+__global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w) {
+  using Q = QueryTile<D>;
+  constexpr int KT = 4, kKeys = kWaves * KT * 16;
+  constexpr int kRing = 4, kCopies = Q::kWords / 1024 / kWaves + 1;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * Q::kBytes];
   const KvAttentionArgs& a = w.a;
   const Place at = place(a);
   if (at.seq >= a.seqs) return;
@@ -128,27 +364,26 @@ __global__ __launch_bounds__(256, 2) void weigh_kernel(const KvWeighArgs w) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int rows = rows_of(a, s), before = s.kv_len - s.q_len;   // position of the first query row
-  const int page = 1 << a.lps;
   const ConstTable table = const_table(a.pages) + (int64_t)at.seq * a.max_pages;
+  const uint8_t* const queries = w.queries + (first_tile(a, s, at.seq) * a.heads + at.head) * Q::kBytes;
+  // (Buffer copies: the compiler takes the other kind for LDS accesses and waits for them before each read.)
+  auto fetch = [&](int tile, int buffer) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(queries + (int64_t)tile * a.heads * Q::kBytes), (short)0, Q::kBytes, 0x00020000);
+    uint8_t* dst = lds + buffer * Q::kBytes;
+#pragma unroll
+    for (int i = 0; i < Q::kWords / 1024 / kWaves; i++) {
+      const int c = wave * (Q::kWords / 1024 / kWaves) + i;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(dst + c * 1024), 16, lane * 16, c * 1024, 0, 0);
+    }
+    // Every wave copies the rows' numbers, to the same place.
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(dst + Q::kWords), 4, lane * 4, Q::kWords, 0, 0);
+  };
 
   for (int64_t base = (int64_t)at.split * kKeys; base < s.kv_len; base += (int64_t)a.splits * kKeys) {
     const int key0 = static_cast<int>(base), first = key0 + wave * (KT * 16);   // the workgroup's, the wave's
-    // The codes and scales of this wave's tokens. Lane (r, g): token r's bytes, chunk g of every 4 * kLoad.
-    uint32_t raw[KT][G::kLoads][G::kWords];
-    float ks[KT];
-    bool there[KT];
-#pragma unroll
-    for (int k = 0; k < KT; k++) {
-      const int j = (first + 16 * k) >> a.lps;      // past the table's end: its last entry, not used
-      const int pg = table[j < a.max_pages ? j : a.max_pages - 1];
-      there[k] = pg >= 0 && pg < a.num_pages && first + 16 * k < s.kv_len;
-      const uint8_t* block = a.cache + ((int64_t)(there[k] ? pg : 0) * a.heads + at.head) * a.head_bytes;
-      const int off = (first + 16 * k) & (page - 1);
-#pragma unroll
-      for (int l = 0; l < G::kLoads; l++)
-        load_words(block + (off + r) * R::kBytes + g * G::kLoad + l * 4 * G::kLoad, raw[k][l]);
-      ks[k] = *reinterpret_cast<const float*>(block + 2 * page * R::kBytes + (off + r) * 4);
-    }
+    Raw<D, BITS, KT> raw;
+    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, first, r, g, raw);
     // The tiles of rows that attend to some token of the workgroup's range, and this workgroup's share.
     int t0 = 0, t1 = (rows + kRows - 1) / kRows;
     if (a.causal) {
@@ -168,121 +403,41 @@ __global__ __launch_bounds__(256, 2) void weigh_kernel(const KvWeighArgs w) {
       t0 += at.tile * share;
       t1 = t0 + share < t1 ? t0 + share : t1;
     }
-    const uint8_t* const queries = PREP ? w.queries + (first_tile(a, s, at.seq) * a.heads + at.head) * Q::kBytes : nullptr;
-    // (Buffer copies: the compiler takes the other kind for LDS accesses and waits for them before each read.)
-    auto fetch = [&](int tile, int buffer) __attribute__((always_inline)) {
-      const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(queries + (int64_t)tile * a.heads * Q::kBytes), (short)0, Q::kBytes, 0x00020000);
-      uint8_t* dst = lds + buffer * Q::kBytes;
 #pragma unroll
-      for (int i = 0; i < Q::kWords / 1024 / kWaves; i++) {
-        const int c = wave * (Q::kWords / 1024 / kWaves) + i;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(dst + c * 1024), 16, lane * 16, c * 1024, 0, 0);
-      }
-      // Every wave copies the rows' numbers, to the same place.
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(dst + Q::kWords), 4, lane * 4, Q::kWords, 0, 0);
-    };
-    if (PREP && t0 < t1) fetch(t0, 0);
-
-    u32x4 key[KT][G::kOps];
-    float factor[KT], sum[KT];
+    for (int i = 0; i < kRing - 1; i++)
+      if (t0 + i < t1) fetch(t0 + i, i);
+    Keys<D, BITS, KT> key;
+    convert_keys<D, BITS, KT>(a, raw, key);
+    float sum[KT];
 #pragma unroll
-    for (int k = 0; k < KT; k++) {
-      // A scale that is no finite number belongs to a token that was never written.
-      factor[k] = fabsf(ks[k]) < __builtin_inff() ? ks[k] * (a.scale * (kLog2e * R::kNorm)) : 0.0f;
-      sum[k] = 0.0f;
-#pragma unroll
-      for (int op = 0; op < G::kOps; op++) {
-        if constexpr (BITS == 4) {
-          uint32_t h[4];
-          nibbles_f16(raw[k][op / G::kWords][op % G::kWords], h);
-          key[k][op] = u32x4{h[0], h[1], h[2], h[3]};
-        } else {
-          uint32_t h[2], i[2];
-          bytes_f16(raw[k][2 * op / G::kWords][2 * op % G::kWords], h);
-          bytes_f16(raw[k][(2 * op + 1) / G::kWords][(2 * op + 1) % G::kWords], i);
-          key[k][op] = u32x4{h[0], h[1], i[0], i[1]};
-        }
-      }
-    }
-
+    for (int k = 0; k < KT; k++) sum[k] = 0.0f;
     for (int tile = t0; tile < t1; tile++) {
-      const int buffer = PREP ? (tile - t0) & 1 : 0;
-      if constexpr (PREP) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's part of the tile is there,
-        __syncthreads();                                    // and everybody's; the other buffer is done with
-        if (tile + 1 < t1) fetch(tile + 1, buffer ^ 1);
+      const int buffer = (tile - t0) % kRing;
+      // This wave's part of the tile is there (those of the next two may be under way), then everybody's, and
+      // the buffer of the tile before is done with: its reads were waited for before their products.
+      if (tile + 2 < t1) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kCopies) : "memory");
+      } else if (tile + 1 < t1) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
       } else {
-        __syncthreads();                                    // the tile before is done with
-        make_query_tile<D, BITS>(a, s, at.head, tile * kRows, rows, lds);
-        __syncthreads();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
-      // Does every row of the tile (those past the last add nothing anyway) attend to all of the wave's tokens?
-      int all = 1;
-      if (a.causal) {
-        const int n1 = tile * kRows + kRows < rows ? tile * kRows + kRows - 1 : rows - 1;
-        all = before + token_of(a, tile * kRows) >= first + KT * 16 - 1 &&
-              (a.window == 0 || before + token_of(a, n1) + 1 - a.window <= first);
-      }
-      all = __builtin_amdgcn_readfirstlane(all);
-      asm volatile("" : "+s"(all));   // settled before the products: no branch between them and their first use
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (tile + kRing - 1 < t1) fetch(tile + kRing - 1, (buffer + kRing - 1) % kRing);
       const uint8_t* q = lds + buffer * Q::kBytes;
+      const RowInfo info = row_info<D>(q, g);
+      int all = whole_tile(a, tile, rows, before, first, first + KT * 16 - 1), common = common_scale(info);
+      asm volatile("" : "+s"(all), "+s"(common));
       f32x4 acc[KT];
-#pragma unroll
-      for (int k = 0; k < KT; k++) acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int op = 0; op < G::kOps; op++) {
-        const u32x4 lead = *reinterpret_cast<const u32x4*>(q + op * 2048 + lane * 16);
-        const u32x4 rest = *reinterpret_cast<const u32x4*>(q + op * 2048 + 1024 + lane * 16);
-#pragma unroll
-        for (int k = 0; k < KT; k++) acc[k] = mfma(lead, key[k][op], acc[k]);
-#pragma unroll
-        for (int k = 0; k < KT; k++) acc[k] = mfma(rest, key[k][op], acc[k]);
-      }
-      const f32x4 lse = *reinterpret_cast<const f32x4*>(q + Q::kWords + g * 16);
-      const f32x4 down = *reinterpret_cast<const f32x4*>(q + Q::kWords + 64 + g * 16);
       float p[KT][4];
-#pragma unroll
-      for (int k = 0; k < KT; k++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          p[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[k][i] * down[i], factor[k], -lse[i]));
-      if (!all) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          int lo, hi;
-          key_range(a, s, token_of(a, tile * kRows + 4 * g + i), lo, hi);
-#pragma unroll
-          for (int k = 0; k < KT; k++) {
-            const int j = first + 16 * k + r;
-            p[k][i] = j >= lo && j < hi ? p[k][i] : 0.0f;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < KT; k++) sum[k] += (p[k][0] + p[k][1]) + (p[k][2] + p[k][3]);
+      multiply<D, BITS, KT>(q, key, lane, acc);
+      weights_of<KT>(acc, info, common, key.factor, p);
+      add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
-    if constexpr (PREP) __syncthreads();   // both buffers are done with before the next range's first copy
-
-    // Over the four lanes of a token; then lane (r, g) writes token r of step g.
-    float mine = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KT; k++) {
-      float x = there[k] ? sum[k] : 0.0f;
-      x += __shfl_xor(x, 16, 64);
-      x += __shfl_xor(x, 32, 64);
-      mine = g == k ? x : mine;
-    }
-    const int j = first + 16 * g + r;
-    if (g < KT && j < s.kv_len) {
-      const int64_t out = ((int64_t)at.seq * a.heads + at.head) * ((int64_t)a.max_pages << a.lps) + j;
-      if (a.row_tiles > 1) {
-        w.parts[at.tile * w.part_stride + out] = mine;
-      } else {
-        const bool had = w.keep != 0.0f && !(a.causal && j >= before);
-        w.weights[out] = had ? __builtin_fmaf(w.keep, w.weights[out], mine) : mine;
-      }
-    }
+    __syncthreads();   // the buffers are done with before the next range's first copy
+    write_sums<KT>(w, at, s, first, raw.there, r, g, sum);
   }
 }
 
@@ -302,28 +457,28 @@ __global__ __launch_bounds__(256) void weigh_join_kernel(const KvWeighArgs w) {
   }
 }
 
-template <int D, int BITS, int KT, bool PREP>
-hipError_t launch_kt(const KvWeighArgs& w, hipStream_t st) {
+template <int D, int BITS>
+hipError_t launch(const KvWeighArgs& w, int kt, bool many, hipStream_t st) {
   const KvAttentionArgs& a = w.a;
-  if constexpr (PREP) {
+  if (many) {
     hipLaunchKernelGGL((weigh_query_kernel<D, BITS>), dim3((unsigned)((int64_t)a.seqs * w.query_tiles_seq * a.heads)), dim3(256), 0, st, w);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int64_t pairs = ((int64_t)a.seqs * a.splits + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL((weigh_kernel<D, BITS, KT, PREP>), dim3((unsigned)(pairs * a.heads * a.row_tiles)), dim3(256), 0, st, w);
+  const dim3 grid((unsigned)(pairs * a.heads * a.row_tiles)), block(256);
+  if (many)
+    hipLaunchKernelGGL((weigh_many_kernel<D, BITS>), grid, block, 0, st, w);
+  else if (kt == 1)
+    hipLaunchKernelGGL((weigh_few_kernel<D, BITS, 1>), grid, block, 0, st, w);
+  else
+    hipLaunchKernelGGL((weigh_few_kernel<D, BITS, 2>), grid, block, 0, st, w);
   if (a.row_tiles > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(weigh_join_kernel, dim3((unsigned)w.join_blocks, (unsigned)(a.seqs * a.heads)), dim3(256), 0, st, w);
   }
   return hipGetLastError();
-}
-
-template <int D, int BITS>
-hipError_t launch(const KvWeighArgs& w, int kt, bool prep, hipStream_t st) {
-  if (prep) return launch_kt<D, BITS, 4, true>(w, st);
-  return kt == 4 ? launch_kt<D, BITS, 4, false>(w, st) : kt == 2 ? launch_kt<D, BITS, 2, false>(w, st) : launch_kt<D, BITS, 1, false>(w, st);
 }
 
 }  // namespace
@@ -333,16 +488,20 @@ KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int
   KvWeighPlan p = {};
   const int64_t group = q_heads / heads;
   p.query_tiles_seq = (max_q_len * group + kRows - 1) / kRows;
-  // Above 32 rows queries are rotated once for all.
-  p.prep = p.query_tiles_seq > 2;
-  p.kt = 4;
+  // Above 32 rows queries are rotated once for all. (Two tiles of them fit beside the codes; see the top for the rest.)
+  p.many = p.query_tiles_seq > kFewTiles;
+  p.kt = p.many ? 4 : 2;
   auto ranges = [&] { return (max_kv_len + kWaves * 16 * p.kt - 1) / (kWaves * 16 * p.kt); };
-  if (!p.prep)
-    while (p.kt > 1 && ranges() * seqs * heads < 1024) p.kt /= 2;
+  if (!p.many)
+    if (ranges() * seqs * heads < 1024) p.kt = 1;
   p.splits = ranges() < 1 ? 1 : ranges();
+  if (!p.many) {
+    const int64_t pairs = (int64_t)seqs * heads, want = (4096 + pairs - 1) / pairs;
+    if (p.splits > want) p.splits = want;
+  }
   p.row_splits = 1;
-  if (p.prep) {
-    const int64_t groups = p.splits * seqs * heads, want = (512 + groups - 1) / groups, most = p.query_tiles_seq / 8;
+  if (p.many) {
+    const int64_t groups = p.splits * seqs * heads, want = (6000 + groups - 1) / groups, most = p.query_tiles_seq / 8;
     p.row_splits = want < most ? want : most;
     if (p.row_splits > 16) p.row_splits = 16;
     if (p.row_splits < 1) p.row_splits = 1;
@@ -354,11 +513,11 @@ KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int
   return p;
 }
 
-hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool prep, hipStream_t stream) {
+hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool many, hipStream_t stream) {
   switch (head_dim) {
-    case 64: return bits == 8 ? launch<64, 8>(w, kt, prep, stream) : launch<64, 4>(w, kt, prep, stream);
-    case 128: return bits == 8 ? launch<128, 8>(w, kt, prep, stream) : launch<128, 4>(w, kt, prep, stream);
-    default: return bits == 8 ? launch<256, 8>(w, kt, prep, stream) : launch<256, 4>(w, kt, prep, stream);
+    case 64: return bits == 8 ? launch<64, 8>(w, kt, many, stream) : launch<64, 4>(w, kt, many, stream);
+    case 128: return bits == 8 ? launch<128, 8>(w, kt, many, stream) : launch<128, 4>(w, kt, many, stream);
+    default: return bits == 8 ? launch<256, 8>(w, kt, many, stream) : launch<256, 4>(w, kt, many, stream);
   }
 }
 
