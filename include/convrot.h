@@ -462,8 +462,12 @@ typedef struct {
 /* What the tables hold is not trusted with memory: kv_len is cut to [0, max_pages * page_size], a token of a
  * page outside the cache is moved as a row of zeros (codes and scales), and a new page outside the
  * cache is not written. No two outputs may overlap, nor an output an input. seqs * kv_heads < 2^22 and
- * seqs * kv_heads * ceil(budget / 64) < 2^24. */
-rq_status rq_kv_evict(const rq_kv_evict_params *p, const rq_kv_config *cfg, void *stream);
+ * seqs * kv_heads * ceil(budget / 64) < 2^24.
+ *   workspace as for rq_kv_attention, of rq_kv_evict_workspace_size() bytes, which looks at seqs and max_pages
+ *             only (few long sequences need one; at most 6 MB) */
+size_t rq_kv_evict_workspace_size(const rq_kv_evict_params *p, const rq_kv_config *cfg);
+rq_status rq_kv_evict(const rq_kv_evict_params *p, const rq_kv_config *cfg, void *workspace,
+                      size_t ws_bytes, void *stream);
 
 /* Static text for a status code. */
 const char *rq_status_string(rq_status s);

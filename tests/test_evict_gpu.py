@@ -80,6 +80,28 @@ def test_long_rows(n):
     _check(d, first=4, recent=300)
 
 
+@pytest.mark.parametrize("n", [16385, 40001, 131071])
+def test_rows_in_parts(n):
+    """Few rows whose choice is shared by many workgroups: cuts of a row in front of, inside and behind what stays."""
+    d = _case([n, n // 3, 900, 1001], 1000, dim=64, page=256, heads=1, seed=n)
+    assert rq.kv_evict_workspace_size(4, d["pages"].shape[1], d["cfg"]) > 0
+    _check(d, first=4, recent=300)
+    _check(d, first=600, recent=400)
+    d["weights"][:] = np.round(d["weights"])       # many of one size
+    _check(d, recent=1)
+    d = _case([n], n - 7, dim=64, page=256, heads=1, seed=n)
+    _check(d, first=n // 2, recent=n // 3)
+    d["weights"][:] = 0.0
+    _check(d)
+
+
+def test_many_long_rows():
+    """As many rows as workgroups are wanted: one each, several passes long."""
+    d = _case([4500] * 130 + [9000], 64, dim=64, page=512, heads=2, seed=11)
+    assert rq.kv_evict_workspace_size(131, d["pages"].shape[1], d["cfg"]) == 0
+    _check(d, recent=16)
+
+
 @pytest.mark.parametrize("kind", ["zeros", "ones", "steps", "specials", "near", "negative", "rising", "falling"])
 def test_weights_of_every_kind(kind):
     """Ties go to the first; NaN is below all; -0 is 0; infinities; weights that differ in their last bit only."""
@@ -148,6 +170,33 @@ def test_streams_outputs_and_replays():
         d["weights"] = np.roll(d["weights"], 7, 2)
         W.copy_(torch.from_numpy(d["weights"]))
         other.copy_(torch.from_numpy(d["raw"]))
+        cache, want, _ = _check(d, first=1, recent=9)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want) and torch.equal(other, cache)
+
+
+def test_parts_in_a_graph_and_given_a_workspace():
+    d = _case([9000, 12000], 500, dim=64, page=256, heads=2, seed=6)
+    W, pages, new_pages, kv_len = torch.from_numpy(d["weights"]).cuda(), _ints(d["pages"]), _ints(d["new_pages"]), _ints(d["kv_len"])
+    need = rq.kv_evict_workspace_size(2, pages.shape[1], d["cfg"])
+    other, space = torch.from_numpy(d["raw"]).cuda(), torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    cache, want, _ = _check(d, first=1, recent=9)
+    kept, n = torch.empty_like(want), torch.empty_like(kv_len)
+    args = dict(first=1, recent=9, kept=kept, new_kv_len=n, workspace=space)
+    with pytest.raises(ValueError, match="workspace"):
+        rq.kv_evict(other, pages, kv_len, W, d["cfg"], 500, new_pages, **{**args, "workspace": space[:need - 1]})
+    rq.kv_evict(other, pages, kv_len, W, d["cfg"], 500, new_pages, **args)
+    assert torch.equal(kept, want) and torch.equal(other, cache) and bool((space[need:] == 255).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rq.kv_evict(other, pages, kv_len, W, d["cfg"], 500, new_pages, **args)
+    for i in range(4):
+        d["weights"] = np.roll(d["weights"], 7, 2)
+        W.copy_(torch.from_numpy(d["weights"]))
+        other.copy_(torch.from_numpy(d["raw"]))
+        space.fill_(i)
         cache, want, _ = _check(d, first=1, recent=9)
         torch.cuda.synchronize()
         graph.replay()

@@ -11,11 +11,11 @@ from tests import evict_ref
 from tests.test_abi import A, GB, HEADER
 
 
-def _evict(cfg=None, **kw):
+def _evict(cfg=None, ws=None, ws_bytes=0, **kw):
     p = dict(cache=A, kv_len=A + GB, pages=A + 2 * GB, new_pages=A + 3 * GB, weights=A + 4 * GB, new_weights=A + 5 * GB,
              new_kv_len=A + 6 * GB, kept=A + 7 * GB, num_pages=100, seqs=4, max_pages=20, new_max_pages=5, budget=300, first=4, recent=32)
     p.update(kw)
-    return rq.rq_kv_evict(rq.rq_kv_evict_params(*p.values()), cfg or rq.make_kv_cfg(2, 128, 64, 4), None)
+    return rq.rq_kv_evict(rq.rq_kv_evict_params(*p.values()), cfg or rq.make_kv_cfg(2, 128, 64, 4), ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -33,6 +33,10 @@ def _evict(cfg=None, **kw):
     (dict(kept=A + 64), rq.RQ_EINVAL), (dict(new_kv_len=A + GB), rq.RQ_EINVAL), (dict(kept=A + 3 * GB), rq.RQ_EINVAL),
     (dict(new_weights=A + 4 * GB), rq.RQ_EINVAL), (dict(new_weights=A + 7 * GB), rq.RQ_EINVAL), (dict(new_kv_len=A + 7 * GB + 64), rq.RQ_EINVAL),
     (dict(weights=A + 4096), rq.RQ_EINVAL), (dict(pages=A + 16), rq.RQ_EINVAL),
+    (dict(max_pages=200), rq.RQ_EWORKSPACE), (dict(max_pages=200, ws=A + 8 * GB, ws_bytes=1000), rq.RQ_EWORKSPACE),
+    (dict(max_pages=200, ws_bytes=GB), rq.RQ_EINVAL), (dict(max_pages=200, ws=A + 8 * GB + 4, ws_bytes=GB), rq.RQ_EINVAL),
+    (dict(max_pages=200, ws=A + 4 * GB, ws_bytes=GB), rq.RQ_EINVAL), (dict(max_pages=200, ws=A + 7 * GB, ws_bytes=GB), rq.RQ_EINVAL),
+    (dict(max_pages=200, ws=A + 64, ws_bytes=GB), rq.RQ_EINVAL),
 ])
 def test_eviction_refused(kw, status):
     assert _evict(**kw) == status
@@ -42,8 +46,8 @@ def test_eviction_refused(kw, status):
 def test_nothing_to_evict():
     assert _evict(seqs=0) == rq.RQ_OK
     cfg = rq.make_kv_cfg(2, 128, 64, 4)
-    assert rq.load().rq_kv_evict(None, ctypes.byref(cfg), None) == rq.RQ_EINVAL
-    assert rq.load().rq_kv_evict(ctypes.byref(rq.rq_kv_evict_params()), None, None) == rq.RQ_EINVAL
+    assert rq.load().rq_kv_evict(None, ctypes.byref(cfg), None, 0, None) == rq.RQ_EINVAL
+    assert rq.load().rq_kv_evict(ctypes.byref(rq.rq_kv_evict_params()), None, None, 0, None) == rq.RQ_EINVAL
 
 
 def test_struct_matches_header():
@@ -92,9 +96,23 @@ def test_workspaces():
     assert rq.kv_attention_weights_workspace_size(4, 8, 4, 100, cfg) == 0                 # single tokens
     assert rq.kv_attention_weights_workspace_size(64, 8, 4, 100, cfg, max_q_len=8, ragged=True) == 0
     # 4 heads of 16 rows' tiles: 4 operand steps of 2 KB and 256 bytes a tile, and a spare tile a sequence.
+    # And the sums of three shares of the rows: 250 ranges of tokens of 8 (sequence, head) pairs are 2000 workgroups.
     got = rq.kv_attention_weights_workspace_size(4000, 8, 4, 1000, cfg, max_q_len=1000, ragged=True)
-    assert got == (4000 * 4 // 16 + 4 + 1) * 2 * (4 * 2048 + 256)
+    query = (4000 * 4 // 16 + 4 + 1) * 2 * (4 * 2048 + 256)
+    assert got == -(-query // 256) * 256 + 3 * 8 * 64000 * 4
     assert rq.kv_attention_weights_workspace_size(-1, 8, 4, 100, cfg) == 0
+
+
+def test_eviction_workspaces():
+    cfg = rq.make_kv_cfg(2, 128, 64, 4)
+    word = 2 + 2 * 2048 + 1024
+    assert rq.kv_evict_workspace_size(4, 64, cfg) == 0                                          # 4096 tokens
+    assert rq.kv_evict_workspace_size(4, 65, cfg) == 8 * 4 * (4 + 2 * word)                     # two parts
+    assert rq.kv_evict_workspace_size(4, 10000, cfg) == 8 * 4 * (4 + 32 * word)                 # the most parts
+    assert rq.kv_evict_workspace_size(64, 10000, cfg) == 128 * 4 * (4 + 2 * word)               # 256 workgroups
+    assert rq.kv_evict_workspace_size(65, 10000, cfg) == 0
+    assert rq.kv_evict_workspace_size(0, 10000, cfg) == 0 and rq.kv_evict_workspace_size(-1, -1, cfg) == 0
+    assert rq.kv_evict_workspace_size(4, 1 << 30, cfg) == 0 and rq.kv_evict_workspace_size(4, 100, rq.make_kv_cfg(2, 96, 64, 4)) == 0
 
 
 def test_wrapper_refusals():

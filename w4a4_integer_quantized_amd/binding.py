@@ -101,7 +101,7 @@ def load():
         "rq_kv_cache_read": [P, I64, P, I64, KV, P, P, I32, I64, I64, I64, I64, P],
         "rq_kv_attention": [ATT, KV, P, I64, P, SZ, P],
         "rq_kv_attention_weights": [ATT, KV, P, I64, P, ctypes.c_float, P, SZ, P],
-        "rq_kv_evict": [ctypes.POINTER(rq_kv_evict_params), KV, P],
+        "rq_kv_evict": [ctypes.POINTER(rq_kv_evict_params), KV, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -119,6 +119,8 @@ def load():
     lib.rq_kv_attention_workspace_size.restype = SZ
     lib.rq_kv_attention_weights_workspace_size.argtypes = [ATT, KV]
     lib.rq_kv_attention_weights_workspace_size.restype = SZ
+    lib.rq_kv_evict_workspace_size.argtypes = [ctypes.POINTER(rq_kv_evict_params), KV]
+    lib.rq_kv_evict_workspace_size.restype = SZ
     lib.rq_status_string.argtypes = [ctypes.c_int]
     lib.rq_status_string.restype = ctypes.c_char_p
     lib.rq_last_error_detail.argtypes = []
@@ -239,8 +241,12 @@ def rq_kv_attention_weights(params, cfg, cache, num_pages, weights, keep, worksp
                                           ws_bytes, stream)
 
 
-def rq_kv_evict(params, cfg, stream) -> int:
-    return load().rq_kv_evict(ctypes.byref(params), ctypes.byref(cfg), stream)
+def rq_kv_evict_workspace_size(params, cfg) -> int:
+    return load().rq_kv_evict_workspace_size(ctypes.byref(params), ctypes.byref(cfg))
+
+
+def rq_kv_evict(params, cfg, workspace, ws_bytes, stream) -> int:
+    return load().rq_kv_evict(ctypes.byref(params), ctypes.byref(cfg), workspace, ws_bytes, stream)
 
 
 def rq_status_string(s: int) -> str:
@@ -907,8 +913,13 @@ def kv_attention_weights_workspace_size(total_q: int, q_heads: int, seqs: int, m
     return rq_kv_attention_weights_workspace_size(p, cfg)
 
 
+def kv_evict_workspace_size(seqs: int, max_pages: int, cfg: rq_kv_config) -> int:
+    """Bytes of workspace a kv_evict call of these sizes needs (0: none)."""
+    return rq_kv_evict_workspace_size(rq_kv_evict_params(seqs=seqs, max_pages=max_pages), cfg)
+
+
 def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_pages, new_weights=None, first: int = 0,
-             recent: int = 0, kept=None, new_kv_len=None, stream=None):
+             recent: int = 0, kept=None, new_kv_len=None, workspace=None, stream=None):
     """The sequences' caches brought down to `budget` tokens, written into new_pages [seqs, new_max_pages]
     (int32; pages that `pages` does not have, each once): for each key head the first `first` tokens, the last
     `recent`, and of the others those with the largest weights [seqs, kv_heads, max_pages * page_size] (f32), in
@@ -931,10 +942,11 @@ def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_
         _kv_table(kept, "kept", kv.int32, (seqs, cfg.kv_heads, budget))
     if new_kv_len is not None:
         _kv_table(new_kv_len, "new_kv_len", kv.int32, (seqs,))
-    index = _kv_device(cache, pages, kv_len, weights, new_pages, new_weights, kept, new_kv_len)
+    index = _kv_device(cache, pages, kv_len, weights, new_pages, new_weights, kept, new_kv_len, workspace)
     if stream is not None or index != kv.current_device():
         with _kv_placed(kv, index, stream):
-            return kv_evict(cache, pages, kv_len, weights, cfg, budget, new_pages, new_weights, first, recent, kept, new_kv_len)
+            return kv_evict(cache, pages, kv_len, weights, cfg, budget, new_pages, new_weights, first, recent, kept, new_kv_len,
+                            workspace)
     if kept is None:
         kept = pages.new_empty((seqs, cfg.kv_heads, max(budget, 0)))
     if new_kv_len is None:
@@ -942,5 +954,11 @@ def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_
     p = rq_kv_evict_params(cache.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), new_pages.data_ptr(), weights.data_ptr(),
                            None if new_weights is None else new_weights.data_ptr(), new_kv_len.data_ptr(), kept.data_ptr(),
                            num_pages, seqs, max_pages, new_max, budget, first, recent)
-    _check(rq_kv_evict(p, cfg, kv.raw_stream(index)), "rq_kv_evict")
+    need = rq_kv_evict_workspace_size(p, cfg)
+    if workspace is not None:
+        _check_bytes(workspace, "workspace", need, exact=False)
+    elif need > 0:
+        workspace = cache.new_empty((need,))
+    at = None if workspace is None else workspace.data_ptr()
+    _check(rq_kv_evict(p, cfg, at, 0 if workspace is None else _nbytes(workspace), kv.raw_stream(index)), "rq_kv_evict")
     return kept, new_kv_len

@@ -700,7 +700,7 @@ rq_status check_kv_weigh(const rq_kv_attention_params* p, const rq_kv_config* cf
 }
 
 // ---- eviction
-rq_status check_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg) {
+rq_status check_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg, const void* ws, size_t ws_bytes, convrot::KvEvictPlan* plan) {
   rq_status s = check_kv_cfg(cfg);
   if (s) return s;
   if (!p) return fail(RQ_EINVAL, "params is NULL");
@@ -731,19 +731,27 @@ rq_status check_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg) {
     if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
       return fail(RQ_EINVAL, "kv_len, pages, new_pages, new_weights, new_kv_len or kept is not 4-byte aligned");
   if ((s = check_ptr(p->weights, "weights", false))) return s;
-  const struct { const void* at; int64_t bytes; } outs[4] = {{p->cache, p->num_pages * kv_head_bytes(cfg) * cfg->kv_heads},
+  *plan = convrot::plan_kv_evict(groups, span);
+  const int64_t need = (int64_t)plan->workspace_bytes;
+  if (need > 0) {
+    if (ws_bytes < (size_t)need) return fail(RQ_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, (size_t)need);
+    if ((s = check_ptr(ws, "workspace"))) return s;
+  }
+  const struct { const void* at; int64_t bytes; } outs[5] = {{p->cache, p->num_pages * kv_head_bytes(cfg) * cfg->kv_heads},
                                                              {p->new_weights, groups * new_span * 4},
                                                              {p->new_kv_len, (int64_t)p->seqs * 4},
-                                                             {p->kept, groups * p->budget * 4}},
+                                                             {p->kept, groups * p->budget * 4},
+                                                             {need > 0 ? ws : nullptr, need}},
                                                  ins[4] = {{p->kv_len, (int64_t)p->seqs * 4},
                                                            {p->pages, (int64_t)p->seqs * p->max_pages * 4},
                                                            {p->new_pages, (int64_t)p->seqs * p->new_max_pages * 4},
                                                            {p->weights, groups * span * 4}};
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < 5; i++) {
     for (const auto& in : ins)
-      if (overlap(outs[i].at, outs[i].bytes, in.at, in.bytes)) return fail(RQ_EINVAL, "the cache or an output overlaps an input");
+      if (overlap(outs[i].at, outs[i].bytes, in.at, in.bytes))
+        return fail(RQ_EINVAL, "the cache, an output or the workspace overlaps an input");
     for (int j = 0; j < i; j++)
-      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return fail(RQ_EINVAL, "the cache and the outputs must not overlap");
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return fail(RQ_EINVAL, "the cache, the outputs and the workspace must not overlap");
   }
   return ok();
 }
@@ -1038,8 +1046,15 @@ rq_status rq_kv_attention_weights(const rq_kv_attention_params* p, const rq_kv_c
                   "kv_weigh launch");
 }
 
-rq_status rq_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg, void* stream) {
-  rq_status s = check_kv_evict(p, cfg);
+size_t rq_kv_evict_workspace_size(const rq_kv_evict_params* p, const rq_kv_config* cfg) {
+  if (check_kv_cfg(cfg) != RQ_OK || !p || p->seqs < 1 || p->seqs > 65535 || p->max_pages < 0) return 0;
+  const int64_t span = (int64_t)p->max_pages * cfg->page_size;
+  return span > kMaxKvTokens ? 0 : convrot::plan_kv_evict((int64_t)p->seqs * cfg->kv_heads, span).workspace_bytes;
+}
+
+rq_status rq_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg, void* workspace, size_t ws_bytes, void* stream) {
+  convrot::KvEvictPlan plan = {};
+  rq_status s = check_kv_evict(p, cfg, workspace, ws_bytes, &plan);
   if (s || p->seqs == 0) return s;
   convrot::KvEvictArgs a = {};
   a.cache = static_cast<uint8_t*>(p->cache);
@@ -1061,6 +1076,8 @@ rq_status rq_kv_evict(const rq_kv_evict_params* p, const rq_kv_config* cfg, void
   a.first = p->first;
   a.recent = p->recent;
   a.chunks = static_cast<int>(convrot::kv_evict_chunks(p->budget));
+  a.parts = plan.parts;
+  a.scratch = static_cast<uint32_t*>(workspace);
   return from_hip(convrot::launch_kv_evict(a, cfg->head_dim * cfg->bits / 8, static_cast<hipStream_t>(stream)), "kv_evict launch");
 }
 

@@ -159,8 +159,15 @@ struct KvEvictArgs {
   int64_t num_pages, head_bytes;
   int seqs, heads, max_pages, new_max_pages, lps, budget, first, recent;
   int chunks;                                  // kv_evict_chunks(budget)
+  int parts;                                   // workgroups that choose for a (sequence, head)
+  uint32_t* scratch;                           // their workspace
+};
+struct KvEvictPlan {
+  int parts;
+  size_t workspace_bytes;
 };
 int64_t kv_evict_chunks(int budget);           // workgroups that move a (sequence, head)
+KvEvictPlan plan_kv_evict(int64_t groups, int64_t span);   // groups: (sequence, head) pairs
 hipError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, hipStream_t stream);
 
 }  // namespace convrot

@@ -5,10 +5,12 @@
 // evict_select_kernel: a workgroup a (sequence, key head). The weight of the last token that still fits
 // is found digit by digit (11, 11 and 10 bits of the weights as ordered integers, a histogram of 2048 counters in LDS for
 // each), then one pass in order writes the indices: everything above that weight, and of those beside it the
-// first. Counters are integers: the same choice every time.
+// first. Counters are integers: the same choice every time. Few long rows are cut into parts (evict_part_kernel).
+// Weights kept in registers over the four passes: no gain (the instructions bound it, and there are fewer waves).
 // evict_move_kernel: bound by memory. Bytes are moved as they are. K rows and scales are copied; V bytes lie four
 // tokens side by side, so each four new tokens gather a byte from each of four old groups: a lone token
-// that stays costs the reading of its whole group's V lines.
+// that stays costs the reading of its whole group's V lines. 64 sequences of 8192 tokens to 2048, 8 heads of 128, 4-bit
+// codes: 93 us for 67 MB of K, 183 MB of V's groups of which some token stays, 16 MB of scales and 134 MB written: 4.3 TB/s.
 #include "kv_common.h"
 
 namespace convrot {
@@ -19,6 +21,10 @@ using namespace kv;
 constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64;
 constexpr int kBins = 2048;
 constexpr int kMoveTokens = 64;   // new tokens of a move workgroup
+// A row's parts, and the workgroups that they come to. (32 rows of 131072 tokens: 137 us with one workgroup a row, whose
+// CU's vector instructions bound it; 40 with 256 in all, 46 with 512 and 71 with 1024, as every part reads every part's
+// counters. 512 rows of 8192: 29 us as they are, 60 in two parts each.)
+constexpr int kPartTokens = 4096, kSelectGroups = 256;
 
 typedef float f32x4u __attribute__((ext_vector_type(4)));
 
@@ -45,113 +51,225 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
   return x;
 }
 
-__global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(const KvEvictArgs a) {
-  __shared__ uint32_t bins[kBins];
-  __shared__ uint32_t part[2][kSelectWaves];
-  __shared__ uint32_t found[2];    // a digit, and how many are still wanted of those that have it
-  const int b = blockIdx.x / a.heads, head = blockIdx.x - b * a.heads;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = kv_length(a, b);
-  int32_t* const kept = a.kept + (int64_t)blockIdx.x * a.budget;
-  const float* const weights = a.weights + (int64_t)blockIdx.x * ((int64_t)a.max_pages << a.lps);
-  float* const out = a.new_weights ? a.new_weights + (int64_t)blockIdx.x * ((int64_t)a.new_max_pages << a.lps) : nullptr;
-  if (head == 0 && tid == 0) a.new_kv_len[b] = n < a.budget ? n : a.budget;
-  if (n <= a.budget) {
-    for (int i = tid; i < a.budget; i += kSelectThreads) {
-      kept[i] = i < n ? i : -1;
-      if (out && i < n) out[i] = weights[i];
-    }
-    return;
+constexpr int digit_bits(int digit) { return digit == 2 ? 10 : 11; }
+constexpr int digit_shift(int digit) { return digit == 0 ? 21 : digit == 1 ? 10 : 0; }
+
+// What a (sequence, key head) is asked for: tokens [lo, hi) of n are chosen from, `want` of them; those around stay.
+struct Choice {
+  int b, head, n, lo, hi;
+  uint32_t want;
+  int32_t* kept;
+  const float* weights;     // begins at a multiple of 16 floats
+  float* out;               // new weights, or null
+};
+__device__ __forceinline__ Choice row_of(const KvEvictArgs& a, int row) {
+  Choice r;
+  r.b = row / a.heads;
+  r.head = row - r.b * a.heads;
+  r.n = kv_length(a, r.b);
+  r.lo = a.first;
+  r.hi = r.n - a.recent;
+  r.want = a.budget - a.first - a.recent;
+  r.kept = a.kept + (int64_t)row * a.budget;
+  r.weights = a.weights + (int64_t)row * ((int64_t)a.max_pages << a.lps);
+  r.out = a.new_weights ? a.new_weights + (int64_t)row * ((int64_t)a.new_max_pages << a.lps) : nullptr;
+  return r;
+}
+
+// A row within the budget: everything stays. Places i0, i0 + step, ..
+__device__ __forceinline__ void keep_all(const KvEvictArgs& a, const Choice& r, int i0, int step) {
+  for (int i = i0; i < a.budget; i += step) {
+    r.kept[i] = i < r.n ? i : -1;
+    if (r.out && i < r.n) r.out[i] = r.weights[i];
   }
-  // Tokens [lo, hi) are chosen from, `want` of them; those around stay. Rows begin at multiples of 16 floats.
-  const int lo = a.first, hi = n - a.recent;
-  uint32_t want = a.budget - a.first - a.recent;
-  uint32_t prefix = 0, edge = 0;
-  const bool choose = want > 0;     // the same for the whole workgroup
-  if (choose) {
-    for (int digit = 0; digit < 3; digit++) {
-      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
-      __syncthreads();
-      for (int base = 0; base < hi; base += 4 * kSelectThreads) {
-        const int j = base + 4 * tid;
-        f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (j < hi) w = *reinterpret_cast<const f32x4u*>(weights + j);   // up to 3 past hi: within the row
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const uint32_t key = order_key(w[e]);
-          const bool in = j + e >= lo && j + e < hi && (digit == 0 || key >> (shift + bits) == prefix);
-          const uint32_t bin = key >> shift & ((1u << bits) - 1);
-          // Lanes that meet the first lane's counter add to it together: weights of one size, zeros above all.
-          const uint64_t active = __ballot(in);
-          if (active == 0) continue;
-          const int leader = __builtin_ctzll(active);
-          const uint32_t same = __shfl(bin, leader, 64);
-          const uint64_t with = __ballot(in && bin == same);
-          if (lane == leader) atomicAdd(&bins[same], (uint32_t)__builtin_popcountll(with));
-          if (in && bin != same) atomicAdd(&bins[bin], 1u);
-        }
-      }
-      __syncthreads();
-      // The counter, from the top, in which the want-th lies: thread t has the counters 2047 - 2t and the next.
-      const uint32_t c0 = bins[kBins - 1 - 2 * tid], c1 = bins[kBins - 2 - 2 * tid];
-      const uint32_t incl = wave_scan(c0 + c1, lane);
-      if (lane == 63) part[0][wave] = incl;
-      __syncthreads();
-      uint32_t before = incl - c0 - c1;
-      for (int v = 0; v < wave; v++) before += part[0][v];
-      if (before < want && before + c0 >= want) {
-        found[0] = kBins - 1 - 2 * tid;
-        found[1] = want - before;
-      } else if (before + c0 < want && before + c0 + c1 >= want) {
-        found[0] = kBins - 2 - 2 * tid;
-        found[1] = want - before - c0;
-      }
-      __syncthreads();
-      prefix = digit == 0 ? found[0] : prefix << bits | found[0];
-      want = found[1];
-      __syncthreads();
-    }
-    edge = prefix;
-  }
-  // In order: what lies around, what is above the edge, and the first `want` beside it.
-  uint32_t above_so_far = 0, beside_so_far = 0;
-  for (int base = 0; base < n; base += 4 * kSelectThreads) {
+}
+
+// How many of the tokens [begin, end) (begin a multiple of 4) that are chosen from, and whose digits before are
+// `prefix`, have each value of a digit. Ends with every counter written.
+__device__ __forceinline__ void count_digit(const Choice& r, int begin, int end, int digit, uint32_t prefix, uint32_t* bins) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int shift = digit_shift(digit), bits = digit_bits(digit);
+  end = end < r.hi ? end : r.hi;
+  for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
+  __syncthreads();
+  for (int base = begin; base < end; base += 4 * kSelectThreads) {
     const int j = base + 4 * tid;
     f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j < n) w = *reinterpret_cast<const f32x4u*>(weights + j);
-    uint32_t above = 0, beside = 0;    // a bit a token
+    if (j < end) w = *reinterpret_cast<const f32x4u*>(r.weights + j);   // up to 3 past the end: within the row
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const uint32_t key = order_key(w[e]);
-      const bool around = j + e < lo || j + e >= hi;
-      if (j + e < n && (around || (choose && key > edge))) above |= 1u << e;
-      if (j + e < n && !around && choose && key == edge) beside |= 1u << e;
+      const bool in = j + e >= r.lo && j + e < end && (digit == 0 || key >> (shift + bits) == prefix);
+      const uint32_t bin = key >> shift & ((1u << bits) - 1);
+      // Lanes that meet the first lane's counter add to it together: weights of one size, zeros above all.
+      const uint64_t active = __ballot(in);
+      if (active == 0) continue;
+      const int leader = __builtin_ctzll(active);
+      const uint32_t same = __shfl(bin, leader, 64);
+      const uint64_t with = __ballot(in && bin == same);
+      if (lane == leader) atomicAdd(&bins[same], (uint32_t)__builtin_popcountll(with));
+      if (in && bin != same) atomicAdd(&bins[bin], 1u);
     }
-    const uint32_t counts = (uint32_t)__builtin_popcount(above) | (uint32_t)__builtin_popcount(beside) << 16;
+  }
+  __syncthreads();
+}
+
+// The digit, from the top, in which the want-th token lies, and the count still wanted of it, into found[0 .. 1].
+// Thread t has the counters c0 of 2047 - 2t and c1 of the next. Ends with found written.
+__device__ __forceinline__ void find_digit(uint32_t c0, uint32_t c1, uint32_t want, uint32_t* part, uint32_t* found) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t incl = wave_scan(c0 + c1, lane);
+  if (lane == 63) part[wave] = incl;
+  __syncthreads();
+  uint32_t before = incl - c0 - c1;
+  for (int v = 0; v < wave; v++) before += part[v];
+  if (before < want && before + c0 >= want) {
+    found[0] = kBins - 1 - 2 * tid;
+    found[1] = want - before;
+  } else if (before + c0 < want && before + c0 + c1 >= want) {
+    found[0] = kBins - 2 - 2 * tid;
+    found[1] = want - before - c0;
+  }
+  __syncthreads();
+}
+
+// The tokens [begin, end) that stay, in order: what lies around, what is above the edge, and the first `want` of the
+// row beside it. `above` and `beside` tokens of each kind lie before them. part: 2 * kSelectWaves numbers.
+__device__ __forceinline__ void write_kept(const Choice& r, int begin, int end, bool choose, uint32_t edge, uint32_t want, uint32_t above,
+                                           uint32_t beside, uint32_t* part) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int turn = 0;
+  for (int base = begin; base < end; base += 4 * kSelectThreads, turn ^= kSelectWaves) {
+    const int j = base + 4 * tid;
+    f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (j < end) w = *reinterpret_cast<const f32x4u*>(r.weights + j);
+    uint32_t is_above = 0, is_beside = 0;    // a bit a token
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const uint32_t key = order_key(w[e]);
+      const bool around = j + e < r.lo || j + e >= r.hi;
+      if (j + e < end && (around || (choose && key > edge))) is_above |= 1u << e;
+      if (j + e < end && !around && choose && key == edge) is_beside |= 1u << e;
+    }
+    const uint32_t counts = (uint32_t)__builtin_popcount(is_above) | (uint32_t)__builtin_popcount(is_beside) << 16;
     const uint32_t incl = wave_scan(counts, lane);    // at most 256 in each half
-    if (lane == 63) part[(base / (4 * kSelectThreads)) & 1][wave] = incl;
+    if (lane == 63) part[turn + wave] = incl;
     __syncthreads();    // (the other half of `part` is read by nobody any more at the next write of this one)
     uint32_t total = 0, ahead = incl - counts;
     for (int v = 0; v < kSelectWaves; v++) {
-      const uint32_t x = part[(base / (4 * kSelectThreads)) & 1][v];
+      const uint32_t x = part[turn + v];
       if (v < wave) ahead += x;
       total += x;        // at most 4096 in each half
     }
-    uint32_t up = above_so_far + (ahead & 0xFFFFu), at_edge = beside_so_far + (ahead >> 16);
+    uint32_t up = above + (ahead & 0xFFFFu), at_edge = beside + (ahead >> 16);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      const bool is_above = above >> e & 1, is_beside = beside >> e & 1;
-      if (is_above || (is_beside && at_edge < want)) {
+      const bool has = is_above >> e & 1, edges = is_beside >> e & 1;
+      if (has || (edges && at_edge < want)) {
         const uint32_t at = up + (at_edge < want ? at_edge : want);
-        kept[at] = j + e;
-        if (out) out[at] = w[e];
+        r.kept[at] = j + e;
+        if (r.out) r.out[at] = w[e];
       }
-      up += is_above;
-      at_edge += is_beside;
+      up += has;
+      at_edge += edges;
     }
-    above_so_far += total & 0xFFFFu;
-    beside_so_far += total >> 16;
+    above += total & 0xFFFFu;
+    beside += total >> 16;
+  }
+}
+
+__global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(const KvEvictArgs a) {
+  __shared__ uint32_t bins[kBins], part[2 * kSelectWaves], found[2];
+  const int tid = threadIdx.x;
+  const Choice r = row_of(a, blockIdx.x);
+  if (r.head == 0 && tid == 0) a.new_kv_len[r.b] = r.n < a.budget ? r.n : a.budget;
+  if (r.n <= a.budget) return keep_all(a, r, tid, kSelectThreads);
+  uint32_t want = r.want, prefix = 0;
+  const bool choose = want > 0;     // the same for the whole workgroup
+  if (choose) {
+    for (int digit = 0; digit < 3; digit++) {
+      count_digit(r, 0, r.n, digit, prefix, bins);
+      find_digit(bins[kBins - 1 - 2 * tid], bins[kBins - 2 - 2 * tid], want, part, found);
+      prefix = digit == 0 ? found[0] : prefix << digit_bits(digit) | found[0];
+      want = found[1];
+      __syncthreads();
+    }
+  }
+  write_kept(r, 0, r.n, choose, prefix, want, 0, 0, part);
+}
+
+// The same by a.parts workgroups a row and one launch for each of 0, 1, 2: counting a digit, and 3: writing. Each
+// launch adds the parts' counters of the digit before up and finds it, every workgroup for itself. A row's scratch:
+//   [2][2]          digits so far and count still wanted, after digit 0 and 1
+//   [2][parts]      tokens of each part above those digits
+//   [parts][2048], [parts][2048], [parts][1024]   counters
+__host__ __device__ constexpr int64_t scratch_words(int parts) { return 4 + (int64_t)parts * (2 + 2 * kBins + kBins / 2); }
+
+template <int STAGE>
+__global__ __launch_bounds__(kSelectThreads) void evict_part_kernel(const KvEvictArgs a) {
+  __shared__ uint32_t bins[kBins], part[2 * kSelectWaves], found[2], sums[kSelectWaves], edges;
+  const int tid = threadIdx.x, parts = a.parts, row = blockIdx.x / parts, p = blockIdx.x - row * parts;
+  const Choice r = row_of(a, row);
+  if (STAGE == 3 && r.head == 0 && p == 0 && tid == 0) a.new_kv_len[r.b] = r.n < a.budget ? r.n : a.budget;
+  if (r.n <= a.budget) {
+    if (STAGE == 3) keep_all(a, r, p * kSelectThreads + tid, parts * kSelectThreads);
+    return;
+  }
+  const int size = ((r.n + parts - 1) / parts + 3) / 4 * 4;
+  const int64_t from = (int64_t)p * size;
+  const int begin = from < r.n ? (int)from : r.n, end = begin + size < r.n ? begin + size : r.n;
+  uint32_t* const scratch = a.scratch + row * scratch_words(parts);
+  uint32_t *const state = scratch, *const tally = scratch + 4, *const counters = tally + 2 * parts;
+  uint32_t want = r.want, prefix = 0, above = 0, beside = 0;
+  const bool choose = want > 0;
+  if (choose && STAGE > 0) {
+    constexpr int kDigit = STAGE - 1, kSize = 1 << digit_bits(kDigit);
+    if (kDigit > 0) {
+      prefix = state[2 * (kDigit - 1)];
+      want = state[2 * (kDigit - 1) + 1];
+    }
+    const uint32_t* const all = counters + (int64_t)kDigit * parts * kBins;
+    const int at = kBins - 2 - 2 * tid;       // c[1] counts digit at + 1, c[0] digit at
+    u32x2 c = {0u, 0u}, mine = {0u, 0u};      // mine: of this part; at the last digit of all before it
+    if (at < kSize) {
+#pragma unroll 8
+      for (int q = 0; q < parts; q++) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(all + q * kSize + at);
+        c += x;
+        if (STAGE == 3 ? q < p : q == p) mine += x;
+      }
+    }
+    find_digit(c[1], c[0], want, part, found);
+    const int digit = found[0];
+    prefix = kDigit == 0 ? digit : prefix << digit_bits(kDigit) | digit;
+    want = found[1];
+    uint32_t mine_above = (at + 1 > digit ? mine[1] : 0u) + (at > digit ? mine[0] : 0u);
+    if (STAGE == 3 && tid < p) mine_above += tally[parts + tid];       // (at most 32 parts)
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) mine_above += __shfl_xor(mine_above, m, 64);
+    if ((tid & 63) == 0) sums[tid >> 6] = mine_above;
+    if (STAGE == 3 && (at == digit || at + 1 == digit)) edges = at == digit ? mine[0] : mine[1];
+    __syncthreads();
+    for (int v = 0; v < kSelectWaves; v++) above += sums[v];
+    if (STAGE == 3) {
+      beside = edges;
+    } else if (tid == 0) {
+      tally[kDigit * parts + p] = above + (kDigit > 0 ? tally[(kDigit - 1) * parts + p] : 0u);
+      if (p == 0) {
+        state[2 * kDigit] = prefix;
+        state[2 * kDigit + 1] = want;
+      }
+    }
+  }
+  if constexpr (STAGE < 3) {
+    if (!choose) return;
+    constexpr int kSize = 1 << digit_bits(STAGE);
+    count_digit(r, begin, end, STAGE, prefix, bins);
+    uint32_t* const out = counters + (int64_t)STAGE * parts * kBins + p * kSize;
+    for (int i = tid; i < kSize; i += kSelectThreads) out[i] = bins[i];
+  } else {
+    above += (begin < r.lo ? begin : r.lo) + (begin > r.hi ? begin - r.hi : 0);     // those around before this part
+    write_kept(r, begin, end, choose, prefix, want, above, beside, part);
   }
 }
 
@@ -244,8 +362,27 @@ __global__ __launch_bounds__(256) void evict_move_kernel(const KvEvictArgs a) {
 
 int64_t kv_evict_chunks(int budget) { return (budget + kMoveTokens - 1) / kMoveTokens; }
 
+KvEvictPlan plan_kv_evict(int64_t groups, int64_t span) {
+  KvEvictPlan p = {1, 0};
+  if (groups < 1) return p;
+  const int64_t most = kSelectGroups / groups, all = (span + kPartTokens - 1) / kPartTokens;
+  p.parts = (int)(most < all ? most : all);
+  if (p.parts > 32) p.parts = 32;
+  if (p.parts < 2) p.parts = 1;
+  if (p.parts > 1) p.workspace_bytes = (size_t)(groups * scratch_words(p.parts) * 4);
+  return p;
+}
+
 hipError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, hipStream_t stream) {
-  hipLaunchKernelGGL(evict_select_kernel, dim3((unsigned)(a.seqs * (int64_t)a.heads)), dim3(kSelectThreads), 0, stream, a);
+  const dim3 rows((unsigned)(a.seqs * (int64_t)a.heads * a.parts));
+  if (a.parts == 1) {
+    hipLaunchKernelGGL(evict_select_kernel, rows, dim3(kSelectThreads), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((evict_part_kernel<0>), rows, dim3(kSelectThreads), 0, stream, a);
+    hipLaunchKernelGGL((evict_part_kernel<1>), rows, dim3(kSelectThreads), 0, stream, a);
+    hipLaunchKernelGGL((evict_part_kernel<2>), rows, dim3(kSelectThreads), 0, stream, a);
+    hipLaunchKernelGGL((evict_part_kernel<3>), rows, dim3(kSelectThreads), 0, stream, a);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((int64_t)a.seqs * a.chunks * a.heads)), block(256);
