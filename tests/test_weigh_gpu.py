@@ -95,6 +95,28 @@ def test_rows_in_shares(kv, window):
     _check(d, _run(d))
 
 
+@pytest.mark.parametrize("window", [1, 59, 128, 129, 2000])
+@pytest.mark.parametrize("q", [1, 2, 50])
+def test_long_caches_and_short_windows(q, window):
+    """Whole ranges of tokens that no row attends to: what was there before, times keep."""
+    d = _call([q] * 3, [3000, 2048, 300], window=window, keep=0.5, seed=window)
+    _check(d, _run(d))
+    d["keep"] = 0.0
+    d["old"].fill_(float("nan"))
+    got = _run(d)
+    for b, n in enumerate(d["kv_len"]):
+        assert bool(got[b, :, n:].isnan().all()) and not bool(got[b, :, :n].isnan().any())
+        assert not bool(got[b, :, :max(n - q + 1 - window, 0)].any())
+
+
+@pytest.mark.parametrize("window", [0, 3000])
+def test_more_ranges_than_workgroups(window):
+    """Single tokens over a batch whose every workgroup walks over several ranges."""
+    kv = [9000 - 37 * i for i in range(20)]
+    d = _call([1] * 20, kv, dim=64, page=256, heads=4, group=2, window=window, seed=8)
+    _check(d, _run(d))
+
+
 @pytest.mark.parametrize("q", [1, 3, 20, 100])
 def test_what_was_there_before(q):
     """keep, and the places of the newest tokens, which hold anything."""

@@ -15,15 +15,16 @@
 // of 16, which the workgroup's four waves (four ranges of tokens) share through LDS.
 //   Few rows (a decode step): bound by the K codes' bytes and the latency of reaching them through the page table.
 //   The workgroup rotates the queries itself, once for all its ranges, and loads the next range's codes before it
-//   works on one. 64 sequences of 8192 tokens, 8 heads of 128, 4-bit codes: 67 us, 2.6 TB/s. KT = 2 and 4096
-//   workgroups; 72 us with KT = 4 (184 registers, half the waves), 79 us with one range a workgroup.
+//   works on one; ranges in front of every row's window take no loads. 64 sequences of 8192 tokens, 8 heads of 128,
+//   4-bit codes: 67 us, 2.6 TB/s. KT = 2 and 4096 workgroups; 72 us with KT = 4 (184 registers, half the waves),
+//   79 us with one range a workgroup.
 //   Many: bound by the matrix instructions (two a product), and one exponential for each pair beside them. Queries are
 //   rotated once, by weigh_query_kernel, into operand order. Chunks of 2048 rows over 9000 tokens, 32 heads over 8 of
-//   128, four sequences: 465 us a call, 26 us of it the queries; the products, 504 GFLOP of fp16, take 403 us at the
-//   rate of a large library product. Rows are shared out until there are 6000 workgroups: with 1152 of them, of which 768 run at
-//   once, the second turn leaves half the card without work, 636 us. Weights of one tile computed between the next
-//   one's products, a barrier for two tiles, a higher priority while products run: no gain. 128 registers instead of
-//   150, for a fourth workgroup on a CU, with operands read one step ahead: 512 us.
+//   128, four sequences: 470 us a call, 26 us of it the queries; the products, 504 GFLOP of fp16, take 403 us at the
+//   rate of a large library product. Rows are shared out until there are 6000 workgroups (520 us with 3000): with 1152
+//   of them, of which 768 run at once, the second turn leaves half the card without work, 636 us. Weights of one tile
+//   computed between the next one's products, a barrier for two tiles, a higher priority while products run: no gain.
+//   128 registers instead of 150, for a fourth workgroup on a CU, with operands read one step ahead: 512 us.
 #include "kv_common.h"
 #include "kv_query.h"
 
@@ -298,6 +299,9 @@ __device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at
   }
 }
 
+// Shares of the query rows: the most, and the fewest tiles of one. (One sequence of 2844 tokens, 16 heads over one: 198 us
+// with 16 shares, 78 with 64; 4 or 16 tiles change calls of a few hundred rows by a tenth either way.)
+constexpr int kMostShares = 64, kLeastTiles = 8;
 constexpr int kFewTiles = 2;   // query tiles that a workgroup makes itself
 
 // Few query rows: the workgroup makes the query tiles once and walks over its ranges of tokens (number `split`
@@ -318,6 +322,13 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
   const int r = lane & 15, g = lane >> 4;
   const int rows = rows_of(a, s), before = s.kv_len - s.q_len, tiles = (rows + kRows - 1) / kRows;   // at most kFewTiles
   const ConstTable table = const_table(a.pages) + (int64_t)at.seq * a.max_pages;
+  // Tokens before lo are outside every row's window: ranges of them take no part but in what was there before.
+  const int lo = a.causal && a.window > 0 && before + 1 - a.window > 0 ? before + 1 - a.window : 0;
+  for (; base < s.kv_len && base + kKeys <= lo; base += step) {
+    float none[KT] = {};
+    write_sums<KT>(w, at, s, static_cast<int>(base) + wave * (KT * 16), 0, r, g, none);
+  }
+  if (base >= s.kv_len) return;
   Raw<D, BITS, KT> next;
   load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, static_cast<int>(base) + wave * (KT * 16), r, g, next);
   for (int tile = 0; tile < tiles; tile++) make_query_tile<D, BITS>(a, s, at.head, tile * kRows, rows, lds + tile * Q::kBytes);
@@ -382,8 +393,6 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
 
   for (int64_t base = (int64_t)at.split * kKeys; base < s.kv_len; base += (int64_t)a.splits * kKeys) {
     const int key0 = static_cast<int>(base), first = key0 + wave * (KT * 16);   // the workgroup's, the wave's
-    Raw<D, BITS, KT> raw;
-    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, first, r, g, raw);
     // The tiles of rows that attend to some token of the workgroup's range, and this workgroup's share.
     int t0 = 0, t1 = (rows + kRows - 1) / kRows;
     if (a.causal) {
@@ -403,14 +412,20 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
       t0 += at.tile * share;
       t1 = t0 + share < t1 ? t0 + share : t1;
     }
+    float sum[KT];
+#pragma unroll
+    for (int k = 0; k < KT; k++) sum[k] = 0.0f;
+    if (t0 >= t1) {   // the same for the whole workgroup
+      write_sums<KT>(w, at, s, first, 0, r, g, sum);
+      continue;
+    }
+    Raw<D, BITS, KT> raw;
+    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, first, r, g, raw);
 #pragma unroll
     for (int i = 0; i < kRing - 1; i++)
       if (t0 + i < t1) fetch(t0 + i, i);
     Keys<D, BITS, KT> key;
     convert_keys<D, BITS, KT>(a, raw, key);
-    float sum[KT];
-#pragma unroll
-    for (int k = 0; k < KT; k++) sum[k] = 0.0f;
     for (int tile = t0; tile < t1; tile++) {
       const int buffer = (tile - t0) % kRing;
       // This wave's part of the tile is there (those of the next two may be under way), then everybody's, and
@@ -451,6 +466,7 @@ __global__ __launch_bounds__(256) void weigh_join_kernel(const KvWeighArgs w) {
   for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < s.kv_len; j += (int64_t)gridDim.x * 256) {
     const int64_t out = (int64_t)blockIdx.y * span + j;
     float sum = 0.0f;
+#pragma unroll 8
     for (int t = 0; t < a.row_tiles; t++) sum += w.parts[t * w.part_stride + out];
     const bool had = w.keep != 0.0f && !(a.causal && j >= before);
     w.weights[out] = had ? __builtin_fmaf(w.keep, w.weights[out], sum) : sum;
@@ -501,9 +517,9 @@ KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int
   }
   p.row_splits = 1;
   if (p.many) {
-    const int64_t groups = p.splits * seqs * heads, want = (6000 + groups - 1) / groups, most = p.query_tiles_seq / 8;
+    const int64_t groups = p.splits * seqs * heads, want = (6000 + groups - 1) / groups, most = p.query_tiles_seq / kLeastTiles;
     p.row_splits = want < most ? want : most;
-    if (p.row_splits > 16) p.row_splits = 16;
+    if (p.row_splits > kMostShares) p.row_splits = kMostShares;
     if (p.row_splits < 1) p.row_splits = 1;
     p.query_bytes = ((total_q * group / kRows + seqs + 1) * heads * (head_dim / 32 * 2048 + 256) + 255) / 256 * 256;
     // Sums of each share for the whole page table: not where that is much.
