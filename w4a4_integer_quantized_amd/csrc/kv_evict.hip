@@ -5,7 +5,8 @@
 // evict_select_kernel: a workgroup a (sequence, key head). The weight of the last token that still fits
 // is found digit by digit (11, 11 and 10 bits of the weights as ordered integers, a histogram of 2048 counters in LDS for
 // each), then one pass in order writes the indices: everything above that weight, and of those beside it the
-// first. Counters are integers: the same choice every time. Few long rows are cut into parts (evict_part_kernel).
+// first. Counters are integers: the same choice every time. Bound by its vector instructions and its barriers: 22 us for
+// 512 rows of 8192. Few long rows are cut into parts (evict_part_kernel), each pass of which is bound by reading.
 // Weights kept in registers over the four passes: no gain (the instructions bound it, and there are fewer waves).
 // evict_move_kernel: bound by memory. Bytes are moved as they are. K rows and scales are copied; V bytes lie four
 // tokens side by side, so each four new tokens gather a byte from each of four old groups: a lone token
@@ -23,7 +24,7 @@ constexpr int kBins = 2048;
 constexpr int kMoveTokens = 64;   // new tokens of a move workgroup
 // A row's parts, and the workgroups that they come to. (32 rows of 131072 tokens: 137 us with one workgroup a row, whose
 // CU's vector instructions bound it; 40 with 256 in all, 46 with 512 and 71 with 1024, as every part reads every part's
-// counters. 512 rows of 8192: 29 us as they are, 60 in two parts each.)
+// counters. 512 rows of 8192: 22 us as they are, twice that in two parts each.)
 constexpr int kPartTokens = 4096, kSelectGroups = 256;
 
 typedef float f32x4u __attribute__((ext_vector_type(4)));
@@ -49,6 +50,20 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x, int lane) {
     x += lane >= m ? y : 0u;
   }
   return x;
+}
+
+// Bits of a wave's mask that lie before this lane.
+__device__ __forceinline__ uint32_t below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// Sum over the wave's first 16 lanes, for all of it.
+__device__ __forceinline__ uint32_t row16_sum(uint32_t x) {
+  x += __builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true);
+  x += __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);
+  x += __builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, true);
+  x += __builtin_amdgcn_mov_dpp((int)x, 0x128, 0xF, 0xF, true);
+  return __builtin_amdgcn_readfirstlane(x);
 }
 
 constexpr int digit_bits(int digit) { return digit == 2 ? 10 : 11; }
@@ -84,28 +99,38 @@ __device__ __forceinline__ void keep_all(const KvEvictArgs& a, const Choice& r, 
   }
 }
 
+// Weights of the tokens j .. j + 3, zeros from `end` on in steps of four (within the row all the same).
+__device__ __forceinline__ f32x4u four_weights(const Choice& r, int j, int end) {
+  f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (j < end) w = *reinterpret_cast<const f32x4u*>(r.weights + j);
+  return w;
+}
+
 // How many of the tokens [begin, end) (begin a multiple of 4) that are chosen from, and whose digits before are
 // `prefix`, have each value of a digit. Ends with every counter written.
 __device__ __forceinline__ void count_digit(const Choice& r, int begin, int end, int digit, uint32_t prefix, uint32_t* bins) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int shift = digit_shift(digit), bits = digit_bits(digit);
   end = end < r.hi ? end : r.hi;
+  f32x4u next = four_weights(r, begin + 4 * tid, end);
   for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
   __syncthreads();
   for (int base = begin; base < end; base += 4 * kSelectThreads) {
     const int j = base + 4 * tid;
-    f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j < end) w = *reinterpret_cast<const f32x4u*>(r.weights + j);   // up to 3 past the end: within the row
+    const f32x4u w = next;
+    next = four_weights(r, j + 4 * kSelectThreads, end);
+    const bool inner = base >= r.lo && base + 4 * kSelectThreads <= end;   // all of them are chosen from
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const uint32_t key = order_key(w[e]);
-      const bool in = j + e >= r.lo && j + e < end && (digit == 0 || key >> (shift + bits) == prefix);
+      bool in = digit == 0 || key >> (shift + bits) == prefix;
+      if (!inner) in = in && j + e >= r.lo && j + e < end;
       const uint32_t bin = key >> shift & ((1u << bits) - 1);
       // Lanes that meet the first lane's counter add to it together: weights of one size, zeros above all.
       const uint64_t active = __ballot(in);
       if (active == 0) continue;
       const int leader = __builtin_ctzll(active);
-      const uint32_t same = __shfl(bin, leader, 64);
+      const uint32_t same = __builtin_amdgcn_readlane(bin, leader);
       const uint64_t with = __ballot(in && bin == same);
       if (lane == leader) atomicAdd(&bins[same], (uint32_t)__builtin_popcountll(with));
       if (in && bin != same) atomicAdd(&bins[bin], 1u);
@@ -122,7 +147,7 @@ __device__ __forceinline__ void find_digit(uint32_t c0, uint32_t c1, uint32_t wa
   if (lane == 63) part[wave] = incl;
   __syncthreads();
   uint32_t before = incl - c0 - c1;
-  for (int v = 0; v < wave; v++) before += part[v];
+  before += row16_sum(lane < wave && lane < kSelectWaves ? part[lane] : 0u);
   if (before < want && before + c0 >= want) {
     found[0] = kBins - 1 - 2 * tid;
     found[1] = want - before;
@@ -139,29 +164,34 @@ __device__ __forceinline__ void write_kept(const Choice& r, int begin, int end, 
                                            uint32_t beside, uint32_t* part) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int turn = 0;
+  f32x4u next = four_weights(r, begin + 4 * tid, end);
   for (int base = begin; base < end; base += 4 * kSelectThreads, turn ^= kSelectWaves) {
     const int j = base + 4 * tid;
-    f32x4u w = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j < end) w = *reinterpret_cast<const f32x4u*>(r.weights + j);
-    uint32_t is_above = 0, is_beside = 0;    // a bit a token
+    const f32x4u w = next;
+    next = four_weights(r, j + 4 * kSelectThreads, end);
+    // A bit a token; and how many of each kind lie before this lane's in the wave (below) and in all of it.
+    uint32_t is_above = 0, is_beside = 0, up = above, at_edge = beside, wave_above = 0, wave_beside = 0;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const uint32_t key = order_key(w[e]);
       const bool around = j + e < r.lo || j + e >= r.hi;
-      if (j + e < end && (around || (choose && key > edge))) is_above |= 1u << e;
-      if (j + e < end && !around && choose && key == edge) is_beside |= 1u << e;
+      const bool has = j + e < end && (around || (choose && key > edge));
+      const bool edges = j + e < end && !around && choose && key == edge;
+      is_above |= has ? 1u << e : 0u;
+      is_beside |= edges ? 1u << e : 0u;
+      const uint64_t m = __ballot(has), n = __ballot(edges);
+      up += below(m);
+      wave_above += __builtin_popcountll(m);
+      at_edge += below(n);
+      wave_beside += __builtin_popcountll(n);
     }
-    const uint32_t counts = (uint32_t)__builtin_popcount(is_above) | (uint32_t)__builtin_popcount(is_beside) << 16;
-    const uint32_t incl = wave_scan(counts, lane);    // at most 256 in each half
-    if (lane == 63) part[turn + wave] = incl;
+    if (lane == 0) part[turn + wave] = wave_above | wave_beside << 16;      // at most 256 in each half
     __syncthreads();    // (the other half of `part` is read by nobody any more at the next write of this one)
-    uint32_t total = 0, ahead = incl - counts;
-    for (int v = 0; v < kSelectWaves; v++) {
-      const uint32_t x = part[turn + v];
-      if (v < wave) ahead += x;
-      total += x;        // at most 4096 in each half
-    }
-    uint32_t up = above + (ahead & 0xFFFFu), at_edge = beside + (ahead >> 16);
+    // Lane v holds wave v's numbers: sums over the waves before this one, and over all (at most 4096 in each half).
+    const uint32_t x = lane < kSelectWaves ? part[turn + lane] : 0u;
+    const uint32_t ahead = row16_sum(lane < wave ? x : 0u), total = row16_sum(x);
+    up += ahead & 0xFFFFu;
+    at_edge += ahead >> 16;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const bool has = is_above >> e & 1, edges = is_beside >> e & 1;
