@@ -11,7 +11,8 @@
 // evict_move_kernel: bound by memory. Bytes are moved as they are. K rows and scales are copied; V bytes lie four
 // tokens side by side, so each four new tokens gather a byte from each of four old groups: a lone token
 // that stays costs the reading of its whole group's V lines. 64 sequences of 8192 tokens to 2048, 8 heads of 128, 4-bit
-// codes: 93 us for 67 MB of K, 183 MB of V's groups of which some token stays, 16 MB of scales and 134 MB written: 4.3 TB/s.
+// codes: 71 us, 221 MB read and 122 MB written by the counters, 4.8 TB/s, what a large copy reaches. (93 us with each kind
+// loaded and stored before the next.)
 #include "kv_common.h"
 
 namespace convrot {
@@ -303,89 +304,97 @@ __global__ __launch_bounds__(kSelectThreads) void evict_part_kernel(const KvEvic
   }
 }
 
-// The head's block of a page of a table, or null.
-__device__ __forceinline__ uint8_t* block_of(const KvEvictArgs& a, const int32_t* table, int token, int head) {
+// Where the head's block of a page of a table begins in the cache, in bytes; -1: the page is not in it.
+__device__ __forceinline__ int64_t block_of(const KvEvictArgs& a, const int32_t* table, int token, int head) {
   const int pg = table[token >> a.lps];
-  return pg >= 0 && pg < a.num_pages ? a.cache + ((int64_t)pg * a.heads + head) * a.head_bytes : nullptr;
+  return pg >= 0 && pg < a.num_pages ? ((int64_t)pg * a.heads + head) * a.head_bytes : -1;
 }
 
-// New tokens [64 c, 64 c + 64) of a (sequence, key head). RB: bytes of a row of codes.
+// New tokens [64 c, 64 c + 64) of a (sequence, key head). RB: bytes of a row of codes. The places are looked up once, then
+// everything is loaded before anything is stored. (What comes from no page is loaded from the cache's first and replaced by
+// zeros: a load under a condition would be waited for on its own.)
 template <int RB>
 __global__ __launch_bounds__(256) void evict_move_kernel(const KvEvictArgs a) {
+  __shared__ int64_t from[kMoveTokens], to[kMoveTokens];   // blocks, or -1
+  __shared__ int places[kMoveTokens];                       // in the old page
   const int tid = threadIdx.x, page = 1 << a.lps;
   const int head = blockIdx.x % a.heads, rest = blockIdx.x / a.heads, chunk = rest % a.chunks, b = rest / a.chunks;
   const int n = kv_length(a, b), count = n < a.budget ? n : a.budget, i0 = chunk * kMoveTokens;
   if (i0 >= count) return;
-  const int32_t* const kept = a.kept + ((int64_t)b * a.heads + head) * a.budget;
-  const int32_t* const from = a.pages + (int64_t)b * a.max_pages;
-  const int32_t* const to = a.new_pages + (int64_t)b * a.new_max_pages;
-  // K rows: 16 bytes a thread.
-  constexpr int kPer = RB / 16;
-#pragma unroll
-  for (int job = tid; job < kMoveTokens * kPer; job += 256) {
-    const int i = i0 + job / kPer, at = job % kPer * 16;
+  if (tid < kMoveTokens) {
+    const int i = i0 + tid;
+    int64_t src = -1, dst = -1;
+    int place = 0;
     if (i < count) {
-      const int j = kept[i];
-      const uint8_t* src = block_of(a, from, j, head);
-      uint8_t* dst = block_of(a, to, i, head);
-      u32x4 x = {0u, 0u, 0u, 0u};
-      if (src) x = *reinterpret_cast<const u32x4*>(src + (j & (page - 1)) * RB + at);
-      if (dst) *reinterpret_cast<u32x4*>(dst + (i & (page - 1)) * RB + at) = x;
+      const int j = a.kept[((int64_t)b * a.heads + head) * a.budget + i];
+      dst = block_of(a, a.new_pages + (int64_t)b * a.new_max_pages, i, head);
+      src = block_of(a, a.pages + (int64_t)b * a.max_pages, j, head);
+      place = j & (page - 1);
+    }
+    from[tid] = src;
+    to[tid] = dst;
+    places[tid] = place;
+  }
+  __syncthreads();
+  const u32x4 zeros = {0u, 0u, 0u, 0u};
+  // K rows: 16 bytes a thread. V: four new tokens and four of their bytes. Scales: K's and V's, 64 of each.
+  constexpr int kPer = RB / 16, kQuads = RB / 4, kTurns = RB < 64 ? 1 : RB / 64;
+  u32x4 k[kTurns], v[kTurns][4];
+#pragma unroll
+  for (int t = 0; t < kTurns; t++) {
+    const int job = tid + 256 * t, i = job / kPer % kMoveTokens, at = job % kPer * 16;
+    const int64_t src = from[i];
+    k[t] = *reinterpret_cast<const u32x4*>(a.cache + (src < 0 ? 0 : src) + places[i] * RB + at);
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; t++) {
+    const int job = tid + 256 * t, i = job / kQuads * 4 % kMoveTokens, at = job % kQuads * 16;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int64_t src = from[i + e];
+      v[t][e] = *reinterpret_cast<const u32x4*>(a.cache + (src < 0 ? 0 : src) + page * RB + (places[i + e] >> 2) * (4 * RB) + at);
     }
   }
-  // V: four new tokens and four of their bytes a thread.
-  constexpr int kQuads = RB / 4;
+  const int si = tid & (kMoveTokens - 1), part = tid / kMoveTokens & 1;
+  const int64_t scales = from[si];
+  const uint32_t scale = *reinterpret_cast<const uint32_t*>(a.cache + (scales < 0 ? 0 : scales) + 2 * page * RB + (part * page + places[si]) * 4);
+  asm volatile("" ::: "memory");   // the loads stay in front of it
+
 #pragma unroll
-  for (int job = tid; job < kMoveTokens / 4 * kQuads; job += 256) {
-    const int i = i0 + job / kQuads * 4, at = job % kQuads * 16;
-    if (i < count) {
-      uint8_t* dst = block_of(a, to, i, head);
-      u32x4 x[4];
-      uint32_t sel[4], keep = 0;
+  for (int t = 0; t < kTurns; t++) {
+    const int job = tid + 256 * t, i = job / kPer, at = job % kPer * 16;
+    if (i < kMoveTokens && to[i] >= 0)
+      *reinterpret_cast<u32x4*>(a.cache + to[i] + ((i0 + i) & (page - 1)) * RB + at) = from[i] < 0 ? zeros : k[t];
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; t++) {
+    const int job = tid + 256 * t, i = job / kQuads * 4, at = job % kQuads * 16;
+    if (i < kMoveTokens && to[i] >= 0) {
+      u32x4* const p = reinterpret_cast<u32x4*>(a.cache + to[i] + page * RB + (((i0 + i) & (page - 1)) >> 2) * (4 * RB) + at);
+      uint32_t keep = 0, sel[4], there[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        x[e] = u32x4{0u, 0u, 0u, 0u};
-        sel[e] = 0;
-        if (i + e < count) {
-          const int j = kept[i + e], off = j & (page - 1);
-          const uint8_t* src = block_of(a, from, j, head);
-          if (src) x[e] = *reinterpret_cast<const u32x4*>(src + page * RB + (off >> 2) * (4 * RB) + at);
-          sel[e] = off & 3;
-        } else {
-          keep |= 0xFFu << (8 * e);    // past the last token: what is there stays
-        }
+        sel[e] = places[i + e] & 3;
+        there[e] = from[i + e] < 0 ? 0u : 0xFFu << (8 * e);
+        if (i0 + i + e >= count) keep |= 0xFFu << (8 * e);    // past the last token: what is there stays
       }
-      if (dst) {
-        u32x4* const p = reinterpret_cast<u32x4*>(dst + page * RB + ((i & (page - 1)) >> 2) * (4 * RB) + at);
-        u32x4 y, old = {0u, 0u, 0u, 0u};
-        if (keep) old = *p;
+      u32x4 y, old = zeros;
+      if (keep) old = *p;
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          uint32_t v = 0;
+      for (int c = 0; c < 4; c++) {
+        uint32_t x = old[c] & keep;
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const uint32_t word = x[e][c];
-            v |= (word >> (8 * sel[e]) & 0xFFu) << (8 * e);
-          }
-          const uint32_t was = old[c];
-          y[c] = (v & ~keep) | (was & keep);
+        for (int e = 0; e < 4; e++) {
+          const uint32_t word = v[t][e][c];
+          x |= (word >> (8 * sel[e]) & 0xFFu) << (8 * e) & there[e];
         }
-        *p = y;
+        y[c] = x;
       }
+      *p = y;
     }
   }
-  // Scales: K's and V's, 64 of each.
-  if (tid < 2 * kMoveTokens) {
-    const int i = i0 + (tid & (kMoveTokens - 1)), part = tid / kMoveTokens;
-    if (i < count) {
-      const int j = kept[i];
-      const uint8_t* src = block_of(a, from, j, head);
-      uint8_t* dst = block_of(a, to, i, head);
-      uint32_t x = 0;
-      if (src) x = *reinterpret_cast<const uint32_t*>(src + 2 * page * RB + (part * page + (j & (page - 1))) * 4);
-      if (dst) *reinterpret_cast<uint32_t*>(dst + 2 * page * RB + (part * page + (i & (page - 1))) * 4) = x;
-    }
-  }
+  if (tid < 2 * kMoveTokens && to[si] >= 0)
+    *reinterpret_cast<uint32_t*>(a.cache + to[si] + 2 * page * RB + (part * page + ((i0 + si) & (page - 1))) * 4) = scales < 0 ? 0u : scale;
 }
 
 }  // namespace
