@@ -17,7 +17,9 @@
 //   The workgroup rotates the queries itself, once for all its ranges, and loads the next range's codes before it
 //   works on one; ranges in front of every row's window take no loads. 64 sequences of 8192 tokens, 8 heads of 128,
 //   4-bit codes: 67 us, 2.6 TB/s. KT = 2 and 4096 workgroups; 72 us with KT = 4 (184 registers, half the waves),
-//   79 us with one range a workgroup.
+//   79 us with one range a workgroup. A wave's 32 tokens cost 276 vector instructions (half the time is their issue) and
+//   256 cycles of products. Two ranges ahead, or what was there before asked for ahead of the products: no gain, as the
+//   registers take a wave a SIMD.
 //   Many: bound by the matrix instructions (two a product), and one exponential for each pair beside them. Queries are
 //   rotated once, by weigh_query_kernel, into operand order. Chunks of 2048 rows over 9000 tokens, 32 heads over 8 of
 //   128, four sequences: 470 us a call, 26 us of it the queries; the products, 504 GFLOP of fp16, take 403 us at the
