@@ -14,12 +14,12 @@
 // A wave keeps KT times 16 tokens as fp16 operands, converted once, and walks over the query rows in tiles
 // of 16, which the workgroup's four waves (four ranges of tokens) share through LDS.
 //   Few rows (a decode step): bound by the K codes' bytes and the latency of reaching them through the page table.
-//   The workgroup rotates the queries itself, once for all its ranges, and loads the next range's codes before it
-//   works on one; ranges in front of every row's window take no loads. 64 sequences of 8192 tokens, 8 heads of 128,
-//   4-bit codes: 67 us, 2.6 TB/s. KT = 2 and 4096 workgroups; 72 us with KT = 4 (184 registers, half the waves),
-//   79 us with one range a workgroup. A wave's 32 tokens cost 276 vector instructions (half the time is their issue) and
-//   256 cycles of products. Two ranges ahead, or what was there before asked for ahead of the products: no gain, as the
-//   registers take a wave a SIMD.
+//   The workgroup rotates the queries itself, once for all its ranges, and loads the next range's codes, and the sums
+//   that were there before, ahead of its work on one; ranges in front of every row's window take no loads. 64 sequences
+//   of 8192 tokens, 8 heads of 128, 4-bit codes: 62 us, 2.8 TB/s. 79 us with one range a workgroup, 65 with the sums
+//   before read when they are needed, 68 with operands read four steps ahead and three waves a SIMD, 72 with KT = 4
+//   (two waves), 67 with two ranges ahead. A wave's 32 tokens cost 220 vector instructions and 256 cycles of products, and
+//   half the time is their issue.
 //   Many: bound by the matrix instructions (two a product), and one exponential for each pair beside them. Queries are
 //   rotated once, by weigh_query_kernel, into operand order. Chunks of 2048 rows over 9000 tokens, 32 heads over 8 of
 //   128, four sequences: 470 us a call, 26 us of it the queries; the products, 504 GFLOP of fp16, take 403 us at the
@@ -59,6 +59,23 @@ __device__ __forceinline__ void make_query_tile(const KvAttentionArgs& a, const 
   const int u = threadIdx.x % R::kLanes, chunk = chunk_of_lane(u), row = threadIdx.x / R::kLanes;
   const int n = n0 + row;
   const bool there = row < kRows && n < rows;
+  float* const info = reinterpret_cast<float*>(dst + QueryTile<D>::kWords);
+  if (__ballot(there) == 0) {   // none of this wave's rows
+    if (row >= kRows) return;
+#pragma unroll
+    for (int k = 0; k < R::kChunks; k++) {
+      constexpr int kPer = G::kLoad / BITS;
+      const int ch = k * 16 + chunk, op = ch / (4 * kPer) * kPer + ch % kPer, g = ch % (4 * kPer) / kPer;
+      uint8_t* p = dst + op * 2048 + (g * 16 + row) * 16;
+      *reinterpret_cast<u32x4*>(p) = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(p + 1024) = u32x4{0u, 0u, 0u, 0u};
+    }
+    if (u == 0) {
+      info[row] = __builtin_inff();
+      info[16 + row] = 1.0f;
+    }
+    return;
+  }
   const int token = there ? token_of(a, n) : 0, qh = head * a.group + (there ? n - token * a.group : 0);
   const uint8_t* x = a.q + ((s.q0 + token) * a.q_token + qh * a.q_head) * 2;
   const float lse = there ? a.lse[(int64_t)(s.q0 + token) * a.q_heads + qh] : __builtin_inff();
@@ -94,7 +111,6 @@ __device__ __forceinline__ void make_query_tile(const KvAttentionArgs& a, const 
     *reinterpret_cast<u32x4*>(p + 1024) = u32x4{w[0], w[1], w[2], w[3]};
   }
   if (u == 0) {
-    float* info = reinterpret_cast<float*>(dst + QueryTile<D>::kWords);
     info[row] = ok ? lse * kLog2e : __builtin_inff();
     info[16 + row] = kCommon / up;
   }
@@ -186,11 +202,11 @@ __device__ __forceinline__ void convert_keys(const KvAttentionArgs& a, const Raw
   }
 }
 
-// The products of a tile of queries at `q` (LDS) with a wave's keys. Operands are read four steps at a time, ahead of
-// the products: read one by one, each waits for LDS.
-template <int D, int BITS, int KT>
+// The products of a tile of queries at `q` (LDS) with a wave's keys. Operands are read AHEAD steps at a time, ahead of
+// the products: read one by one, each waits for LDS. (Few rows: 2, which leaves registers for a fourth wave a SIMD.)
+template <int D, int BITS, int KT, int AHEAD>
 __device__ __forceinline__ void multiply(const uint8_t* q, const Keys<D, BITS, KT>& key, int lane, f32x4 (&acc)[KT]) {
-  constexpr int kAhead = D / 32 < 4 ? D / 32 : 4;
+  constexpr int kAhead = D / 32 < AHEAD ? D / 32 : AHEAD;
 #pragma unroll
   for (int k = 0; k < KT; k++) acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -276,10 +292,23 @@ __device__ __forceinline__ void add_weights(const KvAttentionArgs& a, const Seq&
   for (int k = 0; k < KT; k++) sum[k] += (p[k][0] + p[k][1]) + (p[k][2] + p[k][3]);
 }
 
+// What was there before for the token that a lane will write (see write_sums); zero where it does not count. (Loaded from
+// somewhere in any case: a load under a condition is waited for at once.)
+template <int KT>
+__device__ __forceinline__ bool had_before(const KvWeighArgs& w, const Seq& s, int first, int r, int g) {
+  const int j = first + 16 * g + r;
+  return w.a.row_tiles == 1 && w.keep != 0.0f && g < KT && j < s.kv_len && !(w.a.causal && j >= s.kv_len - s.q_len);
+}
+template <int KT>
+__device__ __forceinline__ float load_before(const KvWeighArgs& w, const Place& at, const Seq& s, int first, int r, int g) {
+  const float* row = w.weights + ((int64_t)at.seq * w.a.heads + at.head) * ((int64_t)w.a.max_pages << w.a.lps);
+  return row[had_before<KT>(w, s, first, r, g) ? first + 16 * g + r : 0];
+}
+
 // Over the four lanes of a token; then lane (r, g) writes token r of step g.
 template <int KT>
 __device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at, const Seq& s, int first, uint32_t there, int r, int g,
-                                           const float (&sum)[KT]) {
+                                           float before, const float (&sum)[KT]) {
   const KvAttentionArgs& a = w.a;
   float mine = 0.0f;
 #pragma unroll
@@ -292,12 +321,10 @@ __device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at
   const int j = first + 16 * g + r;
   if (g < KT && j < s.kv_len) {
     const int64_t out = ((int64_t)at.seq * a.heads + at.head) * ((int64_t)a.max_pages << a.lps) + j;
-    if (a.row_tiles > 1) {
+    if (a.row_tiles > 1)
       w.parts[at.tile * w.part_stride + out] = mine;
-    } else {
-      const bool had = w.keep != 0.0f && !(a.causal && j >= s.kv_len - s.q_len);
-      w.weights[out] = had ? __builtin_fmaf(w.keep, w.weights[out], mine) : mine;
-    }
+    else
+      w.weights[out] = had_before<KT>(w, s, first, r, g) ? __builtin_fmaf(w.keep, before, mine) : mine;
   }
 }
 
@@ -328,11 +355,19 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
   const int lo = a.causal && a.window > 0 && before + 1 - a.window > 0 ? before + 1 - a.window : 0;
   for (; base < s.kv_len && base + kKeys <= lo; base += step) {
     float none[KT] = {};
-    write_sums<KT>(w, at, s, static_cast<int>(base) + wave * (KT * 16), 0, r, g, none);
+    const int first = static_cast<int>(base) + wave * (KT * 16);
+    write_sums<KT>(w, at, s, first, 0, r, g, load_before<KT>(w, at, s, first, r, g), none);
   }
   if (base >= s.kv_len) return;
+  // A range's codes and what was there before; past the last range the last again.
   Raw<D, BITS, KT> next;
-  load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, static_cast<int>(base) + wave * (KT * 16), r, g, next);
+  float next_was;
+  auto load = [&](int64_t at_base) __attribute__((always_inline)) {
+    const int first = static_cast<int>(at_base < s.kv_len ? at_base : base) + wave * (KT * 16);
+    next_was = load_before<KT>(w, at, s, first, r, g);
+    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, first, r, g, next);
+  };
+  load(base);
   for (int tile = 0; tile < tiles; tile++) make_query_tile<D, BITS>(a, s, at.head, tile * kRows, rows, lds + tile * Q::kBytes);
   __syncthreads();
   for (; base < s.kv_len; base += step) {
@@ -340,9 +375,8 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
     Keys<D, BITS, KT> key;
     convert_keys<D, BITS, KT>(a, next, key);
     const uint32_t there = next.there;
-    // (Past the last range this one is loaded again: a load under a condition is waited for at once.)
-    const int64_t ahead = base + step < s.kv_len ? base + step : base;
-    load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, static_cast<int>(ahead) + wave * (KT * 16), r, g, next);
+    const float was = next_was;
+    load(base + step);
     float sum[KT];
 #pragma unroll
     for (int k = 0; k < KT; k++) sum[k] = 0.0f;
@@ -354,11 +388,11 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
       asm volatile("" : "+s"(all), "+s"(common));   // settled before the products
       f32x4 acc[KT];
       float p[KT][4];
-      multiply<D, BITS, KT>(q, key, lane, acc);
+      multiply<D, BITS, KT, 2>(q, key, lane, acc);
       weights_of<KT>(acc, info, common, key.factor, p);
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
-    write_sums<KT>(w, at, s, first, there, r, g, sum);
+    write_sums<KT>(w, at, s, first, there, r, g, was, sum);
   }
 }
 
@@ -418,7 +452,7 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
 #pragma unroll
     for (int k = 0; k < KT; k++) sum[k] = 0.0f;
     if (t0 >= t1) {   // the same for the whole workgroup
-      write_sums<KT>(w, at, s, first, 0, r, g, sum);
+      write_sums<KT>(w, at, s, first, 0, r, g, load_before<KT>(w, at, s, first, r, g), sum);
       continue;
     }
     Raw<D, BITS, KT> raw;
@@ -449,12 +483,12 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
       asm volatile("" : "+s"(all), "+s"(common));
       f32x4 acc[KT];
       float p[KT][4];
-      multiply<D, BITS, KT>(q, key, lane, acc);
+      multiply<D, BITS, KT, 4>(q, key, lane, acc);
       weights_of<KT>(acc, info, common, key.factor, p);
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
     __syncthreads();   // the buffers are done with before the next range's first copy
-    write_sums<KT>(w, at, s, first, raw.there, r, g, sum);
+    write_sums<KT>(w, at, s, first, raw.there, r, g, load_before<KT>(w, at, s, first, r, g), sum);
   }
 }
 
