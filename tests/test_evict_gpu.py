@@ -217,3 +217,26 @@ def test_offsets_past_32_bits():
     kept, _ = rq.kv_evict(big, move(d["pages"]), _ints(d["kv_len"]), torch.from_numpy(d["weights"]).cuda(), d["cfg"], 300,
                           move(d["new_pages"]), first=4, recent=30)
     assert torch.equal(kept, want) and torch.equal(big[torch.from_numpy(at).cuda()], small)
+
+
+def test_weights_past_4_gib():
+    """A page table of 2^28 tokens: a head's weights, and the places kept, by the parts of a row and past 32 bits of bytes."""
+    d = _case([1000], 300, dim=64, page=256, heads=8, seed=10, spare=1)
+    _, want, _ = _check(d, first=4, recent=30)
+    wide = torch.full((1, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    wide[:, :d["pages"].shape[1]] = _ints(d["pages"])
+    W = torch.zeros(1, 8, 1 << 28, device="cuda")
+    W[:, :, :d["weights"].shape[2]] = torch.from_numpy(d["weights"]).cuda()
+    cache = torch.from_numpy(d["raw"]).cuda()
+    kept, n = rq.kv_evict(cache, wide, _ints([1000]), W, d["cfg"], 300, _ints(d["new_pages"]), first=4, recent=30)
+    assert torch.equal(kept, want) and n.tolist() == [300]
+    raw, _, _ = evict_ref.evict(d["raw"], 8, 256, d["row"], d["pages"], [1000], d["weights"], 300, d["new_pages"], 4, 30)
+    assert np.array_equal(cache.cpu().numpy(), raw)
+
+
+def test_sequences_that_share_pages():
+    """A prefix that several sequences have in the same pages is copied for each."""
+    d = _case([300, 250, 90], 64, page=16, seed=12)
+    d["pages"][1, :8] = d["pages"][0, :8]
+    d["pages"][2, :3] = d["pages"][0, :3]
+    _check(d, first=4, recent=10)

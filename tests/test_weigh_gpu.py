@@ -270,6 +270,35 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, want) and bool((out[:, :, :1000] > 0).any())
 
 
+@pytest.mark.parametrize("q", [3, 60])
+def test_weights_past_4_gib(q):
+    """A page table of 2^28 tokens: the last head's sums lie 7 GiB behind the first's."""
+    need_gpu()
+    cfg = rq.make_kv_cfg(8, 64, 256, 4)
+    c = evict_ref.Pages(6, 8, 64, 256, 4, seed=2)
+    Q = torch.randn(q, 16, 64, generator=torch.Generator("cuda").manual_seed(1), device="cuda").half()
+    few = torch.tensor([[1, 2, 5, 3]], dtype=torch.int32, device="cuda")
+    lse = evict_ref.logsums(c, Q, few, [1000], [0, q], True, 0, 64 ** -0.5).float()
+    want = torch.zeros(1, 8, 1024, device="cuda")
+    rq.kv_attention_weights(Q, lse, c.bytes, few, _ints([1000]), cfg, want, max_kv_len=1000)
+    table = torch.full((1, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    table[:, :4] = few
+    out = torch.zeros(1, 8, 1 << 28, device="cuda")
+    rq.kv_attention_weights(Q, lse, c.bytes, table, _ints([1000]), cfg, out, max_kv_len=1000)
+    # (The rows may be shared out otherwise: sums of at most 2 q weights of at most 1 in another order.)
+    assert float((out[:, :, :1024] - want).abs().max()) <= 2 * q * 2 * q * 2.0 ** -24 and bool((want[:, :, :1000] > 0).any())
+    assert not bool(out[:, :, 1000:].any())
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_sequences_that_share_pages(q):
+    d = _call([q] * 3, [300, 250, 90], page=16, keep=0.5, seed=12)
+    d["pages"][1, :8] = d["pages"][0, :8]
+    d["pages"][2, :3] = d["pages"][0, :3]
+    d["lse"] = evict_ref.logsums(d["c"], d["Q"], d["pages"], d["kv_len"], d["starts"], True, 0, d["scale"]).float()
+    _check(d, _run(d))
+
+
 @pytest.mark.parametrize("bits,dim,dtype", [(4, 128, "bf16"), (8, 64, "f16"), (4, 256, "f16")])
 def test_attention_weights_and_eviction_together(bits, dim, dtype):
     """A prompt written, attended to and weighed, brought down to a budget, and single tokens after that over
