@@ -83,6 +83,7 @@ def test_few_tokens_over_many_rows(M, N):
     need_gpu()
     _run(M, 640, N, 8, rq.RQ_X_TILED, "bf16", "silu")
     _run(M, 384, N, 4, rq.RQ_X_ROWS, "f16", "none")
+    _run(M, 384, N, 4, rq.RQ_X_FP6, "bf16", "gelu_tanh")
 
 
 @pytest.mark.parametrize("act", gated_ref.ACTS)

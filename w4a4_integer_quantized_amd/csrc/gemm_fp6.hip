@@ -312,11 +312,11 @@ hipError_t launch_gemm_fp6(const void* Xt, const float* sx, const void* Wt, cons
   return launch6<kOutBF16>(Xt, sx, Wt, sw, bias, M, N, K, Y, act, stream);
 }
 
-// 5184 tokens, K = 4096, N = 4096: 121 us, 2.9 POP/s. Few tokens take the same tiles (26 us a call for 1 to 256 of them at
-// N = 11264, K = 4096, against 14 to 30 with 4-bit rows): this layout is for many.
+// 5184 tokens, K = 4096, N = 4096: 121 us, 2.9 POP/s. Few tokens take the kernel of gemm_skinny.hip.
 hipError_t launch_gemm_gated_fp6(const void* Xt, const float* sx, const void* Wt, const float* sw, const float* bias, int64_t M,
                                  int64_t N, int64_t K, void* Y, int out_dt, int act, hipStream_t stream) {
   if (M == 0 || N == 0) return hipSuccess;
+  if (gated_skinny_supported(M, N)) return launch_gated_skinny6(Xt, sx, Wt, sw, bias, M, N, K, Y, out_dt, act, stream);
   return out_dt == kF16 ? launch6<kOutGateF16>(Xt, sx, Wt, sw, bias, M, 2 * N, K, Y, act, stream)
                         : launch6<kOutGateBF16>(Xt, sx, Wt, sw, bias, M, 2 * N, K, Y, act, stream);
 }

@@ -1,4 +1,4 @@
-// gemm_skinny.hip -- the gated product for few tokens (decode steps, drafts): int8 / int4 codes.
+// gemm_skinny.hip -- the gated product for few tokens (decode steps, drafts): int8 / int4 codes, and FP6 tiles (below).
 //
 // With few tokens the product is bound by the weights' bytes, 2 N * Kb, each read once. So the work is laid
 // out for bytes in flight, not for reuse: a workgroup takes one to four 32-row blocks of the weights (16 gate rows
@@ -27,9 +27,40 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
+constexpr int kFp6 = 2, kUnit = 127;   // the matrix instruction's FP6 E2M3, and E8M0 of 2^0
+
 // 16 bytes a lane from memory to LDS, lane l's at dst + 16 l.
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint8_t* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)dst, 16, off, 0, 0, 0);
+}
+
+// Four outputs of a token from the sums of their gate and up rows. scales, biases: of the block's rows (gate; up 16 on).
+template <int OUT>
+__device__ __forceinline__ void store_gated(const float (&gate)[4], const float (&up)[4], float xs, const float* scales, const float* biases,
+                                            int act, uint16_t* dst) {
+  auto finish = [&](auto tag) __attribute__((always_inline)) {
+    constexpr int ACT = decltype(tag)::value;
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const float g = __builtin_fmaf(gate[e], __fmul_rn(scales[e], xs), biases[e]);
+      const float u = __builtin_fmaf(up[e], __fmul_rn(scales[16 + e], xs), biases[16 + e]);
+      y[e] = __fmul_rn(activate<ACT>(g), u);
+    }
+    uint2 o;
+    o.x = pack2(y[0], y[1], OUT);
+    o.y = pack2(y[2], y[3], OUT);
+    *reinterpret_cast<uint2*>(dst) = o;
+  };
+  if (act == kActSilu) {
+    finish(std::integral_constant<int, kActSilu>{});
+  } else if (act == kActGeluErf) {
+    finish(std::integral_constant<int, kActGeluErf>{});
+  } else if (act == kActGeluTanh) {
+    finish(std::integral_constant<int, kActGeluTanh>{});
+  } else {
+    finish(std::integral_constant<int, kActNone>{});
+  }
 }
 
 // MT tiles of 16 tokens, RB blocks of 32 weight rows. The waves take the 128-byte lines of K in turn, each with a
@@ -185,32 +216,119 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_gated_skinny_kernel(
       for (int h = 0; h < 2; h++)
         sum[h] += __builtin_bit_cast(v4i, red[((w * 2 * RB + 2 * rb + h) * MT + t) * 64 + lane]);
     if (32 * rb >= rows || m >= M) continue;
-    auto finish = [&](auto tag) __attribute__((always_inline)) {
-      constexpr int ACT = decltype(tag)::value;
-      const float xs = x_scales[m];
-      float y[4];
+    float gate[4], up[4];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int n = 32 * rb + 4 * g + e;
-        const int ig = BITS == 4 ? sum[0][e] >> 8 : sum[0][e], iu = BITS == 4 ? sum[1][e] >> 8 : sum[1][e];
-        const float gate = __builtin_fmaf(static_cast<float>(ig), __fmul_rn(w_scales[n], xs), biases[n]);
-        const float up = __builtin_fmaf(static_cast<float>(iu), __fmul_rn(w_scales[16 + n], xs), biases[16 + n]);
-        y[e] = __fmul_rn(activate<ACT>(gate), up);
-      }
-      uint2 o;
-      o.x = pack2(y[0], y[1], OUT);
-      o.y = pack2(y[2], y[3], OUT);
-      *reinterpret_cast<uint2*>(Y + (int64_t)m * N + row0 / 2 + 16 * rb + 4 * g) = o;
-    };
-    if (act == kActSilu) {
-      finish(std::integral_constant<int, kActSilu>{});
-    } else if (act == kActGeluErf) {
-      finish(std::integral_constant<int, kActGeluErf>{});
-    } else if (act == kActGeluTanh) {
-      finish(std::integral_constant<int, kActGeluTanh>{});
-    } else {
-      finish(std::integral_constant<int, kActNone>{});
+    for (int e = 0; e < 4; e++) {
+      gate[e] = static_cast<float>(BITS == 4 ? sum[0][e] >> 8 : sum[0][e]);
+      up[e] = static_cast<float>(BITS == 4 ? sum[1][e] >> 8 : sum[1][e]);
     }
+    const int n = 32 * rb + 4 * g;
+    store_gated<OUT>(gate, up, x_scales[m], w_scales + n, biases + n, act, Y + (int64_t)m * N + row0 / 2 + 16 * rb + 4 * g);
+  }
+}
+
+// The same for FP6 tiles, with v_mfma_scale_f32_16x16x128_f8f6f4: lane (r, g) holds 32 codes of a row, the half g % 2 of
+// slice 2 q + g / 2 of a step q of 128 (16 bytes of plane 1 and 8 of plane 2). A fragment's 16 rows lie side by side in
+// the tiles, 512 and 256 bytes a slice, so loads go straight to registers, DEPTH steps ahead. Past K's end
+// they give zeros. Sums are integers below 2^24: exact in binary32 in any order. N = 11264, K = 4096, a call with its
+// rotation: 16.5 us for one token, 19.7 for 64, 23.4 for 96 (26 to 27 on the 256 x 128 tiles); N = 2048, K = 8192: 13 to
+// 20 us up to 128 tokens, 40 on the tiles. Two blocks of rows a workgroup, or more steps ahead: 1 to 4 us slower.
+template <int OUT, int MT, int DEPTH>
+__global__ __launch_bounds__(256) void gemm_gated_skinny6_kernel(const uint8_t* __restrict__ Xt, const float* __restrict__ sx,
+                                                                 const uint8_t* __restrict__ Wt, const float* __restrict__ sw,
+                                                                 const float* __restrict__ bias, uint16_t* __restrict__ Y, int M, int N,
+                                                                 int K, int act) {
+  typedef int v8i __attribute__((ext_vector_type(8)));
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  constexpr int WAVES = 4, kSliceX = 256 * 48, kSliceW = 128 * 48;
+  __shared__ __attribute__((aligned(16))) float4 red[WAVES * 2 * MT * 64];
+  __shared__ float w_scales[32], biases[32], x_scales[16 * MT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t row0 = (int64_t)blockIdx.x * 32;
+  const int slices = K >> 6, steps = slices >> 1;
+  if (tid < 32) {
+    w_scales[tid] = sw[row0 + tid];
+    biases[tid] = bias ? bias[row0 + tid] : 0.0f;
+  }
+  if (tid < 16 * MT) x_scales[tid] = tid < M ? sx[tid] : 0.0f;
+
+  // A workgroup's 32 rows lie in one 128-row panel.
+  const __amdgpu_buffer_rsrc_t wrs = rsrc(Wt + (row0 >> 7) * ((int64_t)slices * kSliceW), (uint32_t)slices * kSliceW);
+  const __amdgpu_buffer_rsrc_t xrs = rsrc(Xt, (uint32_t)slices * kSliceX);
+  auto place = [&](int row, int panel, uint32_t& one, uint32_t& two) __attribute__((always_inline)) {
+    const uint32_t slice = (uint32_t)(g >> 1) * (panel * 48);
+    one = slice + row * 32 + 16 * ((g & 1) ^ ((row >> 3) & 1));
+    two = slice + panel * 32 + row * 16 + 8 * ((g & 1) ^ ((row >> 4) & 1));
+  };
+  uint32_t w1[2], w2[2], x1[MT], x2[MT];
+#pragma unroll
+  for (int h = 0; h < 2; h++) place((int)(row0 & 127) + 16 * h + r, 128, w1[h], w2[h]);
+#pragma unroll
+  for (int t = 0; t < MT; t++) place(16 * t + r, 256, x1[t], x2[t]);
+  struct Step {
+    v4i w1[2], x1[MT];
+    v2i w2[2], x2[MT];
+  } ring[DEPTH];
+  auto load = [&](Step& s, int q) __attribute__((always_inline)) {
+    const uint32_t wq = (uint32_t)q * (2 * kSliceW), xq = (uint32_t)q * (2 * kSliceX);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      s.w1[h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(wrs, w1[h] + wq, 0, 0));
+      s.w2[h] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(wrs, w2[h] + wq, 0, 0));
+    }
+#pragma unroll
+    for (int t = 0; t < MT; t++) {
+      s.x1[t] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(xrs, x1[t] + xq, 0, 0));
+      s.x2[t] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(xrs, x2[t] + xq, 0, 0));
+    }
+  };
+  auto operand = [](const v4i& a, const v2i& b) __attribute__((always_inline)) {
+    return v8i{a[0], a[1], a[2], a[3], b[0], b[1], 0, 0};
+  };
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  v4f acc[2][MT];
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+#pragma unroll
+    for (int t = 0; t < MT; t++) acc[h][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int d = 0; d < DEPTH; d++) {
+    load(ring[d], wave + WAVES * d);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int q = wave; q < steps; q += WAVES * DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int t = 0; t < MT; t++)
+          acc[h][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(ring[d].w1[h], ring[d].w2[h]), operand(ring[d].x1[t], ring[d].x2[t]),
+                                                                       acc[h][t], kFp6, kFp6, 0, kUnit, 0, kUnit);
+      __builtin_amdgcn_sched_barrier(0);    // in order: else all steps' products wait for all steps' loads
+      load(ring[d], q + WAVES * (DEPTH + d));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // The wait that a read of the last product needs: the loop's end lies between them.
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+#pragma unroll
+    for (int t = 0; t < MT; t++) red[((wave * 2 + h) * MT + t) * 64 + lane] = __builtin_bit_cast(float4, acc[h][t]);
+  __syncthreads();
+  for (int t = wave; t < MT; t += WAVES) {
+    const int m = 16 * t + r;
+    v4f sum[2] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}, v4f{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int w = 0; w < WAVES; w++)
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        sum[h] += __builtin_bit_cast(v4f, red[((w * 2 + h) * MT + t) * 64 + lane]);
+    if (m >= M) continue;
+    const float gate[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]}, up[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+    store_gated<OUT>(gate, up, x_scales[m], w_scales + 4 * g, biases + 4 * g, act, Y + (int64_t)m * N + row0 / 2 + 4 * g);
   }
 }
 
@@ -277,7 +395,8 @@ hipError_t launch_tokens(const SkinnyCall& c) {
 
 // Up to 96 tokens; up to 128 where two rounds of workgroups hold all blocks. Measured against the 256 x 128 tiles
 // (K = 4096, 8 bits): 96 tokens, N = 11264 27.5 against 37 us; 128 tokens, N = 4096 15.9 against 32.6, N = 8192 22.9
-// against 34.7, but N = 11264 42.3 against 37.3 (4 bits: 30.5 against 27.5).
+// against 34.7, but N = 11264 42.3 against 37.3 (4 bits: 30.5 against 27.5). FP6 tiles: 128 tokens, N = 11264 28.2 against
+// 26.5, N = 5120, K = 2048 15.0 against 17.7.
 bool gated_skinny_supported(int64_t M, int64_t N) { return M <= 96 || (M <= 128 && N / 16 <= 2 * kNumCUs); }
 
 hipError_t launch_gated_skinny(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
@@ -290,6 +409,31 @@ hipError_t launch_gated_skinny(const void* Xq, const float* sx, const void* Wq, 
   }
   if (bits == 8) return x_tiled ? launch_tokens<8, kOutBF16, true>(c) : launch_tokens<8, kOutBF16, false>(c);
   return x_tiled ? launch_tokens<4, kOutBF16, true>(c) : launch_tokens<4, kOutBF16, false>(c);
+}
+
+
+template <int OUT, int MT, int DEPTH>
+hipError_t launch6(const SkinnyCall& c) {
+  hipLaunchKernelGGL((gemm_gated_skinny6_kernel<OUT, MT, DEPTH>), dim3((unsigned)(c.N / 16)), dim3(256), 0, c.st, c.Xq, c.sx, c.Wq, c.sw,
+                     c.bias, c.Y, c.M, c.N, c.Kb, c.act);
+  return hipGetLastError();
+}
+
+template <int OUT>
+hipError_t launch6_tokens(const SkinnyCall& c) {
+  if (c.M <= 16) return launch6<OUT, 1, 4>(c);
+  if (c.M <= 32) return launch6<OUT, 2, 2>(c);
+  if (c.M <= 48) return launch6<OUT, 3, 2>(c);
+  if (c.M <= 64) return launch6<OUT, 4, 2>(c);
+  if (c.M <= 96) return launch6<OUT, 6, 2>(c);
+  return launch6<OUT, 8, 1>(c);
+}
+
+hipError_t launch_gated_skinny6(const void* Xt, const float* sx, const void* Wt, const float* sw, const float* bias, int64_t M, int64_t N,
+                                int64_t K, void* Y, int out_dt, int act, hipStream_t st) {
+  const SkinnyCall c = {static_cast<const uint8_t*>(Xt), sx, static_cast<const uint8_t*>(Wt), sw, bias,
+                        static_cast<uint16_t*>(Y), (int)M, (int)N, (int)K, act, st};
+  return out_dt == kF16 ? launch6_tokens<kOutF16>(c) : launch6_tokens<kOutBF16>(c);
 }
 
 }  // namespace convrot

@@ -71,6 +71,9 @@ bool gated_skinny_supported(int64_t M, int64_t N);
 hipError_t launch_gated_skinny(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
                                int64_t N, int64_t Kb, int bits, bool x_tiled, void* Y, int out_dt, int act, hipStream_t stream);
 
+hipError_t launch_gated_skinny6(const void* Xt, const float* sx, const void* Wt, const float* sw, const float* bias, int64_t M, int64_t N,
+                                int64_t K, void* Y, int out_dt, int act, hipStream_t st);
+
 // The same GEMM with each CU's weight tile resident in LDS and eight independent waves
 // (int8 codes in the tiled layout, K = 1024; gemm_rw.hip). launch_gemm takes it where
 // gemm_rw_supported() holds.
