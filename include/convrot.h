@@ -187,7 +187,9 @@ typedef struct {
   const void *weight;        /* [K] of w_dtype, or NULL (ones) */
   void *H;                   /* out: h [M, K] of dtype, or NULL (not kept). May be X or residual
                                 itself (same address and stride); its rows must not overlap
-                                theirs in another way, nor one another */
+                                theirs in another way, nor one another. (Rows that lie between
+                                H's with another stride, not 0: up to 65536 of them, beyond that
+                                RQ_EUNSUPPORTED) */
   void *Xq;                  /* out: rq_codes_bytes(M, K, cfg) bytes in cfg->x_layout */
   float *x_scale;            /* out: [M] */
   int64_t M, K;

@@ -249,3 +249,20 @@ def test_codes_feed_the_products():
         y = Y.cpu().double().numpy()
         # One rounding to fp16 and a few of binary32; below fp16's normal range a step is 2^-24.
         assert np.all(np.abs(y - exact) <= (2.0 ** -11 + 2.0 ** -19) * np.abs(exact) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("M", [3, 65537])
+def test_one_residual_row_in_a_gap_of_h(M):
+    need_gpu()
+    K = 256
+    x, r, w = _case(M, K, "bf16", True, "same", 11)
+    X, W = _cuda(x, w)
+    both = torch.full((M, 2 * K), -3.0, dtype=torch.bfloat16, device="cuda")
+    both[0, K:] = r[0].cuda()
+    keep = both[:, K:].clone()
+    row = both[:1, K:].expand(M, K)
+    Xq, scale, H = rq.norm_rotate_quantize(X, row, W, out=both[:, :K])
+    h = norm_ref.hidden(x, r[:1].expand(M, K))
+    assert torch.equal(H.cpu(), h) and torch.equal(both[:, K:], keep)
+    _check(Xq[:50], scale[:50], h[:50], w, 1e-6, 8, rq.RQ_X_ROWS, K)
+    _check(Xq[-50:], scale[-50:], h[-50:], w, 1e-6, 8, rq.RQ_X_ROWS, K)

@@ -78,3 +78,20 @@ def test_wrapper_refusals():
     for bad in (torch.zeros(255), torch.zeros(256, dtype=torch.bfloat16), torch.zeros(512)[::2], torch.zeros(1, 256)):
         with pytest.raises(ValueError, match="weight"):
             rq.norm_rotate_quantize(X, R, bad)
+
+
+@pytest.mark.parametrize("M", [65536, 65537])
+def test_inputs_in_the_gaps_of_h(M):
+    """X between H's rows, met by none: a single row repeated at any M, rows of another stride up to 65536 of them (not worked
+    out beyond). The residual, looked at after X, lies on H's rows, so that no call here launches."""
+    kw = dict(M=M, H=A, h_stride=512, residual=A + 512 + 16, residual_stride=512, Xq=A + 4 * GB, x_scale=A + 6 * GB)
+    detail = lambda: rq.load().rq_last_error_detail().decode()  # noqa: E731
+    assert _status(X=A + 512, x_stride=0, **kw) == rq.RQ_EINVAL and "residual" in detail()
+    assert _status(X=A + 512 + 1024 * (M - 1), x_stride=0, **kw) == rq.RQ_EINVAL and "residual" in detail()
+    for at in (496, 1024 - 496, 1024 * (M - 1), 1024 * (M - 1) - 496, 1024 * (M - 1) + 496):   # on one of H's rows, or its first or last bytes
+        assert _status(X=A + at, x_stride=0, **kw) == rq.RQ_EINVAL and "overlaps X" in detail(), at
+    apart = _status(X=A + 512, x_stride=1024, **kw)
+    if M <= 65536:
+        assert apart == rq.RQ_EINVAL and "residual" in detail()
+    else:
+        assert apart == rq.RQ_EUNSUPPORTED and "X" in detail()

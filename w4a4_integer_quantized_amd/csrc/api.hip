@@ -328,8 +328,9 @@ rq_status check_norm_apart(const rq_norm_params* p, int64_t es, int64_t hb, cons
   const int64_t hs = p->M == 1 ? 0 : p->h_stride, is = p->M == 1 ? 0 : in_stride;
   if (p->H == in && hs == is) return ok();
   const int64_t r = (int64_t)(reinterpret_cast<intptr_t>(in) - reinterpret_cast<intptr_t>(p->H)) / es;
-  if (rows_meet(p->M, p->K, hs, is, r) != 0)
-    return fail(RQ_EINVAL, "H overlaps %s without being the same rows", name);
+  const int m = rows_meet(p->M, p->K, hs, is, r);
+  if (m == 1) return fail(RQ_EINVAL, "H overlaps %s without being the same rows", name);
+  if (m < 0) return fail(RQ_EUNSUPPORTED, "H and %s lie in each other with strides %lld and %lld", name, (long long)hs, (long long)is);
   return ok();
 }
 
@@ -437,7 +438,7 @@ rq_status check_kv_rows(const void* p, const char* name, int64_t tokens, int64_t
   return ok();
 }
 
-// Two sets of rows of `dim` elements in one buffer, each set's rows apart from one another: 1 if a row of one
+// Two sets of rows of `dim` elements in one buffer, the first set's rows apart from one another: 1 if a row of one
 // meets a row of the other, 0 if none does, -1 if that is not worked out.
 // `n` rows at 0, ks, 2 ks, .. and at r, r + vs, ...
 int rows_meet(int64_t n, int64_t dim, int64_t ks, int64_t vs, int64_t r) {
@@ -446,6 +447,12 @@ int rows_meet(int64_t n, int64_t dim, int64_t ks, int64_t vs, int64_t r) {
     int64_t j = r >= 0 ? -(r / ks) - 1 : -r / ks;
     for (const int64_t last = j + 1; j <= last; j++)
       if (j > -n && j < n && r + j * ks > -dim && r + j * ks < dim) return 1;
+    return 0;
+  }
+  if (vs == 0) {   // one row, between two of the others at most
+    const int64_t i = r >= 0 ? r / ks : 0;
+    for (int64_t k = i; k < n && k <= i + 1; k++)
+      if (r - k * ks > -dim && r - k * ks < dim) return 1;
     return 0;
   }
   if (n > 65536) return -1;
