@@ -155,3 +155,18 @@ def test_the_reference_itself():
     for j in inner:
         ahead = sum(w[i] > w[j] or (w[i] == w[j] and i < j) for i in range(3, 46))
         assert ahead < 13
+
+
+@pytest.mark.parametrize("seqs,rows,heads,group", [(1, 2048, 8, 4), (4, 1024, 8, 4), (1, 2813, 8, 16), (2, 700, 1, 16)])
+def test_weights_workspaces_go_by_lengths_not_by_the_table(seqs, rows, heads, group):
+    """A call of known lengths shares out its rows, and needs the same workspace, whatever its page table could hold."""
+    cfg = rq.make_kv_cfg(heads, 128, 64, 4)
+    need = [rq.kv_attention_weights_workspace_size(seqs * rows, heads * group, seqs, tokens // 64, cfg, max_q_len=rows, max_kv_len=rows,
+                                                   ragged=True) for tokens in (4096, 65536, 131072, 139264, 1 << 20, 1 << 30)]
+    query = (seqs * rows * group // 16 + seqs + 1) * heads * (4 * 2048 + 256)
+    assert len(set(need)) == 1 and need[0] > -(-query // 256) * 256
+    # Without lengths the table's count: the sums of 6000 workgroups of 256 tokens, and of one turn more, at most.
+    for tokens in (4096, 65536, 131072, 139264, 1 << 20, 1 << 30):
+        sums = rq.kv_attention_weights_workspace_size(seqs * rows, heads * group, seqs, tokens // 64, cfg, max_q_len=rows, ragged=True) \
+            - -(-query // 256) * 256
+        assert 0 <= sums <= 2 * 6000 * 256 * 4

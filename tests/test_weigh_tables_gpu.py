@@ -1,0 +1,49 @@
+"""rq_kv_attention_weights on the GPU: rows in shares whatever the page table's width, lengths beyond the hint."""
+import pytest
+import torch
+
+import w4a4_integer_quantized_amd as rq
+from tests import evict_ref
+from tests.test_weigh_gpu import _call, _check, _ints, _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("q,kv,group", [([700], [900], 3), ([400, 90, 0, 640], [1200, 90, 33, 640], 4)])
+def test_tables_wider_than_the_sequences(q, kv, group):
+    """The same call with tables of 2^12 to 2^20 tokens: the same shares of rows, workspace and bits."""
+    got = []
+    for extra in (0, 3, 2048, 16384):
+        d = _call(q, kv, heads=2, group=group, page=64, extra=extra, keep=0.0, seed=21)
+        print("table", d["pages"].shape[1] * 64, flush=True)
+        hints = dict(max_q_len=max(q), max_kv_len=max(kv))
+        out = _run(d, **hints)
+        _check(d, out)
+        need = rq.kv_attention_weights_workspace_size(sum(q), 2 * group, len(q), d["pages"].shape[1], d["cfg"], ragged=True, **hints)
+        got.append((need, [out[b, :, :n] for b, n in enumerate(kv)]))
+    for need, out in got[1:]:
+        assert need == got[0][0] and all(torch.equal(x, y) for x, y in zip(out, got[0][1]))
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 90), (False, 0)])
+@pytest.mark.parametrize("hint", [1, 256, 300])
+def test_lengths_beyond_the_hint(hint, causal, window):
+    """Rows are shared out for the first tokens only; those of a longer sequence's others are added up by one workgroup."""
+    for keep in (0.0, 0.5):
+        d = _call([300, 520, 128, 0], [2000, 513, 256, 700], heads=1, group=5, page=32, causal=causal, window=window, keep=keep, seed=hint)
+        assert rq.kv_attention_weights_workspace_size(948, 5, 4, d["pages"].shape[1], d["cfg"], max_kv_len=hint, ragged=True) > \
+            (948 * 5 // 16 + 5) * (4 * 2048 + 256) + 256
+        _check(d, _run(d, max_kv_len=hint))
+
+
+def test_the_most_shares():
+    """700 tiles of rows over three ranges of tokens: 64 shares, joined, and in a workspace whose ends are left alone."""
+    d = _call([700], [705], heads=1, group=16, page=64, keep=0.5, seed=4)
+    need = rq.kv_attention_weights_workspace_size(700, 16, 1, d["pages"].shape[1], d["cfg"], ragged=True)
+    span = d["pages"].shape[1] * 64
+    assert need == -(-(700 + 2) * (4 * 2048 + 256) // 256) * 256 + 64 * (-(-span // 256) * 256) * 4
+    space = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = _run(d, workspace=space[256:256 + need])
+    _check(d, got)
+    assert bool((space[:256] == 0xFF).all()) and bool((space[256 + need:] == 0xFF).all())
+    assert torch.equal(_run(d), got)

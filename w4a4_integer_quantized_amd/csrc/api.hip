@@ -679,7 +679,7 @@ rq_status check_kv_weigh(const rq_kv_attention_params* p, const rq_kv_config* cf
     return fail(RQ_EUNSUPPORTED, "weights of %d sequences, %d heads and %lld tokens have over 2^46 bytes", p->seqs, cfg->kv_heads,
                 (long long)span);
   *max_q_len = max_q;
-  *plan = convrot::plan_kv_weigh(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q, max_kv, span);
+  *plan = convrot::plan_kv_weigh(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q, max_kv);
   // A grid has fewer than 2^32 threads, 256 a workgroup.
   constexpr int64_t kMost = int64_t(1) << 24;
   if ((int64_t)p->seqs * plan->splits + 8 >= kMost / (cfg->kv_heads * plan->row_splits) ||
@@ -1027,7 +1027,7 @@ size_t rq_kv_attention_weights_workspace_size(const rq_kv_attention_params* p, c
   int64_t max_q = 0, max_kv = 0;
   if (check_kv_shape(p, cfg, &max_q, &max_kv) != RQ_OK || p->seqs == 0 || p->max_pages == 0) return 0;
   const convrot::KvWeighPlan plan = convrot::plan_kv_weigh(p->total_q, p->seqs, p->q_heads, cfg->kv_heads, cfg->head_dim, max_q,
-                                                           max_kv, (int64_t)p->max_pages * cfg->page_size);
+                                                           max_kv);
   return (size_t)(plan.query_bytes + plan.part_bytes);
 }
 
@@ -1045,9 +1045,10 @@ rq_status rq_kv_attention_weights(const rq_kv_attention_params* p, const rq_kv_c
   w.keep = keep;
   w.queries = static_cast<uint8_t*>(workspace);
   if (plan.part_bytes > 0) w.parts = reinterpret_cast<float*>(w.queries + plan.query_bytes);
-  w.part_stride = (int64_t)p->seqs * cfg->kv_heads * p->max_pages * cfg->page_size;
+  w.part_span = plan.part_span;
+  w.part_stride = (int64_t)p->seqs * cfg->kv_heads * plan.part_span;
   w.query_tiles_seq = plan.query_tiles_seq;
-  const int64_t blocks = ((int64_t)p->max_pages * cfg->page_size + 255) / 256;
+  const int64_t blocks = (plan.part_span + 255) / 256;
   w.join_blocks = static_cast<int>(blocks < 1024 ? blocks : 1024);
   return from_hip(convrot::launch_kv_weigh(w, cfg->head_dim, cfg->bits, plan.kt, plan.many, static_cast<hipStream_t>(stream)),
                   "kv_weigh launch");

@@ -136,20 +136,20 @@ hipError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, int bits,
 struct KvWeighArgs {
   KvAttentionArgs a;
   float* weights;             // [seqs, heads, max_pages << lps]
-  float* parts;               // [row_tiles] times that, where row_tiles > 1
+  float* parts;               // [row_tiles][seqs, heads, part_span], where row_tiles > 1
   uint8_t* queries;           // rotated queries (many)
+  int64_t part_span;          // tokens, from a sequence's first on, whose rows are shared out
   int64_t part_stride;        // elements of one share
   int64_t query_tiles_seq;    // tiles of 16 rows of the longest sequence
   int join_blocks;
   float keep;
 };
 struct KvWeighPlan {
-  int64_t splits, row_splits, query_tiles_seq, query_bytes, part_bytes;
+  int64_t splits, row_splits, query_tiles_seq, query_bytes, part_bytes, part_span;
   int kt;                     // 16-token steps of a wave
   bool many;                  // queries are rotated by a kernel of their own
 };
-KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len,
-                          int64_t span);
+KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len);
 hipError_t launch_kv_weigh(const KvWeighArgs& w, int head_dim, int bits, int kt, bool many, hipStream_t stream);
 
 // A cache brought down to a budget (kv_evict.hip). Pre-validated: first + recent <= budget <= new_max_pages << lps.

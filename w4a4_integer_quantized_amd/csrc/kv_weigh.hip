@@ -292,22 +292,22 @@ __device__ __forceinline__ void add_weights(const KvAttentionArgs& a, const Seq&
   for (int k = 0; k < KT; k++) sum[k] += (p[k][0] + p[k][1]) + (p[k][2] + p[k][3]);
 }
 
-// What was there before for the token that a lane will write (see write_sums); zero where it does not count. (Loaded from
-// somewhere in any case: a load under a condition is waited for at once.)
+// What was there before for the token that a lane will write (see write_sums); zero where it does not count, as in a share of
+// the rows (`shared`). (Loaded from somewhere in any case: a load under a condition is waited for at once.)
 template <int KT>
-__device__ __forceinline__ bool had_before(const KvWeighArgs& w, const Seq& s, int first, int r, int g) {
+__device__ __forceinline__ bool had_before(const KvWeighArgs& w, bool shared, const Seq& s, int first, int r, int g) {
   const int j = first + 16 * g + r;
-  return w.a.row_tiles == 1 && w.keep != 0.0f && g < KT && j < s.kv_len && !(w.a.causal && j >= s.kv_len - s.q_len);
+  return !shared && w.keep != 0.0f && g < KT && j < s.kv_len && !(w.a.causal && j >= s.kv_len - s.q_len);
 }
 template <int KT>
-__device__ __forceinline__ float load_before(const KvWeighArgs& w, const Place& at, const Seq& s, int first, int r, int g) {
+__device__ __forceinline__ float load_before(const KvWeighArgs& w, bool shared, const Place& at, const Seq& s, int first, int r, int g) {
   const float* row = w.weights + ((int64_t)at.seq * w.a.heads + at.head) * ((int64_t)w.a.max_pages << w.a.lps);
-  return row[had_before<KT>(w, s, first, r, g) ? first + 16 * g + r : 0];
+  return row[had_before<KT>(w, shared, s, first, r, g) ? first + 16 * g + r : 0];
 }
 
 // Over the four lanes of a token; then lane (r, g) writes token r of step g.
 template <int KT>
-__device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at, const Seq& s, int first, uint32_t there, int r, int g,
+__device__ __forceinline__ void write_sums(const KvWeighArgs& w, bool shared, const Place& at, const Seq& s, int first, uint32_t there, int r, int g,
                                            float before, const float (&sum)[KT]) {
   const KvAttentionArgs& a = w.a;
   float mine = 0.0f;
@@ -320,11 +320,11 @@ __device__ __forceinline__ void write_sums(const KvWeighArgs& w, const Place& at
   }
   const int j = first + 16 * g + r;
   if (g < KT && j < s.kv_len) {
-    const int64_t out = ((int64_t)at.seq * a.heads + at.head) * ((int64_t)a.max_pages << a.lps) + j;
-    if (a.row_tiles > 1)
-      w.parts[at.tile * w.part_stride + out] = mine;
+    const int64_t row = (int64_t)at.seq * a.heads + at.head, out = row * ((int64_t)a.max_pages << a.lps) + j;
+    if (shared)
+      w.parts[at.tile * w.part_stride + row * w.part_span + j] = mine;
     else
-      w.weights[out] = had_before<KT>(w, s, first, r, g) ? __builtin_fmaf(w.keep, before, mine) : mine;
+      w.weights[out] = had_before<KT>(w, shared, s, first, r, g) ? __builtin_fmaf(w.keep, before, mine) : mine;
   }
 }
 
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
   for (; base < s.kv_len && base + kKeys <= lo; base += step) {
     float none[KT] = {};
     const int first = static_cast<int>(base) + wave * (KT * 16);
-    write_sums<KT>(w, at, s, first, 0, r, g, load_before<KT>(w, at, s, first, r, g), none);
+    write_sums<KT>(w, false, at, s, first, 0, r, g, load_before<KT>(w, false, at, s, first, r, g), none);
   }
   if (base >= s.kv_len) return;
   // A range's codes and what was there before; past the last range the last again.
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
   float next_was;
   auto load = [&](int64_t at_base) __attribute__((always_inline)) {
     const int first = static_cast<int>(at_base < s.kv_len ? at_base : base) + wave * (KT * 16);
-    next_was = load_before<KT>(w, at, s, first, r, g);
+    next_was = load_before<KT>(w, false, at, s, first, r, g);
     load_keys<D, BITS, KT>(a, table, at.head, s.kv_len, first, r, g, next);
   };
   load(base);
@@ -392,12 +392,13 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
       weights_of<KT>(acc, info, common, key.factor, p);
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
-    write_sums<KT>(w, at, s, first, there, r, g, was, sum);
+    write_sums<KT>(w, false, at, s, first, there, r, g, was, sum);
   }
 }
 
 // Many query rows: tiles come from memory, made by weigh_query_kernel, copied to a ring in LDS three ahead.
-// a.row_tiles workgroups share a range's rows.
+// a.row_tiles workgroups share a range's rows, up to token w.part_span; behind it, where the lengths that the plan was made for
+// have ended, the first of them takes all.
 template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w) {
   using Q = QueryTile<D>;
@@ -429,6 +430,8 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
 
   for (int64_t base = (int64_t)at.split * kKeys; base < s.kv_len; base += (int64_t)a.splits * kKeys) {
     const int key0 = static_cast<int>(base), first = key0 + wave * (KT * 16);   // the workgroup's, the wave's
+    const bool shared = a.row_tiles > 1 && base < w.part_span;
+    if (!shared && at.tile > 0) break;
     // The tiles of rows that attend to some token of the workgroup's range, and this workgroup's share.
     int t0 = 0, t1 = (rows + kRows - 1) / kRows;
     if (a.causal) {
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
         t1 = n < t1 ? static_cast<int>(n) : t1;
       }
     }
-    if (a.row_tiles > 1 && t1 > t0) {
+    if (shared && t1 > t0) {
       const int share = (t1 - t0 + a.row_tiles - 1) / a.row_tiles;
       t0 += at.tile * share;
       t1 = t0 + share < t1 ? t0 + share : t1;
@@ -452,7 +455,7 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
 #pragma unroll
     for (int k = 0; k < KT; k++) sum[k] = 0.0f;
     if (t0 >= t1) {   // the same for the whole workgroup
-      write_sums<KT>(w, at, s, first, 0, r, g, load_before<KT>(w, at, s, first, r, g), sum);
+      write_sums<KT>(w, shared, at, s, first, 0, r, g, load_before<KT>(w, shared, at, s, first, r, g), sum);
       continue;
     }
     Raw<D, BITS, KT> raw;
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
     __syncthreads();   // the buffers are done with before the next range's first copy
-    write_sums<KT>(w, at, s, first, raw.there, r, g, load_before<KT>(w, at, s, first, r, g), sum);
+    write_sums<KT>(w, shared, at, s, first, raw.there, r, g, load_before<KT>(w, shared, at, s, first, r, g), sum);
   }
 }
 
@@ -499,11 +502,12 @@ __global__ __launch_bounds__(256) void weigh_join_kernel(const KvWeighArgs w) {
   const int b = blockIdx.y / a.heads;
   const Seq s = sequence(a, b);
   const int before = s.kv_len - s.q_len;
-  for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < s.kv_len; j += (int64_t)gridDim.x * 256) {
-    const int64_t out = (int64_t)blockIdx.y * span + j;
+  const int64_t end = s.kv_len < w.part_span ? s.kv_len : w.part_span;
+  for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < end; j += (int64_t)gridDim.x * 256) {
+    const int64_t out = (int64_t)blockIdx.y * span + j, part = (int64_t)blockIdx.y * w.part_span + j;
     float sum = 0.0f;
 #pragma unroll 8
-    for (int t = 0; t < a.row_tiles; t++) sum += w.parts[t * w.part_stride + out];
+    for (int t = 0; t < a.row_tiles; t++) sum += w.parts[t * w.part_stride + part];
     const bool had = w.keep != 0.0f && !(a.causal && j >= before);
     w.weights[out] = had ? __builtin_fmaf(w.keep, w.weights[out], sum) : sum;
   }
@@ -535,8 +539,7 @@ hipError_t launch(const KvWeighArgs& w, int kt, bool many, hipStream_t st) {
 
 }  // namespace
 
-KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len,
-                          int64_t span) {
+KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   KvWeighPlan p = {};
   const int64_t group = q_heads / heads;
   p.query_tiles_seq = (max_q_len * group + kRows - 1) / kRows;
@@ -558,9 +561,11 @@ KvWeighPlan plan_kv_weigh(int64_t total_q, int seqs, int q_heads, int heads, int
     if (p.row_splits > kMostShares) p.row_splits = kMostShares;
     if (p.row_splits < 1) p.row_splits = 1;
     p.query_bytes = ((total_q * group / kRows + seqs + 1) * heads * (head_dim / 32 * 2048 + 256) + 255) / 256 * 256;
-    // Sums of each share for the whole page table: not where that is much.
-    if (p.row_splits > 1 && p.row_splits * seqs * heads * span > (int64_t(1) << 26)) p.row_splits = 1;
-    if (p.row_splits > 1) p.part_bytes = p.row_splits * seqs * heads * span * 4;
+    // Sums of each share for the tokens of the plan's ranges: with the 6000 workgroups above 12 MB at most. (Not for the page
+    // table's, which may be far wider than any sequence is long: 2048 rows over 2048 tokens, 32 heads over 8, take 82 to 88 us
+    // with tables of 2048 to 2^20 tokens; unshared 394.)
+    p.part_span = p.splits * (kWaves * 16 * p.kt);
+    if (p.row_splits > 1) p.part_bytes = p.row_splits * seqs * heads * p.part_span * 4;
   }
   return p;
 }
