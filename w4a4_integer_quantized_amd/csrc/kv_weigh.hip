@@ -172,20 +172,24 @@ __device__ __forceinline__ void load_keys(const KvAttentionArgs& a, ConstTable t
   }
 }
 
-// The same as operands: codes in fp16, and for each token what takes a product to a logit in base 2.
+// What takes a product to a logit in base 2: a token's scale, this, and kCommon / (the row's power of two).
+template <int D, int BITS>
+__device__ __forceinline__ float logit_factor(const KvAttentionArgs& a) { return a.scale * (kLog2e * Row<D, BITS>::kNorm / kCommon); }
+
+// The same as operands: codes in fp16, each token's scale, and that times logit_factor().
 template <int D, int BITS, int KT>
 struct Keys {
   u32x4 op[KT][D / 32];
-  float factor[KT];
+  float scale[KT], factor[KT];
 };
 template <int D, int BITS, int KT>
 __device__ __forceinline__ void convert_keys(const KvAttentionArgs& a, const Raw<D, BITS, KT>& t, Keys<D, BITS, KT>& key) {
-  using R = Row<D, BITS>;
   using G = Geometry<D, BITS>;
 #pragma unroll
   for (int k = 0; k < KT; k++) {
     // A scale that is no finite number belongs to a token that was never written.
-    key.factor[k] = fabsf(t.scale[k]) < __builtin_inff() ? t.scale[k] * (a.scale * (kLog2e * R::kNorm / kCommon)) : 0.0f;
+    key.scale[k] = fabsf(t.scale[k]) < __builtin_inff() ? t.scale[k] : 0.0f;
+    key.factor[k] = key.scale[k] * logit_factor<D, BITS>(a);
 #pragma unroll
     for (int op = 0; op < G::kOps; op++) {
       if constexpr (BITS == 4) {
@@ -256,21 +260,29 @@ __device__ __forceinline__ int common_scale(const RowInfo& i) {
   return __builtin_amdgcn_readfirstlane(__ballot(own) == 0);
 }
 
-// A zero row's product is 0 and its lse +inf: a weight of 0 whatever the scale.
-template <int KT>
-__device__ __forceinline__ void weights_of(f32x4 (&acc)[KT], const RowInfo& info, int common, const float (&factor)[KT], float (&p)[KT][4]) {
+// A zero row's product is 0 and its lse +inf: a weight of 0 whatever the scale. Rows of another power of two may be anywhere in
+// binary32 and the keys at its other end: there the product meets the token's scale first, then what is left, so that nothing
+// in between is larger or smaller than both.
+template <int D, int BITS, int KT>
+__device__ __forceinline__ void weights_of(const KvAttentionArgs& a, f32x4 (&acc)[KT], const RowInfo& info, int common,
+                                           const Keys<D, BITS, KT>& key, float (&p)[KT][4]) {
   // The wait that a read of the last product needs, before the branch: it is not added across one.
 #pragma unroll
   for (int k = 0; k < KT; k++) asm volatile("" : "+v"(acc[k]));
   asm volatile("s_nop 7\n\ts_nop 3" : "+v"(acc[KT - 1]));
   if (!common) {
+    const float c = logit_factor<D, BITS>(a);
 #pragma unroll
-    for (int k = 0; k < KT; k++) acc[k] *= info.down;
+    for (int k = 0; k < KT; k++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        p[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[k][i] * key.scale[k], info.down[i] * c, -info.lse[i]));
+    return;
   }
 #pragma unroll
   for (int k = 0; k < KT; k++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) p[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[k][i], factor[k], -info.lse[i]));
+    for (int i = 0; i < 4; i++) p[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[k][i], key.factor[k], -info.lse[i]));
 }
 
 template <int KT>
@@ -389,7 +401,7 @@ __global__ __launch_bounds__(256, 2) void weigh_few_kernel(const KvWeighArgs w) 
       f32x4 acc[KT];
       float p[KT][4];
       multiply<D, BITS, KT, 2>(q, key, lane, acc);
-      weights_of<KT>(acc, info, common, key.factor, p);
+      weights_of<D, BITS, KT>(a, acc, info, common, key, p);
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
     write_sums<KT>(w, false, at, s, first, there, r, g, was, sum);
@@ -487,7 +499,7 @@ __global__ __launch_bounds__(256, 2) void weigh_many_kernel(const KvWeighArgs w)
       f32x4 acc[KT];
       float p[KT][4];
       multiply<D, BITS, KT, 4>(q, key, lane, acc);
-      weights_of<KT>(acc, info, common, key.factor, p);
+      weights_of<D, BITS, KT>(a, acc, info, common, key, p);
       add_weights<KT>(a, s, tile, all, first, r, g, p, sum);
     }
     __syncthreads();   // the buffers are done with before the next range's first copy
