@@ -240,3 +240,19 @@ def test_sequences_that_share_pages():
     d["pages"][1, :8] = d["pages"][0, :8]
     d["pages"][2, :3] = d["pages"][0, :3]
     _check(d, first=4, recent=10)
+
+
+@pytest.mark.parametrize("kw", [dict(first=(1 << 32) + 3), dict(recent=1 << 32), dict(first=-(1 << 32)), dict(recent=1 << 63),
+                                dict(budget=(1 << 32) + 64), dict(budget=(1 << 31) - 1), dict(budget=97), dict(budget=0)])
+def test_counts_beyond_the_calls_integers(kw):
+    """Refused, not cut to 32 bits; and no room is made for more places than new_pages have."""
+    d = _case([200, 150], 96, seed=2)
+    cache = torch.from_numpy(d["raw"]).cuda()
+    args = {**dict(budget=96, first=4, recent=8), **kw}
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    with pytest.raises(rq.ConvRotError):
+        rq.kv_evict(cache, _ints(d["pages"]), _ints(d["kv_len"]), torch.from_numpy(d["weights"]).cuda(), d["cfg"], new_pages=_ints(d["new_pages"]),
+                    **args)
+    assert torch.cuda.max_memory_allocated() - held < 1 << 24
+    assert np.array_equal(cache.cpu().numpy(), d["raw"])

@@ -701,9 +701,15 @@ def _kv_table(t, name, dtype, shape):
                                                                                      tuple(t.shape)))
 
 
+def _kv_int32(n):
+    """A count as the int32 of the call, which would else be cut to its low bits: none that is refused or
+    means all of a cache changes its meaning."""
+    return max(-1, min(n, (1 << 31) - 1))
+
+
 def _kv_window(window):
     """A window as the int32 of the call: any beyond the longest cache is all of it."""
-    return max(-1, min(window, (1 << 31) - 1))
+    return _kv_int32(window)
 
 
 def _kv_device(*ts):
@@ -947,13 +953,13 @@ def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_
         with _kv_placed(kv, index, stream):
             return kv_evict(cache, pages, kv_len, weights, cfg, budget, new_pages, new_weights, first, recent, kept, new_kv_len,
                             workspace)
-    if kept is None:
-        kept = pages.new_empty((seqs, cfg.kv_heads, max(budget, 0)))
+    if kept is None:   # no room where the budget is refused
+        kept = pages.new_empty((seqs, cfg.kv_heads, budget if 0 < budget <= new_max * cfg.page_size else 0))
     if new_kv_len is None:
         new_kv_len = kv.empty_like(kv_len)
     p = rq_kv_evict_params(cache.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), new_pages.data_ptr(), weights.data_ptr(),
                            None if new_weights is None else new_weights.data_ptr(), new_kv_len.data_ptr(), kept.data_ptr(),
-                           num_pages, seqs, max_pages, new_max, budget, first, recent)
+                           num_pages, seqs, max_pages, new_max, _kv_int32(budget), _kv_int32(first), _kv_int32(recent))
     need = rq_kv_evict_workspace_size(p, cfg)
     if workspace is not None:
         _check_bytes(workspace, "workspace", need, exact=False)
