@@ -73,7 +73,7 @@ template <int BITS, int OUT, bool XT, int MT, int RB, int WAVES, int SLOTS>
 __global__ __launch_bounds__(64 * WAVES) void gemm_gated_skinny_kernel(
     const uint8_t* __restrict__ Xq, const float* __restrict__ sx, const uint8_t* __restrict__ Wq, const float* __restrict__ sw,
     const float* __restrict__ bias, uint16_t* __restrict__ Y, int M, int N, int Kb, int act) {
-  static_assert(SLOTS <= 4, "the waits below know four lines");
+  static_assert(SLOTS <= 2, "the waits below know two lines");
   constexpr int kW = 32 * RB * 128, kSlot = kW + 2 * MT * 1024, kCopies = 4 * RB + 2 * MT;
   constexpr int kRed = WAVES * 2 * RB * MT * 1024, kRing = WAVES * SLOTS * kSlot;
   // One array: with several the compiler, telling them apart, waits for all copies before each read.
@@ -169,12 +169,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_gated_skinny_kernel(
     if (wave + WAVES * i < lines) copy(i, wave + WAVES * i);
   int slot = 0;
   for (int q = wave; q < lines; q += WAVES) {
-    // This line's copies have landed: those of the lines behind it, SLOTS - 1 or what is left, may be under way.
-    if (SLOTS > 3 && q + 3 * WAVES < lines) {
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies * 3) : "memory");
-    } else if (SLOTS > 2 && q + 2 * WAVES < lines) {
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies * 2) : "memory");
-    } else if (SLOTS > 1 && q + WAVES < lines) {
+    // This line's copies have landed: those of the line behind it, where there is one, may be under way.
+    if (SLOTS > 1 && q + WAVES < lines) {
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
