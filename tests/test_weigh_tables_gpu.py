@@ -47,3 +47,44 @@ def test_the_most_shares():
     _check(d, got)
     assert bool((space[:256] == 0xFF).all()) and bool((space[256 + need:] == 0xFF).all())
     assert torch.equal(_run(d), got)
+
+
+def _inside(t):
+    """A copy of t within a buffer of one number, and that buffer's ends."""
+    big = torch.full((t.numel() + 2048,), 0x55, dtype=torch.uint8, device="cuda") if t.dtype == torch.uint8 else \
+        torch.full((t.numel() + 2048,), -77.0, dtype=t.dtype, device="cuda")
+    view = big[1024:1024 + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view, (big[:1024], big[1024 + t.numel():])
+
+
+@pytest.mark.parametrize("q_len", [[1, 1, 1], [9, 0, 7], [40, 70, 3], [300, 333, 40]])
+def test_what_untrusted_tables_give_and_leave(q_len):
+    """Starts and lengths outside their ranges count as cut to them; nothing beside the sequences' sums and the workspace is
+    written. (Sequences whose rows lie over one another need not be right, but stay within them.)"""
+    d = _call(q_len, [100, 150, 64], page=16, extra=2, keep=0.5)
+    pages = d["pages"].clone()
+    pages[0, 2], pages[1, 3], pages[2, 0] = d["c"].pages, -5, (1 << 31) - 1
+    d["pages"] = pages
+    total, span = d["Q"].shape[0], pages.shape[1] * 16
+    need = rq.kv_attention_weights_workspace_size(total, 4, 3, pages.shape[1], d["cfg"], ragged=True)
+    good = [d["starts"][i] for i in range(4)]
+    calls = [([-9, 1 << 30, 5, 2], [100, span, 64]), ([total, total, total + 1, 3], [100, span, 64]), ([3, 2, 1, 0], [100, span, 64]),
+             ([-(1 << 31), 2, 2, (1 << 31) - 1], [span, 0, 37]), (good, [-7, 1 << 30, 64]), (good, [-(1 << 31), span + 1, (1 << 31) - 1]),
+             ([0, total, 0, total], [100, span, 64])]
+    for starts, lengths in calls:
+        print("tables", q_len, starts, lengths, flush=True)
+        out, ends = _inside(d["old"])
+        space, spaces_ends = _inside(torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device="cuda"))
+        rq.kv_attention_weights(d["Q"], d["lse"], d["c"].bytes, pages, _ints(lengths), d["cfg"], out, keep=0.5, q_start=_ints(starts),
+                                workspace=space)
+        torch.cuda.synchronize()
+        assert all(bool((x == -77.0).all()) for x in ends) and all(bool((x == 0x55).all()) for x in spaces_ends)
+        rows = [min(max(x, 0), total) for x in starts]
+        for b in range(3):
+            n = min(max(lengths[b], 0), span)
+            assert torch.equal(out[b, :, n:], d["old"][b, :, n:])
+            if starts[:3] == [0, total, 0] or n == 0:
+                continue
+            one = dict(d, pages=pages[b:b + 1], kv_len=[n], starts=[rows[b], max(rows[b], rows[b + 1])], old=d["old"][b:b + 1])
+            _check(one, out[b:b + 1])
