@@ -443,7 +443,9 @@ rq_status rq_kv_attention_weights(const rq_kv_attention_params *p, const rq_kv_c
  * they are, so a head's token i is what its token kept[i] was. Heads choose for themselves and keep the same
  * number of tokens. Afterwards the caller takes new_pages and new_kv_len for pages and kv_len; the old
  * pages are left as they were and can be given back.
- * (Causality goes by a token's place: queries at or behind the last one still attend to all.) */
+ * (Causality goes by a token's place: queries at or behind the last one still attend to all. A window does too: after an
+ * eviction `window` in rq_kv_attention and rq_kv_attention_weights counts the tokens that stayed, which may have lain further
+ * apart, and in each head others. With recent >= window - 1 they are those that the window had without the eviction.) */
 typedef struct {
   void *cache;                 /* in/out: device, num_pages * rq_kv_page_bytes(cfg) bytes */
   const int32_t *kv_len;       /* [seqs] device */

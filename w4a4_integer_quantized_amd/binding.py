@@ -931,7 +931,8 @@ def kv_evict(cache, pages, kv_len, weights, cfg: rq_kv_config, budget: int, new_
     `recent`, and of the others those with the largest weights [seqs, kv_heads, max_pages * page_size] (f32), in
     their order. Returns (kept, new_kv_len): kept [seqs, kv_heads, budget] (int32) are the old places,
     then -1, and new_kv_len [seqs] goes with new_pages from here on. new_weights [seqs, kv_heads,
-    new_max_pages * page_size]: where the weights of what stays go. See rq_kv_evict in convrot.h."""
+    new_max_pages * page_size]: where the weights of what stays go. A window of later attention calls counts the
+    tokens kept. See rq_kv_evict in convrot.h."""
     kv = _kv()
     num_pages = _kv_cache(kv, cache, cfg)
     if len(pages.shape) != 2 or len(new_pages.shape) != 2:
