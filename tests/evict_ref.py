@@ -91,7 +91,8 @@ def weigh(cache, Q, lse, pages, kv_len, q_start, old, keep, causal, window, scal
     and 2^-33 of the row's largest where the second part is below fp16's normal range); the scale, 1 / sqrt B
     and log2 e 6 u of it; lse times log2 e one rounding each, 3 u of lse; the difference one, u of each; exp2 4 u,
     and nothing is left below 2^-126. A lane adds four rows' weights and these up over the tiles of 16 rows, then four
-    lanes', the shares of rows (at most 16) and what was there: u each."""
+    lanes', the shares of rows and what was there: u each. (At most 64 shares, and an eighth of the tiles: those of one
+    share and the shares are fewer together than all tiles in one chain.)"""
     R = torch.from_numpy(kv_ref.matrix(cache.dim)).to(Q.device)
     B, group = min(128, cache.dim), Q.shape[1] // cache.heads
     out, tol = old.double().clone(), torch.zeros_like(old, dtype=torch.float64)

@@ -798,9 +798,12 @@ hipError_t launch_gated(const void* Xq, const float* sx, const void* Wq, const f
 }  // namespace
 
 // The gated product on the tile kernels: the same launch rule, with the weights' 2 N rows for N. Bound as the plain
-// product is: 16384 tokens, K = 4096, N = 8192 in 1006 us (2.19 POP/s), 5184 tokens, K = 1024,
-// N = 2736 with GELU in 45 us (1.29 POP/s: 43 column tiles and 21 row tiles on 256 CUs). 65 to 256 tokens over K = 4096,
-// N = 11264 take 22 to 36 us a call, 8 or 4 bits.
+// product is, the kernel alone: 16384 tokens, K = 4096, N = 8192 in 1006 us (2.19 POP/s), 5184 tokens, K = 1024,
+// N = 2736 with GELU in 45 us (1.29 POP/s: 43 column tiles and 21 row tiles on 256 CUs). Tokens above those of the kernel for
+// few, up to 256, over K = 4096, N = 11264 take 36 to 37 us a call with 8 bits and 28 to 31 with 4: 176 tiles, so 80 CUs
+// have no work. Row-major codes take 3 to 17% more than tiled ones (5184 tokens, K = 2048, N = 5504: 143 against 128 us). The plain
+// product's 256 x 256 kernel for row-major codes of 1536 to 3071 bytes has no activation and no gated form; over the same
+// rows of weights it takes 168 us there.
 hipError_t launch_gemm_gated(const void* Xq, const float* sx, const void* Wq, const float* sw, const float* bias, int64_t M,
                              int64_t N, int64_t K, int bits, bool x_tiled, void* Y, int out_dt, int act, hipStream_t stream) {
   if (M == 0 || N == 0) return hipSuccess;
