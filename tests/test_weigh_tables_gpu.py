@@ -88,3 +88,51 @@ def test_what_untrusted_tables_give_and_leave(q_len):
                 continue
             one = dict(d, pages=pages[b:b + 1], kv_len=[n], starts=[rows[b], max(rows[b], rows[b + 1])], old=d["old"][b:b + 1])
             _check(one, out[b:b + 1])
+
+
+def test_shares_captured_and_replayed_over_growing_lengths():
+    """Replays whose lengths pass the hint that the call was captured with, with eager work between."""
+    d = _call([300, 90], [700, 256], heads=2, group=3, page=32, extra=40, keep=0.5, seed=6)
+    rest = torch.randperm(d["c"].pages, device="cuda")[:8].int()
+    d["pages"][:, 22:30], d["pages"][1, 8:22] = rest, d["pages"][0, :14]
+    kv_len, out = _ints(d["kv_len"]), d["old"].clone()
+    args = dict(keep=0.5, q_start=_ints(d["starts"]), max_q_len=300, max_kv_len=512)
+
+    def step(w):
+        rq.kv_attention_weights(d["Q"], d["lse"], d["c"].bytes, d["pages"], kv_len, d["cfg"], w, **args)
+
+    step(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out)
+    for lengths in ([700, 256], [511, 100], [512, 513], [900, 700], [0, 257]):
+        d["kv_len"] = lengths
+        kv_len.copy_(_ints(lengths))
+        d["lse"].copy_(evict_ref.logsums(d["c"], d["Q"], d["pages"], lengths, d["starts"], True, 0, d["scale"]).float())
+        mine = d["old"].clone()
+        step(mine)
+        out.copy_(d["old"])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, mine)
+        _check(d, out)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with the workspace that it takes for itself."""
+    a = _call([500], [800], heads=2, group=4, page=32, keep=0.0, seed=7)
+    b = _call([400, 200], [900, 300], heads=1, group=6, dim=64, page=16, keep=0.0, seed=8)
+    want = [_run(a), _run(b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[d["old"].clone() for _ in range(10)] for d in (a, b)]
+    tables = [(_ints(d["kv_len"]), _ints(d["starts"])) for d in (a, b)]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for d, out, s, (n, q) in zip((a, b), outs, streams, tables):
+            rq.kv_attention_weights(d["Q"], d["lse"], d["c"].bytes, d["pages"], n, d["cfg"], out[i], keep=0.0, q_start=q, stream=s)
+    torch.cuda.synchronize()
+    for d, out, w in zip((a, b), outs, want):
+        _check(d, w)
+        assert all(torch.equal(x, w) for x in out)
